@@ -443,6 +443,109 @@ moe_status moe_expert_compute_ex(const void* recv, const int32_t* counts, int E,
                                  int flags, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * From the residual stream to the dispatch -- what a layer runs before the
+ * routed branch: the norm, the router's projection and the choice of experts
+ * that "SGLang、NCCL 与 MoE EP" takes as given (§2.3.1: hidden rows, topk_idx,
+ * topk_w), and the dispatch of rows that the norm has already put in 8 bits.
+ *
+ * moe_add_rms_norm
+ *   r = x + residual in fp32, residual_out = r in residual's type;
+ *   n = r * rsqrt(mean(r^2) + eps) * weight in fp32; y = bf16(n);
+ *   yq, ys = n by the rule of moe_quantize_fp8 (per row and 128 elements),
+ *   taken from n itself, so it may differ by one code from quantising y.
+ *   x            device, BF16 [T, H]
+ *   residual     device, BF16 (residual_bits = 16) or fp32 (32) [T, H], or NULL
+ *                (no addition; residual_bits is not read)
+ *   weight       device, BF16 (weight_bits = 16) or fp32 (32) [H]
+ *   eps          > 0 and finite
+ *   y            device out, BF16 [T, H], or NULL if yq is given
+ *   yq, ys       device out, e4m3 [T, H] (8-byte aligned) and fp32 [T, H/128],
+ *                or both NULL
+ *   residual_out device out, residual's type [T, H]; may be residual (in
+ *                place); NULL: not kept.  Without a residual it must be NULL
+ *   Rows must be finite, with mean(r^2) inside fp32's range: a NaN or infinity
+ *   in a row gives NaN in that row of y and unspecified codes and scales.
+ *
+ * moe_router_logits
+ *   logits[t, e] = sum_h x[t, h] * w[e, h], products and sums in fp32.
+ *   x device BF16 [T, H]; w device BF16 [E, H]; logits device out fp32 [T, E];
+ *   E <= 1024.  dev_status device int32[2] or NULL: MOE_DEV_TIMEOUT may be ORed
+ *   in; the logits of a tile whose bounded wait ran out are NaN.
+ *
+ * moe_router_topk
+ *   s = softmax(l) over the row (MOE_SCORE_SOFTMAX) or 1 / (1 + exp(-l))
+ *   (MOE_SCORE_SIGMOID), fp32; c = s + bias chooses (without a bias the logits
+ *   choose: the same order); the bias enters no weight.
+ *   With groups > 1 the experts are groups equal runs of ids; a run counts by
+ *   its largest c (group_top = 1) or the sum of its two largest (2; of one, if
+ *   only one can be chosen), and the topk_groups best runs stay, ties to the
+ *   lowest.  The two-sum takes s where there is no bias.
+ *   topk_idx = the K largest c of what stays in descending order, ties to the
+ *   lowest id; topk_w = s there, divided by max(sum, 1e-20) with renormalize,
+ *   times scale.  A logit of -inf or NaN, and a c of -inf, is never chosen;
+ *   where fewer than K can be chosen the last entries are -1 (a padding route)
+ *   with weight 0.
+ *   logits    device, fp32 (logits_bits = 32) or BF16 (16) [T, E]
+ *   bias      device, fp32 [E], or NULL
+ *   groups    divides E, at most MOE_MAX_ROUTER_GROUPS; 1 <= topk_groups <= groups;
+ *             topk_groups * E / groups >= K; group_top <= E / groups if groups > 1
+ *   topk_idx  device out, int32 or int64 (idx_bits) [T, K]; topk_w fp32 [T, K]
+ *
+ * moe_dispatch_fp8 -- moe_dispatch_quant_ex for rows already in e4m3: tq device
+ *   [T, H] and ts device fp32 [T, H/128] (moe_add_rms_norm's yq and ys) are
+ *   copied to every kept row of xq and xs.  Everything else as there; tq and xq
+ *   16-byte aligned.
+ * ------------------------------------------------------------------------- */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_MAX_ROUTER_GROUPS 32
+moe_status moe_add_rms_norm(const void* x, const void* residual, int residual_bits,
+                            const void* weight, int weight_bits, float eps, int T, int H, void* y,
+                            uint8_t* yq, float* ys, void* residual_out, moe_stream_t stream);
+moe_status moe_router_logits(const void* x, const void* w, int T, int H, int E, float* logits,
+                             int32_t* dev_status, moe_stream_t stream);
+moe_status moe_router_topk(const void* logits, int logits_bits, const float* bias, int T, int E,
+                           int K, int score, int groups, int topk_groups, int group_top,
+                           int renormalize, float scale, void* topk_idx, int idx_bits,
+                           float* topk_w, moe_stream_t stream);
+moe_status moe_dispatch_fp8(const uint8_t* tq, const float* ts, const void* topk_idx, int idx_bits,
+                            int T, int H, int K, int E, int R, int64_t rows, uint8_t* xq,
+                            float* xs, int32_t* counts, int32_t* src_map, int32_t* dev_status,
+                            void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_experts_w4 -- the routed branch for a few tokens with 4-bit weights:
+ * dispatch, gated-SiLU expert ("SGLang Expert Compute Backend", §1.1) and
+ * weighted combine ("SGLang、NCCL 与 MoE EP", §1.1) of T <= MOE_W4_MAX_TOKENS
+ * tokens as matrix-vector products; every active expert's weights are read
+ * once, and BF16 activations meet the weights without being quantised.
+ *   weight = (code - 8) * scale, 4-bit codes along the contraction, two a byte
+ *   (the even element in the low four bits), one BF16 scale per output row and
+ *   128 elements of the contraction.
+ *   x          device, BF16 [T, H]
+ *   topk_idx   device, [T, K] int32 or int64 (idx_bits); -1 = no route; ids
+ *              outside [-1, E) are reported as MOE_DEV_BAD_EXPERT_ID and ignored
+ *   topk_w     device, fp32 [T, K]
+ *   w13        device, uint8 [E, 2I, H/2] (gate rows, then up rows);
+ *   w13_scale  device, BF16 [E, 2I, H/128]
+ *   w2         device, uint8 [E, H, I/2];  w2_scale device, BF16 [E, H, I/128]
+ *   y          device out, BF16 [T, H]: the weighted sum in fp32 in a fixed
+ *              order (ascending expert); zeros for a token without a route
+ *   dev_status device, int32 [2]: reset, then MOE_DEV_* bits (no capacity, so
+ *              nothing is dropped)
+ *   workspace  device, moe_experts_w4_workspace_size(T, K, H, I) bytes, 256-byte
+ *              aligned: SiLU(gate) * up of every route, rounded to BF16
+ * More tokens: MOE_ERR_INVALID_ARG (the FP8 layer is the faster form there).
+ * ------------------------------------------------------------------------- */
+#define MOE_W4_MAX_TOKENS 64
+size_t moe_experts_w4_workspace_size(int T, int K, int H, int I);
+moe_status moe_experts_w4(const void* x, const void* topk_idx, int idx_bits, const float* topk_w,
+                          int T, int H, int I, int K, int E, const uint8_t* w13,
+                          const void* w13_scale, const uint8_t* w2, const void* w2_scale, void* y,
+                          int32_t* dev_status, void* workspace, size_t workspace_bytes,
+                          moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * moe_layer_stats -- the counts the pages account a layer by, for one routing:
  * "SGLang、NCCL 与 MoE EP", §5.3 (each token sends one payload per distinct
  * destination rank, D_t of them, §2.3.2; routes to an expert on another logical

@@ -13,7 +13,7 @@ import threading
 from . import build as _build
 
 c_int, c_size_t, c_void_p, c_char_p = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_char_p
-c_int64 = ctypes.c_int64
+c_int64, c_float = ctypes.c_int64, ctypes.c_float
 
 # name -> (restype, argtypes), mirroring include/moe.h
 SIGNATURES = {
@@ -73,6 +73,19 @@ SIGNATURES = {
     "moe_expert_compute_ex": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int64, c_int, c_int,
                                       c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                       c_void_p, c_size_t, c_int, c_void_p]),
+    "moe_add_rms_norm": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_int, c_float, c_int, c_int,
+                                 c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "moe_router_logits": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_void_p,
+                                  c_void_p]),
+    "moe_router_topk": (c_int, [c_void_p, c_int, c_void_p, c_int, c_int, c_int, c_int, c_int,
+                                c_int, c_int, c_int, c_float, c_void_p, c_int, c_void_p, c_void_p]),
+    "moe_dispatch_fp8": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int,
+                                 c_int, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                 c_void_p, c_size_t, c_void_p]),
+    "moe_experts_w4_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int]),
+    "moe_experts_w4": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_int, c_int, c_int, c_int,
+                               c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                               c_void_p, c_size_t, c_void_p]),
     "moe_layer_stats": (c_int, [c_void_p, c_int, c_void_p, c_int, c_int, c_int, c_int, c_int,
                                 c_void_p, c_void_p, c_void_p]),
     "moe_expert_compute_gemm_launches": (c_int, [c_int, c_int, c_int64, c_int, c_int]),
@@ -96,6 +109,8 @@ SIGNATURES = {
 W13_INTERLEAVED = 1
 GEMM_ONE_LAUNCH = 2
 GEMM_TWO_LAUNCHES = 4
+SCORES = {"softmax": 0, "sigmoid": 1}
+W4_MAX_TOKENS = 64
 
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED",
           -3: "MOE_ERR_WORKSPACE", -4: "MOE_ERR_CUDA"}

@@ -21,6 +21,8 @@ __all__ = [
     "moe_gemm_down", "moe_gemm_gateup_down", "moe_dispatch_packed", "moe_expert_compute_packed",
     "moe_combine_packed", "moe_dispatch_source_slots", "moe_expert_compute_source_slots",
     "moe_dispatch_quant_source_slots", "moe_gemm_source_slots",
+    "moe_add_rms_norm", "moe_router_logits", "moe_router_topk", "moe_dispatch_fp8",
+    "moe_experts_w4", "experts_w4_workspace_size", "W4_MAX_TOKENS",
     "moe_layer_stats", "layer_stats_dict", "LAYER_STATS",
     "packed_rows", "MoeLayerBuffers", "HostPipeline", "TwoBatchOverlap", "DEV_BAD_EXPERT_ID",
     "DEV_CAPACITY_DROPPED", "DEV_TIMEOUT",
@@ -30,6 +32,7 @@ MoeError = _lib.MoeError
 DEV_BAD_EXPERT_ID = _lib.DEV_BAD_EXPERT_ID
 DEV_CAPACITY_DROPPED = _lib.DEV_CAPACITY_DROPPED
 DEV_TIMEOUT = _lib.DEV_TIMEOUT
+W4_MAX_TOKENS = _lib.W4_MAX_TOKENS
 
 
 def _p(t):
@@ -365,6 +368,185 @@ def moe_expert_compute_packed(recv, counts, R: int, w13, w13_scale, w2, w2_scale
                                    _s(stream))
     _lib.check("moe_expert_compute_ex", st)
     return out
+
+
+def _check(t, dtypes, shape, device, name):
+    """A tensor argument's type, shape, place and layout.  Returns its address."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name}: expected a CUDA tensor on the inputs' device, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_U8 = (torch.uint8,)
+_HALF_OR_F32 = (torch.bfloat16, torch.float32)
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+_IDS = (torch.int64, torch.int32)
+
+
+def _bits(t):
+    return 8 * t.element_size()
+
+
+def moe_add_rms_norm(x, weight, eps: float = 1e-6, *, residual=None, residual_out=None, y=None,
+                     yq=None, ys=None, bf16: bool = True, quant: bool = False, stream=None):
+    """Residual addition and root-mean-square norm of ``x [T, H]`` bf16, with
+    the normed row in BF16 and, with ``quant`` (or ``yq``/``ys`` given), as e4m3
+    codes and fp32 scales per 128 elements (moe_add_rms_norm).  ``residual``
+    and ``weight`` are bf16 or fp32; ``residual_out`` may be ``residual`` (in
+    place).  ``bf16=False`` leaves the BF16 row out.  Returns ``(y, yq, ys,
+    residual_out)``, None for what there is not."""
+    T, H = x.shape
+    dev = x.device
+    px = _check(x, _BF16, (T, H), dev, "x")
+    pw = _check(weight, _HALF_OR_F32, (H,), dev, "weight")
+    pr = po = None
+    rbits = 0
+    if residual is not None:
+        pr = _check(residual, _HALF_OR_F32, (T, H), dev, "residual")
+        rbits = _bits(residual)
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        po = _check(residual_out, (residual.dtype,), (T, H), dev, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out without residual")
+    if y is None and bf16:
+        y = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    py = None if y is None else _check(y, _BF16, (T, H), dev, "y")
+    pq = ps = None
+    if quant or yq is not None or ys is not None:
+        if yq is None:
+            yq = torch.empty(T, H, dtype=torch.uint8, device=dev)
+        if ys is None:
+            ys = torch.empty(T, H // 128, dtype=torch.float32, device=dev)
+        pq = _check(yq, _E4M3, (T, H), dev, "yq")
+        ps = _check(ys, _F32, (T, H // 128), dev, "ys")
+    st = _lib.load().moe_add_rms_norm(px, pr, rbits, pw, _bits(weight), eps, T, H, py, pq, ps, po,
+                                      _s(stream))
+    _lib.check("moe_add_rms_norm", st)
+    return y, yq, ys, residual_out
+
+
+def moe_router_logits(x, w, *, logits=None, dev_status=None, stream=None):
+    """The router's projection (moe_router_logits): ``x [T, H]`` and ``w [E,
+    H]`` bf16 to fp32 ``logits [T, E]``, fp32 products and sums."""
+    T, H = x.shape
+    E = w.shape[0]
+    dev = x.device
+    if logits is None:
+        logits = torch.empty(T, E, dtype=torch.float32, device=dev)
+    st = _lib.load().moe_router_logits(
+        _check(x, _BF16, (T, H), dev, "x"), _check(w, _BF16, (E, H), dev, "w"), T, H, E,
+        _check(logits, _F32, (T, E), dev, "logits"),
+        None if dev_status is None else _check(dev_status, _I32, (2,), dev, "dev_status"),
+        _s(stream))
+    _lib.check("moe_router_logits", st)
+    return logits
+
+
+def moe_router_topk(logits, K: int, *, score: str = "softmax", bias=None, groups: int = 1,
+                    topk_groups: int | None = None, group_top: int = 1, renormalize: bool = True,
+                    scale: float = 1.0, idx_dtype=torch.int64, topk_idx=None, topk_w=None,
+                    stream=None):
+    """The choice of experts from ``logits [T, E]`` fp32 or bf16
+    (moe_router_topk): scores ``"softmax"`` or ``"sigmoid"``, a ``bias [E]``
+    fp32 that enters the choice only, ``topk_groups`` of ``groups`` equal runs
+    of experts by their best one or two (``group_top``), weights renormalised
+    and scaled.  Returns ``(topk_idx [T, K], topk_w [T, K] fp32)``; -1 and 0
+    where nothing is left to choose."""
+    T, E = logits.shape
+    dev = logits.device
+    if score not in _lib.SCORES:
+        raise ValueError(f"score: 'softmax' or 'sigmoid', not {score!r}")
+    if topk_idx is None:
+        topk_idx = torch.empty(T, K, dtype=idx_dtype, device=dev)
+    if topk_w is None:
+        topk_w = torch.empty(T, K, dtype=torch.float32, device=dev)
+    st = _lib.load().moe_router_topk(
+        _check(logits, _HALF_OR_F32, (T, E), dev, "logits"), _bits(logits),
+        None if bias is None else _check(bias, _F32, (E,), dev, "bias"), T, E, K,
+        _lib.SCORES[score], groups, groups if topk_groups is None else topk_groups, group_top,
+        1 if renormalize else 0, scale, _check(topk_idx, _IDS, (T, K), dev, "topk_idx"),
+        _bits(topk_idx), _check(topk_w, _F32, (T, K), dev, "topk_w"), _s(stream))
+    _lib.check("moe_router_topk", st)
+    return topk_idx, topk_w
+
+
+def moe_dispatch_fp8(tq, ts, topk_idx, E: int, R: int, *, xq=None, xs=None, counts=None,
+                     src_map=None, dev_status=None, workspace=None, stream=None, rows=0):
+    """``moe_dispatch_quant`` for rows already in e4m3 (moe_dispatch_fp8): codes
+    ``tq [T, H]`` and scales ``ts [T, H/128]``, as ``moe_add_rms_norm`` gives
+    them, are copied to every kept row.  Returns ``(xq, xs, counts, src_map,
+    dev_status)``."""
+    lib = _lib.load()
+    T, H = tq.shape
+    K = topk_idx.shape[1]
+    dev = tq.device
+    lead = (rows,) if rows else (E, R)
+    if xq is None:
+        xq = torch.empty(*lead, H, dtype=torch.uint8, device=dev)
+    if xs is None:
+        xs = torch.empty(*lead, H // 128, dtype=torch.float32, device=dev)
+    if counts is None:
+        counts = torch.empty(E, dtype=torch.int32, device=dev)
+    if src_map is None:
+        src_map = torch.empty(T, K, dtype=torch.int32, device=dev)
+    if dev_status is None:
+        dev_status = torch.empty(2, dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = _workspace(lib.moe_dispatch_workspace_size(T, K, E), dev)
+    st = lib.moe_dispatch_fp8(
+        _check(tq, _E4M3, (T, H), dev, "tq"), _check(ts, _F32, (T, H // 128), dev, "ts"),
+        _check(topk_idx, _IDS, (T, K), dev, "topk_idx"), _bits(topk_idx), T, H, K, E, R, rows,
+        _check(xq, _E4M3, (*lead, H), dev, "xq"), _check(xs, _F32, (*lead, H // 128), dev, "xs"),
+        _check(counts, _I32, (E,), dev, "counts"), _check(src_map, _I32, (T, K), dev, "src_map"),
+        _check(dev_status, _I32, (2,), dev, "dev_status"), _p(workspace), workspace.numel(),
+        _s(stream))
+    _lib.check("moe_dispatch_fp8", st)
+    return xq, xs, counts, src_map, dev_status
+
+
+def experts_w4_workspace_size(T: int, K: int, H: int, I: int) -> int:
+    return int(_lib.load().moe_experts_w4_workspace_size(T, K, H, I))
+
+
+def moe_experts_w4(x, topk_idx, topk_w, w13, w13_scale, w2, w2_scale, *, y=None, dev_status=None,
+                   workspace=None, stream=None):
+    """The routed branch for up to ``W4_MAX_TOKENS`` tokens with 4-bit weights
+    (moe_experts_w4): ``w13 [E, 2I, H/2]`` and ``w2 [E, H, I/2]`` uint8, two
+    codes a byte, with bf16 scales ``[E, 2I, H/128]`` and ``[E, H, I/128]``; a
+    weight is (code - 8) * scale.  Returns ``y [T, H]`` bf16."""
+    lib = _lib.load()
+    T, H = x.shape
+    K = topk_idx.shape[1]
+    E, n13, _ = w13.shape
+    I = n13 // 2
+    dev = x.device
+    if y is None:
+        y = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    if dev_status is None:
+        dev_status = torch.empty(2, dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = _workspace(lib.moe_experts_w4_workspace_size(T, K, H, I), dev)
+    st = lib.moe_experts_w4(
+        _check(x, _BF16, (T, H), dev, "x"), _check(topk_idx, _IDS, (T, K), dev, "topk_idx"),
+        _bits(topk_idx), _check(topk_w, _F32, (T, K), dev, "topk_w"), T, H, I, K, E,
+        _check(w13, _U8, (E, 2 * I, H // 2), dev, "w13"),
+        _check(w13_scale, _BF16, (E, 2 * I, H // 128), dev, "w13_scale"),
+        _check(w2, _U8, (E, H, I // 2), dev, "w2"),
+        _check(w2_scale, _BF16, (E, H, I // 128), dev, "w2_scale"),
+        _check(y, _BF16, (T, H), dev, "y"), _check(dev_status, _I32, (2,), dev, "dev_status"),
+        _p(workspace), workspace.numel(), _s(stream))
+    _lib.check("moe_experts_w4", st)
+    return y
 
 
 LAYER_STATS = ("valid_routes", "kept_routes", "messages", "cross_rank_routes", "tile_blocks",

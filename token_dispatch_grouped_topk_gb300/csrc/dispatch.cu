@@ -444,6 +444,87 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
   }
 }
 
+// Dispatch of rows that are already in e4m3 with one fp32 scale per 128 (the
+// norm's 8-bit output): slots, counts and source map of route_scatter_kernel;
+// each token's codes and scales are read once and written to every kept row.
+// A block takes whole 128-groups of its tokens' rows (eight 16-byte vectors
+// of codes and one scale each).
+template <typename IdT, bool kSingle>
+__global__ void __launch_bounds__(kDispatchWarps * 32)
+    route_scatter_codes_kernel(const uint4* __restrict__ tq, const float* __restrict__ ts,
+                               const IdT* __restrict__ topk_idx, int T, int H, int K, int E,
+                               RowLayout rl, int nblocks, const int32_t* __restrict__ base,
+                               int32_t* __restrict__ counts, uint4* __restrict__ xq,
+                               float* __restrict__ xs, int32_t* __restrict__ src_map,
+                               int32_t* dev_status, int groups_per_slice) {
+  extern __shared__ int smem[];
+  int* s_cnt = smem;                           // [kDispatchWarps][E]
+  int* s_dest = smem + kDispatchWarps * E;     // [kDispatchWarps][32]
+  int* s_rows = s_dest + kDispatchWarps * 32;  // [E + 1] packed row bases
+  int* s_prev = s_rows + E + 1;                // single pass: [E]
+  int* s_tot = s_prev + E;                     //              [E]
+  for (int i = threadIdx.x; i < kDispatchWarps * E; i += blockDim.x) s_cnt[i] = 0;
+  if (kSingle)
+    single_pass_bases(topk_idx, T, K, E, rl, s_prev, s_tot, s_rows, counts, dev_status);
+  else if (rl.packed)
+    expert_prefix(counts, E, rl.R, 1, 1, s_rows, nullptr);
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gw = blockIdx.x * kDispatchWarps + warp;
+  const RouteLane r = load_route(topk_idx, T, K, E, gw, lane, nullptr);
+  const unsigned peers = __match_any_sync(0xffffffffu, r.e);
+  const int lane_rank = __popc(peers & ((1u << lane) - 1u));
+  if (r.e >= 0 && lane == __ffs(peers) - 1) s_cnt[warp * E + r.e] = __popc(peers);
+  __syncthreads();
+  int q = -1;
+  if (r.e >= 0) {
+    int sl = (kSingle ? s_prev[r.e] : base[static_cast<size_t>(r.e) * nblocks + blockIdx.x]) +
+             lane_rank;
+    for (int w = 0; w < warp; ++w) sl += s_cnt[w * E + r.e];
+    if (sl < rl.R) q = (rl.packed ? s_rows[r.e] : r.e * rl.R) + sl;
+  }
+  if (blockIdx.y == 0 && r.active) src_map[static_cast<int64_t>(r.t) * K + r.k] = q;
+  s_dest[warp * 32 + lane] = q;
+  __syncwarp();
+
+  const int tpw = 32 / K;
+  const int G = H / kGroup, nvec = H / 16;
+  const int g0 = blockIdx.y * groups_per_slice;
+  const int g1 = min(G, g0 + groups_per_slice);
+  const int v0 = g0 * 8, v1 = g1 * 8;
+  const int* wdest = s_dest + warp * 32;
+  for (int tt = 0; tt < tpw; ++tt) {
+    const int t = gw * tpw + tt;
+    if (t >= T) break;
+    const int* dq = wdest + tt * K;
+    bool any = false;
+    for (int k = 0; k < K; ++k) any |= dq[k] >= 0;
+    if (!any) continue;
+    const uint4* src = tq + static_cast<size_t>(t) * nvec;
+    for (int v = v0 + lane; v < v1; v += 32 * 8) {
+      uint4 c[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (v + 32 * u < v1) c[u] = ld_stream(src + v + 32 * u);
+      for (int k = 0; k < K; ++k) {
+        const int qq = dq[k];
+        if (qq < 0) continue;
+        uint4* dst = xq + static_cast<size_t>(qq) * nvec;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (v + 32 * u < v1) dst[v + 32 * u] = c[u];
+      }
+    }
+    for (int g = g0 + lane; g < g1; g += 32) {
+      const float sc = __ldg(ts + static_cast<size_t>(t) * G + g);
+      for (int k = 0; k < K; ++k) {
+        const int qq = dq[k];
+        if (qq >= 0) xs[static_cast<size_t>(qq) * G + g] = sc;
+      }
+    }
+  }
+}
+
 // Per-source fixed-slot dispatch ("DeepEP 架构与实现笔记", §9.5): expert e's
 // R = W * mt rows are W ranges of mt slots, one per source rank, and route
 // (t, k) of source rank r goes to slot r * mt + p, p its position among r's
@@ -820,6 +901,53 @@ cudaError_t launch_dispatch_quant(const void* x, const void* topk_idx, int idx_b
                                counts, src_map, dev_status, hist, sm_count, s);
   return dispatch_quant_impl(x, static_cast<const int64_t*>(topk_idx), T, H, K, E, rl, xq, xs,
                              counts, src_map, dev_status, hist, sm_count, s);
+}
+
+namespace {
+template <typename IdT>
+cudaError_t dispatch_fp8_impl(const uint8_t* tq, const float* ts, const IdT* topk_idx, int T,
+                              int H, int K, int E, RowLayout rl, uint8_t* xq, float* xs,
+                              int32_t* counts, int32_t* src_map, int32_t* dev_status,
+                              int32_t* hist, int sm_count, cudaStream_t s) {
+  const int nblocks = dispatch_blocks(T, K);
+  const bool one = single_pass(T, K);
+  cudaError_t err;
+  if (!one) {
+    err = cudaMemsetAsync(dev_status, 0, 2 * sizeof(int32_t), s);
+    if (err != cudaSuccess) return err;
+    if (nblocks > 0) {
+      route_hist_kernel<IdT><<<nblocks, kDispatchWarps * 32, E * sizeof(int), s>>>(
+          topk_idx, T, K, E, nblocks, hist, dev_status);
+      if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    }
+    route_scan_kernel<<<E, kScanThreads, 0, s>>>(hist, nblocks, rl.R, counts, dev_status);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    if (nblocks == 0) return cudaSuccess;
+  }
+  // slices of four or more whole 128-groups (one 16-byte vector per lane)
+  const int G = H / kGroup;
+  int hsplit = row_slices(nblocks, G, 4, sm_count);
+  const int gps = (G + hsplit - 1) / hsplit;
+  hsplit = (G + gps - 1) / gps;
+  const size_t smem = (kDispatchWarps * E + kDispatchWarps * 32 + 3 * E + 1) * sizeof(int);
+  auto kernel = one ? route_scatter_codes_kernel<IdT, true> : route_scatter_codes_kernel<IdT, false>;
+  if ((err = allow_smem(kernel, smem)) != cudaSuccess) return err;
+  kernel<<<dim3(nblocks, hsplit), kDispatchWarps * 32, smem, s>>>(
+      reinterpret_cast<const uint4*>(tq), ts, topk_idx, T, H, K, E, rl, nblocks, hist, counts,
+      reinterpret_cast<uint4*>(xq), xs, src_map, dev_status, gps);
+  return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_dispatch_fp8(const uint8_t* tq, const float* ts, const void* topk_idx,
+                                int idx_bits, int T, int H, int K, int E, RowLayout rl,
+                                uint8_t* xq, float* xs, int32_t* counts, int32_t* src_map,
+                                int32_t* dev_status, int32_t* hist, int sm_count, cudaStream_t s) {
+  if (idx_bits == 32)
+    return dispatch_fp8_impl(tq, ts, static_cast<const int32_t*>(topk_idx), T, H, K, E, rl, xq, xs,
+                             counts, src_map, dev_status, hist, sm_count, s);
+  return dispatch_fp8_impl(tq, ts, static_cast<const int64_t*>(topk_idx), T, H, K, E, rl, xq, xs,
+                           counts, src_map, dev_status, hist, sm_count, s);
 }
 
 }  // namespace moe

@@ -56,12 +56,11 @@
 //    before the current tile's tail whenever the tile is already published.
 // Every wait is bounded; on expiry the kernel raises MOE_DEV_TIMEOUT in the
 // status word, drains its own copies and MMAs, frees TMEM and returns.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tensormap.h"
 
 namespace moe {
 namespace {
@@ -739,38 +738,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0 && ctl->abort) atomicOr(args.dev_status, kDevTimeout);
 }
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = []() -> EncodeTiledFn {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
-  return fn;
-}
-
-// 2D map over a row-major byte matrix [rows, cols] with boxes of 128 bytes x
-// box_rows and the 128-byte swizzle the MMA descriptors expect.
+// 2D map over a row-major byte matrix [rows, cols].
 cudaError_t make_map_u8(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
                         uint32_t box_rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (enc == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols};
-  const cuuint32_t box[2] = {128, box_rows};
-  const cuuint32_t es[2] = {1, 1};
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides,
-                         box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return make_map_rows128(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, cols, rows, box_rows);
 }
 
 // Activation maps with 128-, 64- and 32-row boxes.

@@ -151,6 +151,34 @@ cudaError_t launch_ep_result(const int32_t* route_msg, const int32_t* route_pos,
                              const int32_t* offsets, const int32_t* flag, int64_t n_ret, int T,
                              int K, int32_t* result_map, cudaStream_t s);
 
+// ----- the layer's front end: norm, router, choice of experts
+// residual null: no addition; y, yq/ys, residual_out may each be null.
+cudaError_t launch_add_rms_norm(const void* x, const void* residual, int residual_bits,
+                                const void* weight, int weight_bits, float eps, int T, int H,
+                                void* y, uint8_t* yq, float* ys, void* residual_out, int sm_count,
+                                cudaStream_t s);
+cudaError_t launch_router_logits(const void* x, const void* w, int T, int H, int E, float* logits,
+                                 int32_t* dev_status, int sm_count, cudaStream_t s);
+constexpr int kMaxRouterGroups = 32;
+cudaError_t launch_router_topk(const void* logits, int logits_bits, const float* bias, int T,
+                               int E, int K, int sigmoid, int groups, int topk_groups,
+                               int group_top, int renorm, float scale, void* topk_idx,
+                               int idx_bits, float* topk_w, int sm_count, cudaStream_t s);
+
+// ----- dispatch of rows already in e4m3 (xq [T, H], xs [T, H/128])
+cudaError_t launch_dispatch_fp8(const uint8_t* tq, const float* ts, const void* topk_idx,
+                                int idx_bits, int T, int H, int K, int E, RowLayout rl,
+                                uint8_t* xq, float* xs, int32_t* counts, int32_t* src_map,
+                                int32_t* dev_status, int32_t* hist, int sm_count, cudaStream_t s);
+
+// ----- 4-bit experts for a few tokens: z is scratch, BF16 [T * K, I]
+constexpr int kW4MaxTokens = 64;
+cudaError_t launch_experts_w4(const void* x, const void* topk_idx, int idx_bits,
+                              const float* topk_w, int T, int H, int I, int K, int E,
+                              const uint8_t* w13, const void* w13_scale, const uint8_t* w2,
+                              const void* w2_scale, void* z, void* y, int32_t* dev_status,
+                              int sm_count, cudaStream_t s);
+
 // ----- layer statistics of one routing (kLayerStats 64-bit counters):
 // [0] valid routes, [1] kept routes, [2] messages (sum over tokens of the
 // distinct destination ranks), [3] cross-rank routes, [4] 128-row blocks of

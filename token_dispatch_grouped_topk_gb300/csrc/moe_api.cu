@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
@@ -19,6 +20,8 @@ std::mutex g_info_mu;
 DeviceInfo g_info[kMaxDevices];
 bool g_info_ok[kMaxDevices];
 
+static_assert(kW4MaxTokens == MOE_W4_MAX_TOKENS && kMaxRouterGroups == MOE_MAX_ROUTER_GROUPS,
+              "the header's limits are the kernels'");
 constexpr size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 }  // namespace
@@ -380,6 +383,120 @@ moe_status moe_dispatch_quant(const void* x, const int64_t* topk_idx, const floa
                               size_t workspace_bytes, moe_stream_t stream) {
   return moe_dispatch_quant_ex(x, topk_idx, 64, topk_w, T, H, K, E, R, 0, xq, xs, counts, src_map,
                                dev_status, workspace, workspace_bytes, stream);
+}
+
+moe_status moe_dispatch_fp8(const uint8_t* tq, const float* ts, const void* topk_idx, int idx_bits,
+                            int T, int H, int K, int E, int R, int64_t rows, uint8_t* xq,
+                            float* xs, int32_t* counts, int32_t* src_map, int32_t* dev_status,
+                            void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  if (T < 0 || !valid_hidden(H) || !valid_experts(E, R) || K < 1 || K > 32 || K > E)
+    return MOE_ERR_INVALID_ARG;
+  if (idx_bits != 32 && idx_bits != 64) return MOE_ERR_INVALID_ARG;
+  if (counts == nullptr || dev_status == nullptr) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (tq == nullptr || ts == nullptr || topk_idx == nullptr || xq == nullptr ||
+                xs == nullptr || src_map == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!aligned16(tq) || !aligned16(xq))) return MOE_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(T) * K > (int64_t{1} << 31) - 1) return MOE_ERR_INVALID_ARG;
+  RowLayout rl = padded_rows(E, R);
+  if (rows != 0) {
+    const int64_t need_rows =
+        std::min<int64_t>(static_cast<int64_t>(T) * K, static_cast<int64_t>(E) * R);
+    if (!valid_rows(rows) || rows < need_rows) return MOE_ERR_INVALID_ARG;
+    rl = RowLayout{R, 1, rows};
+  }
+  const size_t need = moe_dispatch_workspace_size(T, K, E);
+  if (workspace == nullptr || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  const DeviceInfo* dev = nullptr;
+  if (moe_status st = check_device(&dev); st != MOE_OK) return st;
+  return from_cuda(launch_dispatch_fp8(tq, ts, topk_idx, idx_bits, T, H, K, E, rl, xq, xs, counts,
+                                       src_map, dev_status, static_cast<int32_t*>(workspace),
+                                       dev->sm_count, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_add_rms_norm(const void* x, const void* residual, int residual_bits,
+                            const void* weight, int weight_bits, float eps, int T, int H, void* y,
+                            uint8_t* yq, float* ys, void* residual_out, moe_stream_t stream) {
+  if (T < 0 || !valid_hidden(H) || !(eps > 0.f) || std::isinf(eps)) return MOE_ERR_INVALID_ARG;
+  if (weight_bits != 16 && weight_bits != 32) return MOE_ERR_INVALID_ARG;
+  if (residual != nullptr && residual_bits != 16 && residual_bits != 32) return MOE_ERR_INVALID_ARG;
+  if (residual == nullptr && residual_out != nullptr) return MOE_ERR_INVALID_ARG;
+  if ((yq == nullptr) != (ys == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (x == nullptr || weight == nullptr || (y == nullptr && yq == nullptr)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(y) ||
+      (reinterpret_cast<uintptr_t>(yq) & 7u) != 0 || !aligned16(residual_out))
+    return MOE_ERR_INVALID_ARG;
+  const DeviceInfo* dev = nullptr;
+  if (moe_status st = check_device(&dev); st != MOE_OK) return st;
+  return from_cuda(launch_add_rms_norm(x, residual, residual_bits, weight, weight_bits, eps, T, H,
+                                       y, yq, ys, residual_out, dev->sm_count,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_router_logits(const void* x, const void* w, int T, int H, int E, float* logits,
+                             int32_t* dev_status, moe_stream_t stream) {
+  if (T < 0 || !valid_hidden(H) || E < 1 || E > 1024) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (x == nullptr || w == nullptr || logits == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w)) return MOE_ERR_INVALID_ARG;
+  const DeviceInfo* dev = nullptr;
+  if (moe_status st = check_device(&dev); st != MOE_OK) return st;
+  return from_cuda(launch_router_logits(x, w, T, H, E, logits, dev_status, dev->sm_count,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_router_topk(const void* logits, int logits_bits, const float* bias, int T, int E,
+                           int K, int score, int groups, int topk_groups, int group_top,
+                           int renormalize, float scale, void* topk_idx, int idx_bits,
+                           float* topk_w, moe_stream_t stream) {
+  if (T < 0 || E < 1 || E > 1024 || K < 1 || K > 32 || K > E) return MOE_ERR_INVALID_ARG;
+  if (logits_bits != 16 && logits_bits != 32) return MOE_ERR_INVALID_ARG;
+  if (idx_bits != 32 && idx_bits != 64) return MOE_ERR_INVALID_ARG;
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (groups < 1 || groups > kMaxRouterGroups || E % groups != 0 || topk_groups < 1 ||
+      topk_groups > groups || static_cast<int64_t>(topk_groups) * (E / groups) < K)
+    return MOE_ERR_INVALID_ARG;
+  if ((group_top != 1 && group_top != 2) || (groups > 1 && group_top > E / groups))
+    return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (logits == nullptr || topk_idx == nullptr || topk_w == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  const DeviceInfo* dev = nullptr;
+  if (moe_status st = check_device(&dev); st != MOE_OK) return st;
+  return from_cuda(launch_router_topk(logits, logits_bits, bias, T, E, K,
+                                      score == MOE_SCORE_SIGMOID ? 1 : 0, groups, topk_groups,
+                                      group_top, renormalize ? 1 : 0, scale, topk_idx, idx_bits,
+                                      topk_w, dev->sm_count,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_experts_w4_workspace_size(int T, int K, int H, int I) {
+  if (T < 0 || T > kW4MaxTokens || K < 1 || K > 32 || !valid_hidden(H) || !valid_hidden(I)) return 0;
+  return align_up(std::max<size_t>(static_cast<size_t>(T) * K * I * 2, 1), 256);
+}
+
+moe_status moe_experts_w4(const void* x, const void* topk_idx, int idx_bits, const float* topk_w,
+                          int T, int H, int I, int K, int E, const uint8_t* w13,
+                          const void* w13_scale, const uint8_t* w2, const void* w2_scale, void* y,
+                          int32_t* dev_status, void* workspace, size_t workspace_bytes,
+                          moe_stream_t stream) {
+  if (T < 0 || T > MOE_W4_MAX_TOKENS || !valid_hidden(H) || !valid_hidden(I) || E < 1 ||
+      E > 1024 || K < 1 || K > 32 || K > E)
+    return MOE_ERR_INVALID_ARG;
+  if (idx_bits != 32 && idx_bits != 64) return MOE_ERR_INVALID_ARG;
+  if (w13 == nullptr || w13_scale == nullptr || w2 == nullptr || w2_scale == nullptr ||
+      dev_status == nullptr ||
+      (T > 0 && (x == nullptr || topk_idx == nullptr || topk_w == nullptr || y == nullptr)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w13) || !aligned16(w2)) return MOE_ERR_INVALID_ARG;
+  if (workspace == nullptr || workspace_bytes < moe_experts_w4_workspace_size(T, K, H, I) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return MOE_ERR_WORKSPACE;
+  const DeviceInfo* dev = nullptr;
+  if (moe_status st = check_device(&dev); st != MOE_OK) return st;
+  return from_cuda(launch_experts_w4(x, topk_idx, idx_bits, topk_w, T, H, I, K, E, w13, w13_scale,
+                                     w2, w2_scale, workspace, y, dev_status, dev->sm_count,
+                                     reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_expert_compute_workspace_size(int E, int R, int H, int I) {
