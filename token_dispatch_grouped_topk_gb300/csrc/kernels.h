@@ -171,13 +171,15 @@ cudaError_t launch_dispatch_fp8(const uint8_t* tq, const float* ts, const void* 
                                 uint8_t* xq, float* xs, int32_t* counts, int32_t* src_map,
                                 int32_t* dev_status, int32_t* hist, int sm_count, cudaStream_t s);
 
-// ----- 4-bit experts for a few tokens: z is scratch, BF16 [T * K, I]
+// ----- 4-bit experts for a few tokens
 constexpr int kW4MaxTokens = 64;
+constexpr int kW4MaxBlocks = 304;   // the down launch's grid: two blocks per SM
+size_t experts_w4_workspace(int T, int K, int H, int I);
 cudaError_t launch_experts_w4(const void* x, const void* topk_idx, int idx_bits,
                               const float* topk_w, int T, int H, int I, int K, int E,
                               const uint8_t* w13, const void* w13_scale, const uint8_t* w2,
-                              const void* w2_scale, void* z, void* y, int32_t* dev_status,
-                              int sm_count, cudaStream_t s);
+                              const void* w2_scale, void* workspace, void* y,
+                              int32_t* dev_status, int sm_count, cudaStream_t s);
 
 // ----- layer statistics of one routing (kLayerStats 64-bit counters):
 // [0] valid routes, [1] kept routes, [2] messages (sum over tokens of the

@@ -472,7 +472,7 @@ moe_status moe_router_topk(const void* logits, int logits_bits, const float* bia
 
 size_t moe_experts_w4_workspace_size(int T, int K, int H, int I) {
   if (T < 0 || T > kW4MaxTokens || K < 1 || K > 32 || !valid_hidden(H) || !valid_hidden(I)) return 0;
-  return align_up(std::max<size_t>(static_cast<size_t>(T) * K * I * 2, 1), 256);
+  return experts_w4_workspace(T, K, H, I);
 }
 
 moe_status moe_experts_w4(const void* x, const void* topk_idx, int idx_bits, const float* topk_w,
@@ -488,7 +488,9 @@ moe_status moe_experts_w4(const void* x, const void* topk_idx, int idx_bits, con
       dev_status == nullptr ||
       (T > 0 && (x == nullptr || topk_idx == nullptr || topk_w == nullptr || y == nullptr)))
     return MOE_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(w13) || !aligned16(w2)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w13) || !aligned16(w2) || !aligned16(w13_scale) ||
+      !aligned16(w2_scale))
+    return MOE_ERR_INVALID_ARG;
   if (workspace == nullptr || workspace_bytes < moe_experts_w4_workspace_size(T, K, H, I) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return MOE_ERR_WORKSPACE;
