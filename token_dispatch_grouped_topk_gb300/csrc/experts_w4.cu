@@ -32,11 +32,16 @@
 // order: lane 4 * r + q holds codes [32q, 32q + 32) of a 128-group; word i of
 // its four words gives the pairs (8i + j, 8i + j + 4), j = 0..3.
 //
-// Every warp streams its own weights: TMA boxes of 16 rows x 128 bytes (two
-// groups) into a ring of its own, a few boxes ahead and over the ends of its
-// items, so memory never waits for a reduction; a tile's scales, which are
-// contiguous, come as one copy with the tile's first box.  The rings have one
-// user and need no second barrier per slot.
+// Streaming.  A block's unit is 128 weight rows (of gate and up each) x two
+// groups: a producer thread brings the codes with TMA (128-byte swizzled
+// boxes) and the operand rows of the pass's tokens with bulk copies through a
+// ring of stages; each of eight warps takes 16 of the rows.  The launch's units
+// in order (tile by tile) are cut into equal runs, one per block, so every SM
+// reads the same number of bytes whatever the sizes and the routes are.  A
+// tile that one block has whole is finished by it; of a tile that several
+// blocks share each warp leaves its sums in the workspace, and the last to
+// finish adds them in block order.  The order of every sum is fixed by the
+// routes alone.
 //
 // Four launches, each started while the one before still runs (programmatic
 // dependent launch): the plan (active experts and their routes) and x as
@@ -55,16 +60,18 @@
 namespace moe {
 namespace {
 
-constexpr int kW4Warps = 8;
-constexpr int kW4Threads = kW4Warps * 32;
+constexpr int kW4Warps = 8;       // that compute; one more brings the data
+constexpr int kW4Threads = (kW4Warps + 1) * 32;
+constexpr int kPrepThreads = 256;
 constexpr int kCols = 8;          // token columns of one pass
-constexpr int kRows = 16;         // weight rows of one tile
-constexpr int kBoxBytes = kRows * 128;  // two 128-groups of a tile's codes
+constexpr int kRows = 16;         // weight rows of one warp
+constexpr int kTileRows = kW4Warps * kRows;
+constexpr int kBoxBytes = kTileRows * 128;  // two 128-groups of a tile's codes
+constexpr int kOpBytes = 288;     // operand record of a group: 256 bytes, its sum, padding
+constexpr int kColBytes = 2 * kOpBytes;     // one column of a unit (64 mod 128: no bank conflicts)
+constexpr int kMaxStages = 5;
 constexpr int kMaxRoutes = kW4MaxTokens * 32;
 constexpr int kMaxPasses = 1024 + kMaxRoutes / kCols;
-constexpr int kMaxTiles = 16384 / kRows;
-constexpr int kGuDepth = 2;       // ring slots per warp: a gate and an up box each
-constexpr int kDnDepth = 4;       // one box each
 
 // Passes in ascending expert, up to eight routes of one active expert each;
 // routes in ascending route id.  A token's second route to one expert is
@@ -96,18 +103,18 @@ struct W4Args {
   uint16_t* y;          // BF16 [T, H]
   int32_t* dev_status;
   W4Plan* plan;
-  uint8_t* xs;          // [T][2H] x as operand rows, see store_operand
+  uint8_t* xs;          // [T] operand rows of x, see store_operand
   float* xscale;        // [T] 2^-k
-  float* xsum;          // [T][H / 128] 8 * 2^-24 times the groups' sums of x * 2^k
   float* z;             // [T * K, I] by route
   uint32_t* zmax;       // [T * K] bits of the route's largest |z|
-  uint8_t* zs;          // [T * K][2I] z as operand rows
+  uint8_t* zs;          // [T * K] operand rows of z
   float* zscale;        // [T * K]
-  float* zsum;          // [T * K][I / 128]
-  int* done;            // [H / 16] blocks done with a tile of rows that several share
-  float* part;          // [2 * blocks][T][16] their sums
+  int* done;            // [2][blocks][warps]: warps done with the tile that several blocks
+                        // share and the block begins, of gate/up and of down
+  float* part;          // their sums: [2 * blocks][warps][256 or T * 16]
   int T, H, I, K, E;
   int max_passes;       // bound of the plan's passes
+  int stages;
 };
 
 __device__ __forceinline__ void grid_dependency_wait() {
@@ -126,11 +133,16 @@ __device__ __forceinline__ float operand_scale(uint32_t max_bits, float* back) {
   *back = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
   return __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
 }
+// Bytes of an operand row: an even number of group records, so a unit's two
+// are always there.
+__host__ __device__ __forceinline__ int operand_row_bytes(int n) {
+  return (n / kGroup + 1) / 2 * kColBytes;
+}
 // Eight elements [8i, 8i + 8) of a row, times `mult`, as the operand pairs
-// (j, j + 4), the odd j times 2^-4: 16 bytes, in the row's order.  Half a warp
-// stores a group together, which sums[i / 16] is of.
-__device__ __forceinline__ void store_operand(uint8_t* row, float* sums, int i, const float* v,
-                                              float mult) {
+// (j, j + 4), the odd j times 2^-4.  A group's record: word by word, the 16
+// bytes of the four lanes q; then 8 * 2^-24 times the group's sum.  Half a warp
+// stores a group together.
+__device__ __forceinline__ void store_operand(uint8_t* row, int i, const float* v, float mult) {
   float sum = 0.f;
   uint32_t out[4];
 #pragma unroll
@@ -147,11 +159,19 @@ __device__ __forceinline__ void store_operand(uint8_t* row, float* sums, int i, 
     sum += (f.x + f.y) * (j & 1 ? 16.f : 1.f);
     out[j] = *reinterpret_cast<const uint32_t*>(&p);
   }
-  *reinterpret_cast<uint4*>(row + i * 16) = make_uint4(out[0], out[1], out[2], out[3]);
+  uint8_t* rec = row + (i / 16) * kOpBytes;
+  const int q = i % 16 / 4, w = i % 4;
+  *reinterpret_cast<uint4*>(rec + w * 64 + q * 16) = make_uint4(out[0], out[1], out[2], out[3]);
   const unsigned half = 0xffffu << (threadIdx.x & 16);
 #pragma unroll
   for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor_sync(half, sum, o);
-  if (i % 16 == 0) sums[i / 16] = sum * 0x1p-21f;   // 8 * 2^-24
+  if (i % 16 == 0) *reinterpret_cast<float*>(rec + 256) = sum * 0x1p-21f;
+}
+// The record past an odd number of groups: zeros.
+__device__ __forceinline__ void store_operand_end(uint8_t* row, int n) {
+  const int G = n / kGroup;
+  if ((G & 1) && threadIdx.x < kOpBytes / 16)
+    *reinterpret_cast<uint4*>(row + G * kOpBytes + threadIdx.x * 16) = make_uint4(0, 0, 0, 0);
 }
 
 // ------------------------------------------------------------------ prepare
@@ -160,7 +180,8 @@ __device__ void make_plan(const W4Args& a) {
   __shared__ int pos[1024 + 1];    // counts, then next free place
   __shared__ int off[1024 + 1];    // first route of each expert
   __shared__ int first[1024 + 1];  // first pass of each expert
-  __shared__ int16_t ids[kMaxRoutes];
+  __shared__ int16_t ids[kMaxRoutes], kept[kMaxRoutes];
+  __shared__ float weight[kMaxRoutes];
   __shared__ int s_bad;
   const IdT* topk_idx = static_cast<const IdT*>(a.topk_idx);
   const int n = a.T * a.K, E = a.E;
@@ -169,20 +190,19 @@ __device__ void make_plan(const W4Args& a) {
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     const int64_t id = static_cast<int64_t>(topk_idx[i]);
+    weight[i] = a.topk_w[i];
     const bool in = id >= 0 && id < E;
     ids[i] = in ? static_cast<int16_t>(id) : int16_t{-1};
     if (!in && id != -1) s_bad = 1;
   }
   __syncthreads();
   // a route's expert, or -1 for none and for a repeat
-  auto kept = [&](int i) -> int {
-    const int e = ids[i];
-    for (int j = i - i % a.K; j < i; ++j)
-      if (ids[j] == e) return -1;
-    return e;
-  };
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int e = kept(i);
+    int e = ids[i];
+    const int k0 = i - i % a.K;
+    for (int j = k0; j < i; ++j)
+      if (ids[j] == e) e = -1;
+    kept[i] = static_cast<int16_t>(e);
     if (e >= 0) atomicAdd(&pos[e], 1);
   }
   __syncthreads();
@@ -206,15 +226,15 @@ __device__ void make_plan(const W4Args& a) {
   const int lane = threadIdx.x;
   for (int i0 = 0; i0 < n; i0 += 32) {
     const int i = i0 + lane;
-    const int e = i < n ? kept(i) : -1;
+    const int e = i < n ? kept[i] : -1;
     const unsigned peers = __match_any_sync(0xffffffffu, e);
     if (e >= 0) {
       const int at = pos[e] + __popc(peers & ((1u << lane) - 1u));
-      a.plan->route[at] = static_cast<uint16_t>(i);
-      float w = a.topk_w[i];
+      float w = weight[i];
       const int k1 = i - i % a.K + a.K;
       for (int j = i + 1; j < k1; ++j)
-        if (ids[j] == e) w += a.topk_w[j];
+        if (ids[j] == e) w += weight[j];
+      a.plan->route[at] = static_cast<uint16_t>(i);
       a.plan->weight[at] = w;
     }
     __syncwarp();
@@ -223,23 +243,23 @@ __device__ void make_plan(const W4Args& a) {
   }
 }
 
-// Block 0 plans; block 1 + t makes token t's operand row.  The counters of the later
-// launches start at zero here.
+// Block 0 plans; block 1 + t makes token t's operand row.  The counters of the
+// later launches start at zero here.
 template <typename IdT>
-__global__ void __launch_bounds__(kW4Threads) w4_prepare_kernel(const W4Args a) {
+__global__ void __launch_bounds__(kPrepThreads) w4_prepare_kernel(const W4Args a) {
   grid_launch_dependents();
   if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < a.H / kRows; i += kW4Threads) a.done[i] = 0;
-    for (int i = threadIdx.x; i < a.T * a.K; i += kW4Threads) a.zmax[i] = 0;
+    for (int i = threadIdx.x; i < 2 * kW4MaxBlocks * kW4Warps; i += kPrepThreads) a.done[i] = 0;
+    for (int i = threadIdx.x; i < a.T * a.K; i += kPrepThreads) a.zmax[i] = 0;
     make_plan<IdT>(a);
     return;
   }
-  __shared__ uint32_t s_max[kW4Warps];
+  __shared__ uint32_t s_max[kPrepThreads / 32];
   const int t = blockIdx.x - 1, lane = threadIdx.x & 31;
   const uint4* x = reinterpret_cast<const uint4*>(a.x + static_cast<int64_t>(t) * a.H);
   const int nvec = a.H / 8;
   uint32_t m = 0;
-  for (int i = threadIdx.x; i < nvec; i += kW4Threads) {
+  for (int i = threadIdx.x; i < nvec; i += kPrepThreads) {
     float v[8];
     bf16x8_to_f32(x[i], v);
 #pragma unroll
@@ -248,15 +268,17 @@ __global__ void __launch_bounds__(kW4Threads) w4_prepare_kernel(const W4Args a) 
   m = __reduce_max_sync(0xffffffffu, m);
   if (lane == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();
-  m = __reduce_max_sync(0xffffffffu, s_max[lane % kW4Warps]);
+  m = __reduce_max_sync(0xffffffffu, s_max[lane % (kPrepThreads / 32)]);
   float back;
   const float mult = operand_scale(m, &back);
   if (threadIdx.x == 0) a.xscale[t] = back;
-  for (int i = threadIdx.x; i < nvec; i += kW4Threads) {
+  uint8_t* row = a.xs + static_cast<int64_t>(t) * operand_row_bytes(a.H);
+  for (int i = threadIdx.x; i < nvec; i += kPrepThreads) {
     float v[8];
     bf16x8_to_f32(x[i], v);
-    store_operand(a.xs + static_cast<int64_t>(t) * 2 * a.H, a.xsum + t * (a.H / kGroup), i, v, mult);
+    store_operand(row, i, v, mult);
   }
+  store_operand_end(row, a.H);
 }
 
 // A block per kept route.
@@ -269,25 +291,25 @@ __global__ void __launch_bounds__(128) w4_operand_z_kernel(const W4Args a) {
   const float mult = operand_scale(a.zmax[route], &back);
   if (threadIdx.x == 0) a.zscale[route] = back;
   const float4* z = reinterpret_cast<const float4*>(a.z + static_cast<int64_t>(route) * a.I);
+  uint8_t* row = a.zs + static_cast<int64_t>(route) * operand_row_bytes(a.I);
   for (int i = threadIdx.x; i < a.I / 8; i += blockDim.x) {
     const float4 lo = z[2 * i], hi = z[2 * i + 1];
     const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    store_operand(a.zs + static_cast<int64_t>(route) * 2 * a.I, a.zsum + route * (a.I / kGroup), i, v,
-                mult);
+    store_operand(row, i, v, mult);
   }
+  store_operand_end(row, a.I);
 }
 
 // ----------------------------------------------------------------- products
-// The lane's 64 bytes of a 128-group of its column: the pairs of words 0..3.
-__device__ __forceinline__ void load_column(uint4* v, const uint8_t* row, int g, int q) {
-  const uint4* p = reinterpret_cast<const uint4*>(row + g * 256 + q * 64);
+// The lane's 64 bytes of a group record: the pairs of words 0..3.
+__device__ __forceinline__ void load_column(uint4* v, const uint8_t* rec, int q) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = p[i];
+  for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(rec + i * 64 + q * 16);
 }
 
 __device__ __forceinline__ void mma_16x8x16(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -324,12 +346,12 @@ __device__ __forceinline__ void w4_dot(float* acc, const uint8_t* p, uint32_t sa
 // lie in different halves of the 128 bytes.
 __device__ __forceinline__ int tile_row(int r) { return (r >> 1) | ((r & 1) << 2); }
 
-// The scales of groups g and g + 1 (if there is one) of one row, the first in
-// the low half.
+// The scales of groups g and g + 1 of one row, the first in the low half; zero
+// for a group that is not there.
 __device__ __forceinline__ uint32_t load_scales(const uint16_t* row, int g, int G) {
-  if ((G & 1) == 0) return *reinterpret_cast<const uint32_t*>(row + g);
-  uint32_t v = row[g];
-  if (g + 1 < G) v |= static_cast<uint32_t>(row[g + 1]) << 16;
+  if ((G & 1) == 0) return __ldg(reinterpret_cast<const uint32_t*>(row + g));
+  uint32_t v = __ldg(row + g);
+  if (g + 1 < G) v |= static_cast<uint32_t>(__ldg(row + g + 1)) << 16;
   return v;
 }
 __device__ __forceinline__ uint32_t scale_lo(uint32_t s) { return s << 16; }
@@ -350,166 +372,299 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
   return p + (((a + 1023u) & ~1023u) - a);
 }
 
-// Gate/up: an item is 16 gate rows and the same 16 up rows of one pass.  A
-// team of warps takes an item: one warp where there are items enough to fill
-// the GPU, else up to eight that take the item's boxes in turn.
+// The gate/up launch (a tile: 128 gate rows and the same up rows of one pass)
+// and the down launch (a tile: 128 rows of H, for every pass).
+template <bool kDown>
 __global__ void __launch_bounds__(kW4Threads, 2)
-    w4_gateup_kernel(const __grid_constant__ CUtensorMap map, const W4Args a) {
+    w4_stream_kernel(const __grid_constant__ CUtensorMap map, const W4Args a) {
+  constexpr int kBoxes = kDown ? 1 : 2;
+  constexpr int kABytes = kBoxes * kBoxBytes;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ float s_red[kW4Warps][2][4][32];
-  __shared__ uint64_t s_full[kW4Warps][kGuDepth], s_scale[kW4Warps][2];
+  __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages];
   __shared__ int s_abort;
-  uint8_t* ring0 = align1024(smem_raw);
-  const int G = a.H / kGroup, ns = (G + 1) / 2;
-  const int scale_bytes = kRows * G * 2;   // of a tile
-  uint8_t* scales0 = ring0 + kW4Warps * kGuDepth * 2 * kBoxBytes;
-  uint32_t* passes = reinterpret_cast<uint32_t*>(scales0 + kW4Warps * 4 * scale_bytes);
-  uint16_t* routes = reinterpret_cast<uint16_t*>(passes + a.max_passes);
+  uint8_t* ring = align1024(smem_raw);                     // [stages][kABytes]
+  uint8_t* cols = ring + a.stages * kABytes;               // [stages][kCols][kColBytes]
+  float* s_y = reinterpret_cast<float*>(cols + a.stages * kCols * kColBytes);  // down: [warps][T][kRows]
+  const int per = kDown ? a.T * kRows : 0;
+  uint32_t* passes = reinterpret_cast<uint32_t*>(s_y + kW4Warps * per);
+  float* weights = reinterpret_cast<float*>(passes + a.max_passes);            // down
+  uint16_t* routes = reinterpret_cast<uint16_t*>(weights + (kDown ? a.T * a.K : 0));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = lane >> 2, q = lane & 3;
-  if (lane == 0) {
-    for (int i = 0; i < kGuDepth; ++i) mbar_init(&s_full[warp][i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&s_scale[warp][i], 1);
-    fence_barrier_init();
-  }
   if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], kW4Warps);
+    }
     s_abort = 0;
+    fence_barrier_init();
     tma_prefetch_desc(&map);
   }
-  grid_dependency_wait();
-  // only now: the launch after next reads the plan without waiting for this one
-  grid_launch_dependents();
-  const int np = a.plan->passes, nr = a.plan->routes;
-  for (int i = threadIdx.x; i < np; i += kW4Threads) passes[i] = a.plan->pass[i];
-  for (int i = threadIdx.x; i < nr; i += kW4Threads) routes[i] = a.plan->route[i];
+  if constexpr (!kDown) {
+    grid_dependency_wait();
+    // only now: the launch after next reads the plan without waiting for this one
+    grid_launch_dependents();
+  }
+  // The plan.  In the down launch it is read through L2 before the wait: it was
+  // complete before the gate/up blocks let the launches after them start.
+  const int np = __ldcg(&a.plan->passes), nr = __ldcg(&a.plan->routes);
+  for (int i = threadIdx.x; i < np; i += kW4Threads) passes[i] = __ldcg(&a.plan->pass[i]);
+  for (int i = threadIdx.x; i < nr; i += kW4Threads) {
+    routes[i] = __ldcg(&a.plan->route[i]);
+    if (kDown) weights[i] = __ldcg(&a.plan->weight[i]);
+  }
   __syncthreads();
-  const int tiles = a.I / kRows;
-  const int total = np * tiles;   // at most 1280 passes x 1024 tiles
-  int team = 1;
-  while (team < kW4Warps && total * team * 2 <= static_cast<int>(gridDim.x) * kW4Warps) team *= 2;
-  const int rank = warp & (team - 1);
-  const int it0 = blockIdx.x + gridDim.x * (warp / team);
-  const int it_step = gridDim.x * (kW4Warps / team);
-  uint8_t* ring = ring0 + warp * kGuDepth * 2 * kBoxBytes;
-  uint8_t* scales = scales0 + warp * 4 * scale_bytes;
+
+  const int G = (kDown ? a.I : a.H) / kGroup, ns = (G + 1) / 2;
+  const int row_tiles = (kDown ? a.H : a.I) / kTileRows;
+  const int tiles = kDown ? row_tiles : np * row_tiles;
+  const int units = kDown ? np * ns : ns;     // of a tile
+  const int64_t all = static_cast<int64_t>(tiles) * units;
+  // as many blocks as there are units at most, so no run is empty
+  const int nb = static_cast<int>(min(static_cast<int64_t>(gridDim.x), all));
+  auto start_of = [&](int b) { return all * b / nb; };
+  const bool idle = static_cast<int>(blockIdx.x) >= nb;
+  const int64_t f0 = idle ? 0 : start_of(blockIdx.x), f1 = idle ? 0 : start_of(blockIdx.x + 1);
+  const int t0 = f1 > f0 ? static_cast<int>(f0 / units) : 0;
+  const int t1 = f1 > f0 ? static_cast<int>((f1 - 1) / units) + 1 : 0;   // tiles [t0, t1)
+  // this block's units of tile t
+  auto lo_of = [&](int t) { return static_cast<int>(max(f0 - static_cast<int64_t>(t) * units, int64_t{0})); };
+  auto hi_of = [&](int t) {
+    return static_cast<int>(min(f1 - static_cast<int64_t>(t) * units, static_cast<int64_t>(units)));
+  };
   volatile int* abort_flag = &s_abort;
 
-  // The warp's next box to fetch: box ps of item pit, its pj-th, whose scales
-  // go to buffer pj % 2; it is at most one item ahead of the item in use, uj.
-  int pit = rank < ns ? it0 : total, ps = rank, pj = 0, uj = 0, prow = 0;
-  int issued = 0, used = 0;
-  bool entered = false;
-  auto fetch = [&]() {
-    while (issued - used < kGuDepth && pit < total && pj <= uj + 1) {
-      if (!entered) {
-        prow = unpack_pass(passes[pit / tiles]).e * 2 * a.I + pit % tiles * kRows;
-        if (lane == 0) {
-          uint8_t* dst = scales + (pj & 1) * 2 * scale_bytes;
-          const uint16_t* src = a.s13 + static_cast<int64_t>(prow) * G;
-          mbar_arrive_expect_tx(&s_scale[warp][pj & 1], 2 * scale_bytes);
-          bulk_load(dst, src, scale_bytes, &s_scale[warp][pj & 1]);
-          bulk_load(dst + scale_bytes, src + static_cast<int64_t>(a.I) * G, scale_bytes,
-                    &s_scale[warp][pj & 1]);
+  if (warp == kW4Warps) {
+    // ------------------------------------------------------------- producer
+    // lane 0 fetches the codes, lane c the operand row of column c
+    const uint8_t* ops = kDown ? a.zs : a.xs;
+    const int64_t op_row = operand_row_bytes(kDown ? a.I : a.H);
+    auto columns = [&](const Pass& pass, int s, int sl) {
+      if (lane < pass.n) {
+        const int route = routes[pass.off + lane];
+        bulk_load(cols + (sl * kCols + lane) * kColBytes,
+                  ops + (kDown ? route : route / a.K) * op_row + s * kColBytes, kColBytes, &s_full[sl]);
+      }
+    };
+    // down: z, and the columns of the stages whose codes were fetched without it
+    int issued = 0;
+    auto late_columns = [&]() {
+      grid_dependency_wait();
+      int n = 0;
+      for (int t = t0; t < t1 && n < issued; ++t)
+        for (int u = lo_of(t); u < hi_of(t) && n < issued; ++u, ++n)
+          columns(unpack_pass(passes[u / ns]), u % ns, n);
+    };
+    int slot = 0;
+    uint32_t phase = 1;
+    bool ok = true, waited = !kDown;
+    for (int t = t0; t < t1 && ok; ++t) {
+      const int hi = hi_of(t);
+      for (int u = lo_of(t); u < hi; ++u) {
+        const int p = kDown ? u / ns : t / row_tiles;
+        const int s = kDown ? u - p * ns : u;
+        const Pass pass = unpack_pass(passes[p]);
+        if (!waited && issued == a.stages) {   // the ring is full of codes
+          late_columns();
+          waited = true;
         }
-        entered = true;
-      }
-      if (lane == 0) {
-        const int slot = issued % kGuDepth;
-        uint8_t* dst = ring + slot * 2 * kBoxBytes;
-        mbar_arrive_expect_tx(&s_full[warp][slot], 2 * kBoxBytes);
-        tma_load_2d(dst, &map, &s_full[warp][slot], ps * 128, prow);
-        tma_load_2d(dst + kBoxBytes, &map, &s_full[warp][slot], ps * 128, prow + a.I);
-      }
-      ++issued;
-      ps += team;
-      if (ps >= ns) {
-        ps = rank;
-        pit += it_step;
-        ++pj;
-        entered = false;
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_empty[slot], phase, abort_flag))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          uint8_t* dst = ring + slot * kABytes;
+          mbar_arrive_expect_tx(&s_full[slot], kABytes + pass.n * kColBytes);
+          if (kDown) {
+            tma_load_2d(dst, &map, &s_full[slot], s * 128, pass.e * a.H + t * kTileRows);
+          } else {
+            const int row = pass.e * 2 * a.I + t % row_tiles * kTileRows;
+            tma_load_2d(dst, &map, &s_full[slot], s * 128, row);
+            tma_load_2d(dst + kBoxBytes, &map, &s_full[slot], s * 128, row + a.I);
+          }
+        }
+        __syncwarp();
+        if (waited) columns(pass, s, slot);
+        ++issued;
+        if (++slot == a.stages) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
     }
-  };
-  fetch();
+    if (!waited) late_columns();   // no more units than stages
+    if (!ok) {
+      // no copy may land after the block has ended
+      *abort_flag = 1;
+      for (int i = 0; i < min(issued, a.stages); ++i) {
+        const int n = issued - 1 - i;
+        int none = 0;
+        mbar_wait(&s_full[n % a.stages], (n / a.stages) & 1, &none);
+      }
+    }
+    return;
+  }
 
-  // the lane's first row in a box, for the even and the odd group
+  // ------------------------------------------------------------------ products
+  const int r = lane >> 2, q = lane & 3;
   const int row = tile_row(r);
-  const int off0 = row * 128 + ((q ^ (row & 7)) << 4), off1 = off0 ^ 64;
-  int landed = 0, slot = 0;
+  // the lane's first row in a box, for the first and the second group
+  const int off0 = (warp * kRows + row) * 128 + ((q ^ (row & 7)) << 4), off1 = off0 ^ 64;
+  const uint16_t* scales = kDown ? a.s2 : a.s13;
+  const int64_t up = kDown ? 0 : static_cast<int64_t>(a.I) * G;
+  float* mine = s_y + warp * per;
+  int slot = 0;
   uint32_t phase = 0;
   bool ok = true;
-  for (int it = it0; it < total; it += it_step) {
-    const Pass pass = unpack_pass(passes[it / tiles]);
-    const int i0 = it % tiles * kRows;
-    const uint8_t* xr =
-        r < pass.n ? a.xs + static_cast<int64_t>(routes[pass.off + r] / a.K) * 2 * a.H : nullptr;
-    const float* sum0 = a.xsum + routes[pass.off + min(2 * q, pass.n - 1)] / a.K * G;
-    const float* sum1 = a.xsum + routes[pass.off + min(2 * q + 1, pass.n - 1)] / a.K * G;
-    float ag[4] = {0.f, 0.f, 0.f, 0.f}, au[4] = {0.f, 0.f, 0.f, 0.f};
-    // columns of the even and the odd groups, each loaded while the other's
-    // products run; zeros where the pass has no such column
-    uint4 even[4], odd[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) even[i] = odd[i] = make_uint4(0, 0, 0, 0);
-    if (xr != nullptr && rank < ns) load_column(even, xr, 2 * rank, q);
-    const uint16_t* sc = reinterpret_cast<const uint16_t*>(scales + (uj & 1) * 2 * scale_bytes) + row * G;
-    if (rank < ns && ok &&
-        !__all_sync(0xffffffffu, mbar_wait(&s_scale[warp][uj & 1], (uj >> 1) & 1, abort_flag))) {
-      ok = false;
-      landed = used;
-      *abort_flag = 1;
+  if (kDown) {
+    grid_dependency_wait();   // zscale, and y's readers before this call
+    if (np == 0) {            // no routes
+      for (int t = blockIdx.x; t < tiles; t += gridDim.x)
+        for (int i = threadIdx.x; i < a.T * kTileRows; i += kW4Warps * 32)
+          a.y[static_cast<int64_t>(i / kTileRows) * a.H + t * kTileRows + i % kTileRows] = 0;
     }
-    for (int s = rank; s < ns; s += team) {
-      const bool two = 2 * s + 1 < G;
-      if (xr != nullptr && two) load_column(odd, xr, 2 * s + 1, q);
-      const uint32_t sg0 = load_scales(sc, 2 * s, G), sg1 = load_scales(sc + 8 * G, 2 * s, G);
-      const uint32_t su0 = load_scales(sc + kRows * G, 2 * s, G);
-      const uint32_t su1 = load_scales(sc + (kRows + 8) * G, 2 * s, G);
-      if (ok && !__all_sync(0xffffffffu, mbar_wait(&s_full[warp][slot], phase, abort_flag))) {
-        ok = false;
-        landed = used;
-        *abort_flag = 1;
-      }
-      const uint8_t* box = ring + slot * 2 * kBoxBytes;
-      if (ok) {
-        const float s0 = sum0[2 * s], s1 = sum1[2 * s];
-        w4_dot(ag, box + off0, scale_lo(sg0), scale_lo(sg1), even, s0, s1);
-        w4_dot(au, box + kBoxBytes + off0, scale_lo(su0), scale_lo(su1), even, s0, s1);
-      }
-      if (xr != nullptr && s + team < ns) load_column(even, xr, 2 * (s + team), q);
-      if (ok && two) {
-        const float s0 = sum0[2 * s + 1], s1 = sum1[2 * s + 1];
-        w4_dot(ag, box + off1, scale_hi(sg0), scale_hi(sg1), odd, s0, s1);
-        w4_dot(au, box + kBoxBytes + off1, scale_hi(su0), scale_hi(su1), odd, s0, s1);
-      }
-      ++used;
-      if (++slot == kGuDepth) {
-        slot = 0;
-        phase ^= 1;
-      }
-      __syncwarp();   // every lane has read the slot
-      if (ok) fetch();
+  }
+  for (int t = t0; t < t1 && ok; ++t) {
+    const int lo = lo_of(t), hi = hi_of(t);
+    if (kDown) {
+      for (int i = lane; i < per; i += 32) mine[i] = 0.f;
+      __syncwarp();
     }
-    ++uj;
-    if (ok) fetch();   // the next item's scales may have waited for this one's
-    if (team > 1) {   // the parts of the team's warps, in their order
+    float acc[kBoxes][4];
+    Pass pass{};
+    for (int u = lo; u < hi && ok;) {
+      const int p = kDown ? u / ns : t / row_tiles;
+      const int first_s = kDown ? u - p * ns : u;
+      const int last_s = kDown ? min(hi - p * ns, ns) : hi;
+      u += last_s - first_s;
+      pass = unpack_pass(passes[p]);
+      const uint16_t* sp =
+          scales + static_cast<int64_t>((kDown ? pass.e * a.H + t * kTileRows
+                                               : pass.e * 2 * a.I + t % row_tiles * kTileRows) +
+                                        warp * kRows + row) * G;
+      uint32_t next[2 * kBoxes];
+      auto scales_of = [&](int s) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s_red[warp][0][j][lane] = ag[j];
-        s_red[warp][1][j][lane] = au[j];
+        for (int b = 0; b < kBoxes; ++b) {
+          next[2 * b] = load_scales(sp + b * up, 2 * s, G);
+          next[2 * b + 1] = load_scales(sp + b * up + 8 * G, 2 * s, G);
+        }
+      };
+      scales_of(first_s);
+#pragma unroll
+      for (int b = 0; b < kBoxes; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[b][j] = 0.f;
+      for (int s = first_s; s < last_s; ++s) {
+        uint32_t sc[2 * kBoxes];
+#pragma unroll
+        for (int j = 0; j < 2 * kBoxes; ++j) sc[j] = next[j];
+        if (s + 1 < last_s) scales_of(s + 1);   // a unit ahead of their use
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[slot], phase, abort_flag))) {
+          ok = false;
+          break;
+        }
+        const uint8_t* box = ring + slot * kABytes;
+        const uint8_t* col = cols + slot * kCols * kColBytes;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          uint4 v[4];
+          load_column(v, col + r * kColBytes + g * kOpBytes, q);
+          const float* sums = reinterpret_cast<const float*>(col + 2 * q * kColBytes + g * kOpBytes + 256);
+          const float s0 = sums[0], s1 = sums[kColBytes / 4];
+#pragma unroll
+          for (int b = 0; b < kBoxes; ++b)
+            w4_dot(acc[b], box + b * kBoxBytes + (g ? off1 : off0),
+                   g ? scale_hi(sc[2 * b]) : scale_lo(sc[2 * b]),
+                   g ? scale_hi(sc[2 * b + 1]) : scale_lo(sc[2 * b + 1]), v, s0, s1);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[slot]);
+        if (++slot == a.stages) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / team), "r"(32 * team) : "memory");
-      if (rank == 0) {
-        for (int w = 1; w < team; ++w)
+      if (kDown) {
+        // the routes of a pass have different tokens: no two lanes share a sum
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            ag[j] += s_red[warp + w][0][j][lane];
-            au[j] += s_red[warp + w][1][j][lane];
+        for (int j = 0; j < 2; ++j) {
+          const int cc = 2 * q + j;
+          if (cc < pass.n) {
+            const int route = routes[pass.off + cc];
+            const float wt = weights[pass.off + cc] * a.zscale[route];
+            float* yt = mine + route / a.K * kRows + row;
+            yt[0] = fmaf(wt, acc[0][j] * 0x1p24f, yt[0]);
+            yt[8] = fmaf(wt, acc[0][2 + j] * 0x1p24f, yt[8]);
           }
+        }
+        __syncwarp();
       }
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / team), "r"(32 * team) : "memory");
     }
-    if (rank == 0) {
+    if (!ok) break;
+
+    // A shared tile: leave the sums, and go on only as the last of its blocks.
+    const bool whole = lo == 0 && hi == units;
+    int b0 = 0, b1 = 0;
+    if (!whole) {
+      const int count = kDown ? per : 256;
+      const int64_t first = static_cast<int64_t>(t) * units, last = first + units - 1;
+      b0 = static_cast<int>(first * nb / all);
+      b1 = static_cast<int>(last * nb / all);
+      int64_t begin = start_of(b0);
+      for (int64_t n; (n = start_of(b0 + 1)) <= first; ++b0) begin = n;
+      while (start_of(b1 + 1) <= last) ++b1;
+      const int sharing = b1 - b0 + 1;
+      // a block's first tile is its slot 0; only b0 can have begun before this one
+      const int b0_slot = begin < first ? 1 : 0;
+      auto part_of = [&](int b) {
+        return a.part + ((static_cast<int64_t>(b) * 2 + (b == b0 ? b0_slot : 0)) * kW4Warps + warp) * count;
+      };
+      float* part = part_of(blockIdx.x);
+      if (kDown) {
+        for (int i = lane; i < per; i += 32) part[i] = mine[i];
+      } else {
+#pragma unroll
+        for (int b = 0; b < kBoxes; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) part[(b * 4 + j) * 32 + lane] = acc[b][j];
+      }
+      __threadfence();
+      __syncwarp();
+      int before = 0;
+      if (lane == 0)
+        before = atomicAdd(a.done + ((kDown ? kW4MaxBlocks : 0) + b0) * kW4Warps + warp, 1);
+      before = __shfl_sync(0xffffffffu, before, 0);
+      if (before != sharing - 1) continue;
+      __threadfence();
+      if (kDown) {
+        for (int i = lane; i < per; i += 32) mine[i] = 0.f;
+      } else {
+#pragma unroll
+        for (int b = 0; b < kBoxes; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[b][j] = 0.f;
+      }
+      for (int b = b0; b <= b1; ++b) {
+        const float* from = part_of(b);
+        if (kDown) {
+          for (int i = lane; i < per; i += 32) mine[i] += __ldcg(from + i);
+        } else {
+#pragma unroll
+          for (int x = 0; x < kBoxes; ++x)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[x][j] += __ldcg(from + (x * 4 + j) * 32 + lane);
+        }
+      }
+      __syncwarp();
+    }
+
+    if constexpr (kDown) {
+      for (int i = lane; i < per; i += 32)
+        a.y[static_cast<int64_t>(i / kRows) * a.H + t * kTileRows + warp * kRows + i % kRows] =
+            __bfloat16_as_ushort(__float2bfloat16_rn(mine[i]));
+      __syncwarp();
+    } else {
+      const int i0 = t % row_tiles * kTileRows + warp * kRows + row;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int cc = 2 * q + j;
@@ -518,12 +673,12 @@ __global__ void __launch_bounds__(kW4Threads, 2)
         if (cc < pass.n) {
           route = routes[pass.off + cc];
           const float back = a.xscale[route / a.K];
-          float* z = a.z + static_cast<int64_t>(route) * a.I + i0 + row;
+          float* z = a.z + static_cast<int64_t>(route) * a.I + i0;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float gate = ag[2 * h + j] * 0x1p24f * back;
-            const float up_v = au[2 * h + j] * 0x1p24f * back;
-            const float v = gate / (1.f + expf(-gate)) * up_v;
+            const float gate = acc[0][2 * h + j] * 0x1p24f * back;
+            const float upv = acc[kBoxes - 1][2 * h + j] * 0x1p24f * back;
+            const float v = gate / (1.f + expf(-gate)) * upv;
             z[8 * h] = v;
             m = max(m, __float_as_uint(v) & 0x7fffffffu);
           }
@@ -536,267 +691,14 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     }
   }
   if (!ok) {
-    // no copy may land after the block has ended
-    for (; landed < issued; ++landed) {
-      int none = 0;
-      mbar_wait(&s_full[warp][landed % kGuDepth], (landed / kGuDepth) & 1, &none);
-    }
-    for (int j = uj; j <= pj && j <= uj + 1; ++j) {
-      int none = 0;
-      if (j < pj || entered) mbar_wait(&s_scale[warp][j & 1], (j >> 1) & 1, &none);
-    }
-    if (lane == 0) atomicOr(a.dev_status, kDevTimeout);
-  }
-}
-
-// Down: 16 rows of H for every pass make a tile; the (tile, pass, box) units
-// in that order are cut into equal runs, one per block, so every SM reads the
-// same number of bytes whatever H and the routes are.  Inside a block the
-// warps take equal runs of a tile's units and keep a sum per token.  A tile
-// that one block has whole is written by it; of a tile that several blocks
-// share each leaves its sums in the workspace, and the last to finish adds
-// them in block order.  The order of the sums is fixed by the routes alone.
-__global__ void __launch_bounds__(kW4Threads, 2)
-    w4_down_kernel(const __grid_constant__ CUtensorMap map, const W4Args a) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t s_full[kW4Warps][kDnDepth], s_scale[kW4Warps][2];
-  __shared__ int s_abort, s_last;
-  uint8_t* ring0 = align1024(smem_raw);
-  float* s_y = reinterpret_cast<float*>(ring0 + kW4Warps * kDnDepth * kBoxBytes);  // [warps][T][kRows]
-  const int per = a.T * kRows;
-  const int G = a.I / kGroup, ns = (G + 1) / 2;
-  const int scale_bytes = kRows * G * 2;   // of a tile
-  uint8_t* scales0 = reinterpret_cast<uint8_t*>(s_y + kW4Warps * per);
-  uint32_t* passes = reinterpret_cast<uint32_t*>(scales0 + kW4Warps * 2 * scale_bytes);
-  float* weights = reinterpret_cast<float*>(passes + a.max_passes);
-  uint16_t* routes = reinterpret_cast<uint16_t*>(weights + a.T * a.K);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = lane >> 2, q = lane & 3;
-  if (lane == 0) {
-    for (int i = 0; i < kDnDepth; ++i) mbar_init(&s_full[warp][i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&s_scale[warp][i], 1);
-    fence_barrier_init();
-  }
-  if (threadIdx.x == 0) {
-    s_abort = 0;
-    tma_prefetch_desc(&map);
-  }
-  // the plan was complete before the launch of the gate/up blocks went on, so
-  // it is read (through L2) and the first weights are fetched before the wait
-  const int np = __ldcg(&a.plan->passes), nr = __ldcg(&a.plan->routes);
-  for (int i = threadIdx.x; i < np; i += kW4Threads) passes[i] = __ldcg(&a.plan->pass[i]);
-  for (int i = threadIdx.x; i < nr; i += kW4Threads) {
-    routes[i] = __ldcg(&a.plan->route[i]);
-    weights[i] = __ldcg(&a.plan->weight[i]);
-  }
-  __syncthreads();
-  const int tiles = a.H / kRows;
-  const int units = np * ns;      // of a tile: at most 1280 x 64
-  const int64_t all = static_cast<int64_t>(tiles) * units;
-  const int nb = gridDim.x;
-  auto start_of = [&](int b) { return all * b / nb; };
-  const int64_t f0 = start_of(blockIdx.x), f1 = start_of(blockIdx.x + 1);
-  const int t0 = units ? static_cast<int>(f0 / units) : 0;
-  const int t1 = units && f1 > f0 ? static_cast<int>((f1 - 1) / units) + 1 : t0;   // tiles [t0, t1)
-  // this block's units of tile t, and this warp's of those
-  auto block_lo = [&](int t) { return static_cast<int>(max(f0 - static_cast<int64_t>(t) * units, int64_t{0})); };
-  auto block_hi = [&](int t) {
-    return static_cast<int>(min(f1 - static_cast<int64_t>(t) * units, static_cast<int64_t>(units)));
-  };
-  auto warp_at = [&](int t, int w) {
-    const int lo = block_lo(t);
-    return lo + (block_hi(t) - lo) * w / kW4Warps;
-  };
-  uint8_t* ring = ring0 + warp * kDnDepth * kBoxBytes;
-  uint8_t* scales = scales0 + warp * 2 * scale_bytes;
-  float* mine = s_y + warp * per;
-  volatile int* abort_flag = &s_abort;
-
-  // The warp's next box to fetch: unit pu of tile pt, where the warp's run ends
-  // at pend.  Runs of one pass in one tile share their scales: the pj-th run's
-  // are in buffer pj % 2, at most one run ahead of the run in use, uj.
-  int pt = t0, pu = 0, pend = 0, pj = 0, uj = 0;
-  int issued = 0, used = 0, prow = 0, prun = 0;   // prun: where the run ends
-  bool entered = false;
-  auto settle = [&]() {
-    while (pt < t1 && pu >= pend) {
-      ++pt;
-      if (pt < t1) {
-        pu = warp_at(pt, warp);
-        pend = warp_at(pt, warp + 1);
-      }
-    }
-  };
-  auto fetch = [&]() {
-    while (issued - used < kDnDepth && pt < t1 && pj <= uj + 1) {
-      if (!entered) {
-        const int p = pu / ns;
-        prow = unpack_pass(passes[p]).e * a.H + pt * kRows;
-        prun = min(pend, (p + 1) * ns);
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&s_scale[warp][pj & 1], scale_bytes);
-          bulk_load(scales + (pj & 1) * scale_bytes, a.s2 + static_cast<int64_t>(prow) * G,
-                    scale_bytes, &s_scale[warp][pj & 1]);
-        }
-        entered = true;
-      }
-      if (lane == 0) {
-        const int slot = issued % kDnDepth;
-        mbar_arrive_expect_tx(&s_full[warp][slot], kBoxBytes);
-        tma_load_2d(ring + slot * kBoxBytes, &map, &s_full[warp][slot], pu % ns * 128, prow);
-      }
-      ++issued;
-      if (++pu == prun) {
-        ++pj;
-        entered = false;
-        settle();
-      }
-    }
-  };
-  if (pt < t1) {
-    pu = warp_at(pt, warp);
-    pend = warp_at(pt, warp + 1);
-    settle();
-  }
-  fetch();
-  grid_dependency_wait();   // z
-  if (units == 0) {   // no routes
-    for (int t = blockIdx.x; t < tiles; t += nb)
-      for (int i = threadIdx.x; i < per; i += kW4Threads)
-        a.y[static_cast<int64_t>(i / kRows) * a.H + t * kRows + i % kRows] = 0;
-    return;
-  }
-
-  const int row = tile_row(r);
-  const int off0 = row * 128 + ((q ^ (row & 7)) << 4), off1 = off0 ^ 64;
-  int landed = 0, slot = 0;
-  uint32_t phase = 0;
-  bool ok = true;
-  for (int t = t0; t < t1; ++t) {
-    for (int i = lane; i < per; i += 32) mine[i] = 0.f;
-    __syncwarp();
-    const int u1 = warp_at(t, warp + 1);
-    for (int u = warp_at(t, warp); u < u1;) {
-      const int p = u / ns;
-      const Pass pass = unpack_pass(passes[p]);
-      const int s1 = min(u1 - p * ns, ns);
-      const uint8_t* zr =
-          r < pass.n ? a.zs + static_cast<int64_t>(routes[pass.off + r]) * 2 * a.I : nullptr;
-      const float* sum0 = a.zsum + routes[pass.off + min(2 * q, pass.n - 1)] * G;
-      const float* sum1 = a.zsum + routes[pass.off + min(2 * q + 1, pass.n - 1)] * G;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      uint4 even[4], odd[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) even[i] = odd[i] = make_uint4(0, 0, 0, 0);
-      int s = u - p * ns;
-      u = p * ns + s1;
-      if (zr != nullptr) load_column(even, zr, 2 * s, q);
-      const uint16_t* sc = reinterpret_cast<const uint16_t*>(scales + (uj & 1) * scale_bytes) + row * G;
-      if (ok && !__all_sync(0xffffffffu, mbar_wait(&s_scale[warp][uj & 1], (uj >> 1) & 1, abort_flag))) {
-        ok = false;
-        landed = used;
-        *abort_flag = 1;
-      }
-      for (; s < s1; ++s) {
-        const bool two = 2 * s + 1 < G;
-        if (zr != nullptr && two) load_column(odd, zr, 2 * s + 1, q);
-        const uint32_t sa = load_scales(sc, 2 * s, G), sb = load_scales(sc + 8 * G, 2 * s, G);
-        if (ok && !__all_sync(0xffffffffu, mbar_wait(&s_full[warp][slot], phase, abort_flag))) {
-          ok = false;
-          landed = used;
-          *abort_flag = 1;
-        }
-        const uint8_t* box = ring + slot * kBoxBytes;
-        if (ok) {
-            const float s0 = sum0[2 * s], s1 = sum1[2 * s];
-          w4_dot(acc, box + off0, scale_lo(sa), scale_lo(sb), even, s0, s1);
-        }
-        if (zr != nullptr && s + 1 < s1) load_column(even, zr, 2 * s + 2, q);
-        if (ok && two) {
-            const float s0 = sum0[2 * s + 1], s1 = sum1[2 * s + 1];
-          w4_dot(acc, box + off1, scale_hi(sa), scale_hi(sb), odd, s0, s1);
-        }
-        ++used;
-        if (++slot == kDnDepth) {
-          slot = 0;
-          phase ^= 1;
-        }
-        __syncwarp();   // every lane has read the slot
-        if (ok) fetch();
-      }
-      ++uj;
-      if (ok) fetch();
-      // the routes of a pass have different tokens: no two lanes share a sum
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int cc = 2 * q + j;
-        if (cc < pass.n) {
-          const int route = routes[pass.off + cc];
-          const float wt = weights[pass.off + cc] * a.zscale[route];
-          float* yt = mine + route / a.K * kRows + row;
-          yt[0] = fmaf(wt, acc[j] * 0x1p24f, yt[0]);
-          yt[8] = fmaf(wt, acc[2 + j] * 0x1p24f, yt[8]);
-        }
-      }
-      __syncwarp();
-    }
-    __syncthreads();
-    const bool whole = block_lo(t) == 0 && block_hi(t) == units;
-    float* part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (t > t0 ? 1 : 0)) * per;
-    for (int i = threadIdx.x; i < per; i += kW4Threads) {
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kW4Warps; ++w) v += s_y[w * per + i];
-      if (whole)
-        a.y[static_cast<int64_t>(i / kRows) * a.H + t * kRows + i % kRows] =
-            __bfloat16_as_ushort(__float2bfloat16_rn(v));
-      else
-        part[i] = v;
-    }
-    if (!whole) {
-      // blocks b0 .. b1 share the tile
-      const int64_t lo = static_cast<int64_t>(t) * units, hi = lo + units;
-      int b0 = static_cast<int>(lo * nb / all), b1 = static_cast<int>((hi - 1) * nb / all);
-      while (start_of(b0 + 1) <= lo) ++b0;
-      while (start_of(b1 + 1) <= hi - 1) ++b1;
-      int sharing = 0;
-      for (int b = b0; b <= b1; ++b) sharing += start_of(b + 1) > start_of(b);
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) s_last = atomicAdd(a.done + t, 1) == sharing - 1;
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        for (int i = threadIdx.x; i < per; i += kW4Threads) {
-          float v = 0.f;
-          for (int b = b0; b <= b1; ++b) {
-            const int64_t f = start_of(b);
-            if (start_of(b + 1) == f) continue;
-            v += __ldcg(a.part + (static_cast<int64_t>(b) * 2 + (f / units < t ? 1 : 0)) * per + i);
-          }
-          a.y[static_cast<int64_t>(i / kRows) * a.H + t * kRows + i % kRows] =
-              __bfloat16_as_ushort(__float2bfloat16_rn(v));
-        }
-      }
-    }
-    __syncthreads();
-  }
-  if (!ok) {
-    for (; landed < issued; ++landed) {
-      int none = 0;
-      mbar_wait(&s_full[warp][landed % kDnDepth], (landed / kDnDepth) & 1, &none);
-    }
-    for (int j = uj; j <= pj && j <= uj + 1; ++j) {
-      int none = 0;
-      if (j < pj || entered) mbar_wait(&s_scale[warp][j & 1], (j >> 1) & 1, &none);
-    }
+    *abort_flag = 1;
     if (lane == 0) atomicOr(a.dev_status, kDevTimeout);
   }
 }
 
 // Offsets of the workspace's parts.
 struct W4Workspace {
-  size_t plan, xs, xscale, xsum, z, zmax, zs, zscale, zsum, done, part, total;
+  size_t plan, xs, xscale, z, zmax, zs, zscale, done, part, total;
 };
 W4Workspace w4_workspace(int T, int K, int H, int I) {
   size_t off = 0;
@@ -808,16 +710,14 @@ W4Workspace w4_workspace(int T, int K, int H, int I) {
   const size_t n = static_cast<size_t>(T) * K;
   W4Workspace w{};
   w.plan = take(sizeof(W4Plan));
-  w.xs = take(static_cast<size_t>(T) * 2 * H);
+  w.xs = take(static_cast<size_t>(T) * operand_row_bytes(H));
   w.xscale = take(static_cast<size_t>(T) * 4);
-  w.xsum = take(static_cast<size_t>(T) * (H / kGroup) * 4);
   w.z = take(n * I * 4);
   w.zmax = take(n * 4);
-  w.zs = take(n * 2 * I);
+  w.zs = take(n * operand_row_bytes(I));
   w.zscale = take(n * 4);
-  w.zsum = take(n * (I / kGroup) * 4);
-  w.done = take(kMaxTiles * 4);
-  w.part = take(static_cast<size_t>(kW4MaxBlocks) * 2 * T * kRows * 4);
+  w.done = take(2 * kW4MaxBlocks * kW4Warps * 4);
+  w.part = take(static_cast<size_t>(kW4MaxBlocks) * 2 * kW4Warps * std::max(256, T * kRows) * 4);
   w.total = off;
   return w;
 }
@@ -863,12 +763,10 @@ cudaError_t launch_experts_w4(const void* x, const void* topk_idx, int idx_bits,
   a.plan = reinterpret_cast<W4Plan*>(ws + w.plan);
   a.xs = ws + w.xs;
   a.xscale = reinterpret_cast<float*>(ws + w.xscale);
-  a.xsum = reinterpret_cast<float*>(ws + w.xsum);
   a.z = reinterpret_cast<float*>(ws + w.z);
   a.zmax = reinterpret_cast<uint32_t*>(ws + w.zmax);
   a.zs = ws + w.zs;
   a.zscale = reinterpret_cast<float*>(ws + w.zscale);
-  a.zsum = reinterpret_cast<float*>(ws + w.zsum);
   a.done = reinterpret_cast<int*>(ws + w.done);
   a.part = reinterpret_cast<float*>(ws + w.part);
   a.T = T;
@@ -880,35 +778,43 @@ cudaError_t launch_experts_w4(const void* x, const void* topk_idx, int idx_bits,
 
   CUtensorMap m13, m2;
   cudaError_t err = make_map_rows128(&m13, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w13, H / 2,
-                                     static_cast<uint64_t>(E) * 2 * I, kRows);
+                                     static_cast<uint64_t>(E) * 2 * I, kTileRows);
   if (err == cudaSuccess)
     err = make_map_rows128(&m2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w2, I / 2,
-                           static_cast<uint64_t>(E) * H, kRows);
-  const int gu_smem = 1024 + kW4Warps * (kGuDepth * 2 * kBoxBytes + 4 * kRows * (H / kGroup) * 2) +
-                      4 * a.max_passes + 2 * n;
-  const int dn_smem = 1024 + kW4Warps * (kDnDepth * kBoxBytes + T * kRows * 4 +
-                                         2 * kRows * (I / kGroup) * 2) +
-                      4 * a.max_passes + 6 * n;
-  constexpr int kMaxSmem = 218 * 1024;
-  static_assert(1024 + kW4Warps * (kGuDepth * 2 * kBoxBytes + 4 * kRows * 128 * 2) + 4 * kMaxPasses +
-                            2 * kMaxRoutes <= kMaxSmem &&
-                    1024 + kW4Warps * (kDnDepth * kBoxBytes + kW4MaxTokens * kRows * 4 +
-                                       2 * kRows * 128 * 2) + 4 * kMaxPasses + 6 * kMaxRoutes <=
-                        kMaxSmem,
+                           static_cast<uint64_t>(E) * H, kTileRows);
+  // Two blocks per SM: as many stages as half an SM's shared memory (less what
+  // the system takes) holds, three at least.
+  constexpr int kHalf = 113 * 1024 - 256;
+  constexpr int kMaxSmem = 200 * 1024;
+  constexpr int kStage = kCols * kColBytes;
+  auto smem_of = [&](bool down, int stages) {
+    return 1024 + stages * ((down ? 1 : 2) * kBoxBytes + kStage) + 4 * a.max_passes + 2 * n +
+           (down ? kW4Warps * T * kRows * 4 + 4 * n : 0);
+  };
+  auto stages_of = [&](bool down) {
+    int s = kMaxStages;
+    while (s > 3 && smem_of(down, s) > kHalf) --s;
+    return s;
+  };
+  static_assert(1024 + 3 * (2 * kBoxBytes + kStage) + 4 * kMaxPasses + 2 * kMaxRoutes <= kMaxSmem &&
+                    1024 + 3 * (kBoxBytes + kStage) + kW4Warps * kW4MaxTokens * kRows * 4 +
+                            4 * kMaxPasses + 6 * kMaxRoutes <= kMaxSmem,
                 "shared memory of the largest call");
   if (err == cudaSuccess)
-    err = cudaFuncSetAttribute(w4_gateup_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    err = cudaFuncSetAttribute(w4_stream_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (err == cudaSuccess)
-    err = cudaFuncSetAttribute(w4_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    err = cudaFuncSetAttribute(w4_stream_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (err != cudaSuccess) return err;
-  if (idx_bits == 32) w4_prepare_kernel<int32_t><<<1 + T, kW4Threads, 0, s>>>(a);
-  else w4_prepare_kernel<int64_t><<<1 + T, kW4Threads, 0, s>>>(a);
+  if (idx_bits == 32) w4_prepare_kernel<int32_t><<<1 + T, kPrepThreads, 0, s>>>(a);
+  else w4_prepare_kernel<int64_t><<<1 + T, kPrepThreads, 0, s>>>(a);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
   const int blocks = std::min(kW4MaxBlocks, 2 * sm_count);
-  err = launch_dependent(w4_gateup_kernel, std::min(a.max_passes * (I / kRows), blocks), kW4Threads,
-                         gu_smem, s, m13, a);
+  a.stages = stages_of(false);
+  err = launch_dependent(w4_stream_kernel<false>, blocks, kW4Threads, smem_of(false, a.stages), s, m13, a);
   if (err == cudaSuccess) err = launch_dependent(w4_operand_z_kernel, n, 128, 0, s, a);
-  if (err == cudaSuccess) err = launch_dependent(w4_down_kernel, blocks, kW4Threads, dn_smem, s, m2, a);
+  a.stages = stages_of(true);
+  if (err == cudaSuccess)
+    err = launch_dependent(w4_stream_kernel<true>, blocks, kW4Threads, smem_of(true, a.stages), s, m2, a);
   return err;
 }
 
