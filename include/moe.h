@@ -518,10 +518,9 @@ moe_status moe_dispatch_fp8(const uint8_t* tq, const float* ts, const void* topk
  * dispatch, gated-SiLU expert ("SGLang Expert Compute Backend", §1.1) and
  * weighted combine ("SGLang、NCCL 与 MoE EP", §1.1) of T <= MOE_W4_MAX_TOKENS
  * tokens as matrix-vector products; every active expert's weights are read
- * once.  x enters exactly (down to 2^-27 of a token's largest element), SiLU(g)
- * * u of a route with eleven significant bits (down to 2^-24 of the route's
- * largest); products and sums are fp32.  A token with a NaN or an infinity gets
- * NaN.
+ * once.  x enters exactly (down to 2^-27 of the largest of its 128), SiLU(g) * u
+ * with eleven significant bits (down to 2^-24 of the largest of its 128);
+ * products and sums are fp32.  A token with a NaN or an infinity gets NaN.
  *   weight = (code - 8) * scale, 4-bit codes along the contraction, two a byte
  *   (the even element in the low four bits), one BF16 scale per output row and
  *   128 elements of the contraction.
@@ -533,8 +532,8 @@ moe_status moe_dispatch_fp8(const uint8_t* tq, const float* ts, const void* topk
  *   w13_scale  device, BF16 [E, 2I, H/128]
  *   w2         device, uint8 [E, H, I/2];  w2_scale device, BF16 [E, H, I/128]
  *              (x, codes and scales 16-byte aligned)
- *   y          device out, BF16 [T, H]: the weighted sum in fp32 in a fixed
- *              order (ascending expert); zeros for a token without a route
+ *   y          device out, BF16 [T, H]: the weighted sum in fp32 over k
+ *              ascending; zeros for a token without a route
  *   dev_status device, int32 [2]: reset, then MOE_DEV_* bits (no capacity, so
  *              nothing is dropped)
  *   workspace  device, moe_experts_w4_workspace_size(T, K, H, I) bytes, 256-byte

@@ -173,7 +173,7 @@ cudaError_t launch_dispatch_fp8(const uint8_t* tq, const float* ts, const void* 
 
 // ----- 4-bit experts for a few tokens
 constexpr int kW4MaxTokens = 64;
-constexpr int kW4MaxBlocks = 304;   // the down launch's grid: two blocks per SM
+constexpr int kW4MaxBlocks = 304;   // two blocks per SM
 size_t experts_w4_workspace(int T, int K, int H, int I);
 cudaError_t launch_experts_w4(const void* x, const void* topk_idx, int idx_bits,
                               const float* topk_w, int T, int H, int I, int K, int E,
