@@ -130,6 +130,8 @@ def load(build_if_stale: bool = True) -> ctypes.CDLL:
     """Load (building first if the sources are newer) the library and declare
     every entry point.  Raises if it cannot."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

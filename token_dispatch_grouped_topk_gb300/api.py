@@ -370,17 +370,35 @@ def moe_expert_compute_packed(recv, counts, R: int, w13, w13_scale, w2, w2_scale
     return out
 
 
-def _check(t, dtypes, shape, device, name):
-    """A tensor argument's type, shape, place and layout.  Returns its address."""
+def _check(t, dtypes, shape, dev, name):
+    """A tensor argument's type, shape, device (index, that of the first input)
+    and layout.  Returns its address."""
+    if (t.dtype in dtypes and t.shape == shape and t.get_device() == dev and dev >= 0
+            and t.is_contiguous()):
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device or device.type != "cuda":
+    if not t.is_cuda or t.get_device() != dev:
         raise ValueError(f"{name}: expected a CUDA tensor on the inputs' device, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _stream_on(stream, dev):
+    """The raw stream of a call on device ``dev``, which has to be the current
+    device (where the library launches)."""
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the inputs are on cuda:{dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _check_ws(workspace, dev):
+    """(address, bytes) of a workspace on device ``dev``."""
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous CUDA tensor on the inputs' device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 _BF16 = (torch.bfloat16,)
@@ -405,7 +423,7 @@ def moe_add_rms_norm(x, weight, eps: float = 1e-6, *, residual=None, residual_ou
     place).  ``bf16=False`` leaves the BF16 row out.  Returns ``(y, yq, ys,
     residual_out)``, None for what there is not."""
     T, H = x.shape
-    dev = x.device
+    dev = x.get_device()
     px = _check(x, _BF16, (T, H), dev, "x")
     pw = _check(weight, _HALF_OR_F32, (H,), dev, "weight")
     pr = po = None
@@ -419,18 +437,18 @@ def moe_add_rms_norm(x, weight, eps: float = 1e-6, *, residual=None, residual_ou
     elif residual_out is not None:
         raise ValueError("residual_out without residual")
     if y is None and bf16:
-        y = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+        y = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
     py = None if y is None else _check(y, _BF16, (T, H), dev, "y")
     pq = ps = None
     if quant or yq is not None or ys is not None:
         if yq is None:
-            yq = torch.empty(T, H, dtype=torch.uint8, device=dev)
+            yq = torch.empty(T, H, dtype=torch.uint8, device=x.device)
         if ys is None:
-            ys = torch.empty(T, H // 128, dtype=torch.float32, device=dev)
+            ys = torch.empty(T, H // 128, dtype=torch.float32, device=x.device)
         pq = _check(yq, _E4M3, (T, H), dev, "yq")
         ps = _check(ys, _F32, (T, H // 128), dev, "ys")
     st = _lib.load().moe_add_rms_norm(px, pr, rbits, pw, _bits(weight), eps, T, H, py, pq, ps, po,
-                                      _s(stream))
+                                      _stream_on(stream, dev))
     _lib.check("moe_add_rms_norm", st)
     return y, yq, ys, residual_out
 
@@ -440,14 +458,14 @@ def moe_router_logits(x, w, *, logits=None, dev_status=None, stream=None):
     H]`` bf16 to fp32 ``logits [T, E]``, fp32 products and sums."""
     T, H = x.shape
     E = w.shape[0]
-    dev = x.device
+    dev = x.get_device()
     if logits is None:
-        logits = torch.empty(T, E, dtype=torch.float32, device=dev)
+        logits = torch.empty(T, E, dtype=torch.float32, device=x.device)
     st = _lib.load().moe_router_logits(
         _check(x, _BF16, (T, H), dev, "x"), _check(w, _BF16, (E, H), dev, "w"), T, H, E,
         _check(logits, _F32, (T, E), dev, "logits"),
         None if dev_status is None else _check(dev_status, _I32, (2,), dev, "dev_status"),
-        _s(stream))
+        _stream_on(stream, dev))
     _lib.check("moe_router_logits", st)
     return logits
 
@@ -463,19 +481,19 @@ def moe_router_topk(logits, K: int, *, score: str = "softmax", bias=None, groups
     and scaled.  Returns ``(topk_idx [T, K], topk_w [T, K] fp32)``; -1 and 0
     where nothing is left to choose."""
     T, E = logits.shape
-    dev = logits.device
+    dev = logits.get_device()
     if score not in _lib.SCORES:
         raise ValueError(f"score: 'softmax' or 'sigmoid', not {score!r}")
     if topk_idx is None:
-        topk_idx = torch.empty(T, K, dtype=idx_dtype, device=dev)
+        topk_idx = torch.empty(T, K, dtype=idx_dtype, device=logits.device)
     if topk_w is None:
-        topk_w = torch.empty(T, K, dtype=torch.float32, device=dev)
+        topk_w = torch.empty(T, K, dtype=torch.float32, device=logits.device)
     st = _lib.load().moe_router_topk(
         _check(logits, _HALF_OR_F32, (T, E), dev, "logits"), _bits(logits),
         None if bias is None else _check(bias, _F32, (E,), dev, "bias"), T, E, K,
         _lib.SCORES[score], groups, groups if topk_groups is None else topk_groups, group_top,
         1 if renormalize else 0, scale, _check(topk_idx, _IDS, (T, K), dev, "topk_idx"),
-        _bits(topk_idx), _check(topk_w, _F32, (T, K), dev, "topk_w"), _s(stream))
+        _bits(topk_idx), _check(topk_w, _F32, (T, K), dev, "topk_w"), _stream_on(stream, dev))
     _lib.check("moe_router_topk", st)
     return topk_idx, topk_w
 
@@ -489,27 +507,27 @@ def moe_dispatch_fp8(tq, ts, topk_idx, E: int, R: int, *, xq=None, xs=None, coun
     lib = _lib.load()
     T, H = tq.shape
     K = topk_idx.shape[1]
-    dev = tq.device
+    dev = tq.get_device()
     lead = (rows,) if rows else (E, R)
     if xq is None:
-        xq = torch.empty(*lead, H, dtype=torch.uint8, device=dev)
+        xq = torch.empty(*lead, H, dtype=torch.uint8, device=tq.device)
     if xs is None:
-        xs = torch.empty(*lead, H // 128, dtype=torch.float32, device=dev)
+        xs = torch.empty(*lead, H // 128, dtype=torch.float32, device=tq.device)
     if counts is None:
-        counts = torch.empty(E, dtype=torch.int32, device=dev)
+        counts = torch.empty(E, dtype=torch.int32, device=tq.device)
     if src_map is None:
-        src_map = torch.empty(T, K, dtype=torch.int32, device=dev)
+        src_map = torch.empty(T, K, dtype=torch.int32, device=tq.device)
     if dev_status is None:
-        dev_status = torch.empty(2, dtype=torch.int32, device=dev)
+        dev_status = torch.empty(2, dtype=torch.int32, device=tq.device)
     if workspace is None:
-        workspace = _workspace(lib.moe_dispatch_workspace_size(T, K, E), dev)
+        workspace = _workspace(lib.moe_dispatch_workspace_size(T, K, E), tq.device)
     st = lib.moe_dispatch_fp8(
         _check(tq, _E4M3, (T, H), dev, "tq"), _check(ts, _F32, (T, H // 128), dev, "ts"),
         _check(topk_idx, _IDS, (T, K), dev, "topk_idx"), _bits(topk_idx), T, H, K, E, R, rows,
         _check(xq, _E4M3, (*lead, H), dev, "xq"), _check(xs, _F32, (*lead, H // 128), dev, "xs"),
         _check(counts, _I32, (E,), dev, "counts"), _check(src_map, _I32, (T, K), dev, "src_map"),
-        _check(dev_status, _I32, (2,), dev, "dev_status"), _p(workspace), workspace.numel(),
-        _s(stream))
+        _check(dev_status, _I32, (2,), dev, "dev_status"), *_check_ws(workspace, dev),
+        _stream_on(stream, dev))
     _lib.check("moe_dispatch_fp8", st)
     return xq, xs, counts, src_map, dev_status
 
@@ -529,13 +547,13 @@ def moe_experts_w4(x, topk_idx, topk_w, w13, w13_scale, w2, w2_scale, *, y=None,
     K = topk_idx.shape[1]
     E, n13, _ = w13.shape
     I = n13 // 2
-    dev = x.device
+    dev = x.get_device()
     if y is None:
-        y = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+        y = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
     if dev_status is None:
-        dev_status = torch.empty(2, dtype=torch.int32, device=dev)
+        dev_status = torch.empty(2, dtype=torch.int32, device=x.device)
     if workspace is None:
-        workspace = _workspace(lib.moe_experts_w4_workspace_size(T, K, H, I), dev)
+        workspace = _workspace(lib.moe_experts_w4_workspace_size(T, K, H, I), x.device)
     st = lib.moe_experts_w4(
         _check(x, _BF16, (T, H), dev, "x"), _check(topk_idx, _IDS, (T, K), dev, "topk_idx"),
         _bits(topk_idx), _check(topk_w, _F32, (T, K), dev, "topk_w"), T, H, I, K, E,
@@ -544,7 +562,7 @@ def moe_experts_w4(x, topk_idx, topk_w, w13, w13_scale, w2, w2_scale, *, y=None,
         _check(w2, _U8, (E, H, I // 2), dev, "w2"),
         _check(w2_scale, _BF16, (E, H, I // 128), dev, "w2_scale"),
         _check(y, _BF16, (T, H), dev, "y"), _check(dev_status, _I32, (2,), dev, "dev_status"),
-        _p(workspace), workspace.numel(), _s(stream))
+        *_check_ws(workspace, dev), _stream_on(stream, dev))
     _lib.check("moe_experts_w4", st)
     return y
 

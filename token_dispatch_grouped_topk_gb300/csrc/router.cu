@@ -14,9 +14,15 @@
 // choose: equal choices at any spread of the logits, and only the K chosen
 // scores are computed.
 //
-// A warp takes a token: lane i holds experts [i*V, i*V + V) in registers, so
-// the lowest lane with the largest value holds the lowest id.  A choice is a
-// warp maximum (redux on order-preserving integer keys) and a ballot.
+// A warp takes a token: lane i holds the keys of experts [i*V, i*V + V) in
+// registers, so the lowest lane with the largest key holds the lowest id.  The
+// kernel is bound by instructions, not by its few bytes, so a choice is kept
+// short: a warp maximum over the lanes' largest keys (redux on order-preserving
+// integers) finds the lane; that lane's V keys are read from shared memory by V
+// lanes at once, which find the expert, strike it out and give the lane its next
+// largest by one more redux, where the lane alone would walk its registers.
+// Scores are computed up front only where they choose (a bias, or sums of two);
+// otherwise lane k computes the k-th chosen one at the end, from its logit.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -46,142 +52,204 @@ __device__ __forceinline__ uint32_t choice_key(float c) {
   const uint32_t u = __float_as_uint(__fadd_rn(c, 0.f));   // -0 and +0 are one value
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-__device__ __forceinline__ float key_value(uint32_t k) {
-  if (k == 0u) return -INFINITY;
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
-}
-
 template <typename LogitT>
-__device__ __forceinline__ float load_logit(const LogitT* p) {
-  if constexpr (sizeof(LogitT) == 2) return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
-  else return __ldg(p);
+__device__ __forceinline__ float logit_value(LogitT v) {
+  if constexpr (sizeof(LogitT) == 2) return __uint_as_float(static_cast<uint32_t>(v) << 16);
+  else return v;
+}
+// The lane's V logits; -inf past E and for NaN.
+template <typename LogitT, int V>
+__device__ __forceinline__ void load_logits(float* l, const LogitT* row, int e0, int E, bool vec) {
+  constexpr int kBytes = V * static_cast<int>(sizeof(LogitT));
+  LogitT raw[V];
+  if (kBytes >= 4 && vec) {
+    if (e0 < E) {
+      if constexpr (kBytes >= 16) {
+#pragma unroll
+        for (int i = 0; i < kBytes / 16; ++i)
+          reinterpret_cast<uint4*>(raw)[i] = __ldg(reinterpret_cast<const uint4*>(row + e0) + i);
+      } else if constexpr (kBytes == 8) {
+        *reinterpret_cast<uint2*>(raw) = __ldg(reinterpret_cast<const uint2*>(row + e0));
+      } else if constexpr (kBytes == 4) {
+        *reinterpret_cast<uint32_t*>(raw) = __ldg(reinterpret_cast<const uint32_t*>(row + e0));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) l[j] = e0 < E ? logit_value(raw[j]) : -INFINITY;
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) l[j] = e0 + j < E ? logit_value(__ldg(row + e0 + j)) : -INFINITY;
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) l[j] = l[j] == l[j] ? l[j] : -INFINITY;
 }
 
-__device__ __forceinline__ float sigmoid(float l) {
-  return __fdiv_rn(1.f, __fadd_rn(1.f, expf(-l)));
-}
+// 1 / (1 + exp(-l)): each step rounded to nearest.
+__device__ __forceinline__ float sigmoid(float l) { return __frcp_rn(__fadd_rn(1.f, expf(-l))); }
+
+// Best two of a group of experts.
+struct Best {
+  float a, b;
+  __device__ void add(float v) {
+    b = fmaxf(b, fminf(a, v));
+    a = fmaxf(a, v);
+  }
+};
 
 template <typename LogitT, int V>
-__global__ void router_topk_kernel(const TopkArgs a) {
-  extern __shared__ float s_val[];   // straddling groups: [warps][E]
+__global__ void router_topk_kernel(const TopkArgs a, const bool vec) {
+  extern __shared__ uint32_t s_keys[];   // [warps][32 * V]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * (blockDim.x >> 5) + warp;
   if (t >= a.T) return;
   const int E = a.E, e0 = lane * V;
+  uint32_t* keys = s_keys + warp * 32 * V;
   const LogitT* row = static_cast<const LogitT*>(a.logits) + static_cast<int64_t>(t) * E;
+  const bool biased = a.bias != nullptr;
+  const bool sums = a.groups > 1 && a.top == 2;   // groups by sums of two scores
 
   float l[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    l[j] = -INFINITY;
-    if (e0 + j < E) {
-      const float v = load_logit(row + e0 + j);
-      l[j] = v == v ? v : -INFINITY;
-    }
-  }
-  // softmax: the maximum and the sum; e = 1 at the maximum itself, so an
-  // infinite logit takes the whole weight
+  load_logits<LogitT, V>(l, row, e0, E, vec);
+  // softmax: the maximum, and the sum of the exponentials (1 at the maximum
+  // itself, so an infinite logit takes the whole weight).  Where the largest is
+  // always among the chosen and the weights are renormalised, the sum cancels.
   float m = -INFINITY, den = 1.f;
+  const bool need_sum = !a.sigmoid && (biased || sums || !a.renorm);
   if (!a.sigmoid) {
 #pragma unroll
     for (int j = 0; j < V; ++j) m = fmaxf(m, l[j]);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
   }
-  // s: the score, for softmax before the division by the sum
+  auto score = [&](float x) -> float {   // for softmax before the division by the sum
+    if (x == -INFINITY) return 0.f;
+    if (a.sigmoid) return sigmoid(x);
+    return x == m ? 1.f : expf(x - m);
+  };
   float s[V];
-  uint32_t key[V];
-  float sum = 0.f;
+  if (need_sum || biased || sums) {
+    float sum = 0.f;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    if (l[j] == -INFINITY) s[j] = 0.f;
-    else if (a.sigmoid) s[j] = sigmoid(l[j]);
-    else s[j] = l[j] == m ? 1.f : expf(l[j] - m);
-    sum += s[j];
-  }
-  if (!a.sigmoid) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    den = fmaxf(sum, 1e-30f);
-  }
-  float gval[V];   // what groups are scored by when two entries are added
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    float c = l[j];
-    gval[j] = l[j] == -INFINITY ? -INFINITY : s[j];
-    if (a.bias != nullptr && l[j] != -INFINITY) {
-      if (!a.sigmoid) s[j] = __fdiv_rn(s[j], den);
-      c = gval[j] = __fadd_rn(s[j], __ldg(a.bias + e0 + j));
+    for (int j = 0; j < V; ++j) {
+      s[j] = score(l[j]);
+      sum += s[j];
     }
-    key[j] = choice_key(c);
-    if (key[j] == 0u) gval[j] = -INFINITY;
-    if (a.top == 1) gval[j] = key_value(key[j]);
+    if (need_sum) {
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      den = fmaxf(sum, 1e-30f);
+    }
   }
-  if (a.bias != nullptr) den = 1.f;
+  // key: what chooses among experts; value: what a group is scored by
+  uint32_t key[V];
+  float value[V];
+  if (biased) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (!a.sigmoid) s[j] = __fdiv_rn(s[j], den);
+      const float c = l[j] == -INFINITY ? -INFINITY : __fadd_rn(s[j], __ldg(a.bias + e0 + j));
+      key[j] = choice_key(c);
+      value[j] = key[j] ? c : -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      key[j] = choice_key(l[j]);
+      value[j] = sums ? (key[j] ? s[j] : -INFINITY) : l[j];
+    }
+  }
 
   if (a.groups > 1) {
     const int size = E / a.groups;
-    float* sv = s_val + warp * E;
+    const int span = size / V;   // lanes of a group, if groups begin and end with lanes
+    const bool aligned = span * V == size && (span & (span - 1)) == 0 && V > 0;
+    uint32_t gk = 0;   // lane g's (aligned: every lane's own) group
+    Best best{-INFINITY, -INFINITY};
+    if (aligned) {
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (e0 + j < E) sv[e0 + j] = gval[j];
-    __syncwarp();
-    float b1 = -INFINITY, b2 = -INFINITY;
-    if (lane < a.groups) {
-      for (int i = 0; i < size; ++i) {
-        const float v = sv[lane * size + i];
-        b2 = fmaxf(b2, fminf(b1, v));
-        b1 = fmaxf(b1, v);
+      for (int j = 0; j < V; ++j) best.add(value[j]);
+      for (int o = 1; o < span; o <<= 1) {
+        const float oa = __shfl_xor_sync(kFull, best.a, o), ob = __shfl_xor_sync(kFull, best.b, o);
+        best.b = fmaxf(fmaxf(best.b, ob), fminf(best.a, oa));
+        best.a = fmaxf(best.a, oa);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (e0 + j < E) reinterpret_cast<float*>(keys)[e0 + j] = value[j];
+      __syncwarp();
+      if (lane < a.groups)
+        for (int i = 0; i < size; ++i) best.add(reinterpret_cast<float*>(keys)[lane * size + i]);
+      __syncwarp();
+    }
+    const bool mine = aligned ? e0 < E : lane < a.groups;
+    if (mine) gk = choice_key(a.top == 2 && best.b > -INFINITY ? __fadd_rn(best.a, best.b) : best.a);
+    if (aligned) {
+      // the lowest lane with the best key is in the lowest such group
+      const int own = lane / span;
+      bool kept = false;
+      for (int i = 0; i < a.keep; ++i) {
+        const uint32_t top = __reduce_max_sync(kFull, gk);
+        if (top == 0u) break;
+        const int g = (__ffs(__ballot_sync(kFull, gk == top)) - 1) / span;
+        if (own == g) {
+          kept = true;
+          gk = 0u;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) key[j] = kept ? key[j] : 0u;
+    } else {
+      uint32_t kept = 0;
+      for (int i = 0; i < a.keep; ++i) {
+        const uint32_t top = __reduce_max_sync(kFull, gk);
+        if (top == 0u) break;
+        const int g = __ffs(__ballot_sync(kFull, gk == top)) - 1;
+        kept |= 1u << g;
+        if (lane == g) gk = 0u;
+      }
+      int g = e0 / size, left = size - (e0 - g * size);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (e0 + j < E && !((kept >> g) & 1u)) key[j] = 0u;
+        if (--left == 0) {
+          left = size;
+          ++g;
+        }
       }
     }
-    uint32_t gk = choice_key(a.top == 2 && b2 > -INFINITY ? __fadd_rn(b1, b2) : b1);
-    if (lane >= a.groups) gk = 0u;
-    uint32_t kept = 0;
-    for (int i = 0; i < a.keep; ++i) {
-      const uint32_t best = __reduce_max_sync(kFull, gk);
-      if (best == 0u) break;
-      const int src = __ffs(__ballot_sync(kFull, gk == best)) - 1;
-      kept |= 1u << src;
-      if (lane == src) gk = 0u;
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (e0 + j < E && !((kept >> ((e0 + j) / size)) & 1u)) key[j] = 0u;
   }
 
   uint32_t lm = 0;
 #pragma unroll
-  for (int j = 0; j < V; ++j) lm = max(lm, key[j]);
-  int id = -1;
-  float w = 0.f;
-  for (int k = 0; k < a.K; ++k) {
-    const uint32_t best = __reduce_max_sync(kFull, lm);
-    if (best == 0u) break;
-    const int src = __ffs(__ballot_sync(kFull, lm == best)) - 1;
-    int jj = 0;
-    float sj = 0.f;
-    if (lane == src) {
-      bool found = false;
-      lm = 0;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if (!found && key[j] == best) {
-          found = true;
-          jj = j;
-          sj = s[j];
-          key[j] = 0u;
-        }
-        lm = max(lm, key[j]);
-      }
-    }
-    const int got = __shfl_sync(kFull, e0 + jj, src);
-    const float gw = __shfl_sync(kFull, sj, src);
-    if (lane == k) {
-      id = got;
-      w = gw;
-    }
+  for (int j = 0; j < V; ++j) {
+    lm = max(lm, key[j]);
+    // the lane's keys as V lanes read them: no bank twice for V <= 32
+    keys[e0 + j] = key[j];
   }
-  w = __fdiv_rn(w, den);
+  __syncwarp();
+  int id = -1;
+  for (int k = 0; k < a.K; ++k) {
+    const uint32_t top = __reduce_max_sync(kFull, lm);
+    if (top == 0u) break;
+    const int src = __ffs(__ballot_sync(kFull, lm == top)) - 1;
+    uint32_t v = lane < V ? keys[src * V + lane] : 0u;
+    const int j = __ffs(__ballot_sync(kFull, v == top)) - 1;
+    if (lane == j) {
+      v = 0u;
+      keys[src * V + j] = 0u;
+    }
+    const uint32_t rest = __reduce_max_sync(kFull, v);
+    if (lane == src) lm = rest;
+    if (lane == k) id = src * V + j;
+    __syncwarp();
+  }
+  float w = 0.f;
+  if (id >= 0) {
+    const float x = logit_value(__ldg(row + id));
+    w = score(x);
+    if (need_sum) w = __fdiv_rn(w, den);
+  }
   if (a.renorm) {
     float tot = w;
 #pragma unroll
@@ -193,23 +261,28 @@ __global__ void router_topk_kernel(const TopkArgs a) {
     const int64_t o = static_cast<int64_t>(t) * a.K + lane;
     if (a.idx64) static_cast<int64_t*>(a.idx)[o] = id;
     else static_cast<int32_t*>(a.idx)[o] = id;
-    a.w[o] = id < 0 ? 0.f : w;
+    a.w[o] = w;
   }
+}
+
+template <typename LogitT, int V>
+cudaError_t launch_topk_v(const TopkArgs& a, int sm_count, cudaStream_t s) {
+  const int warps = a.T >= 8 * sm_count ? 8 : a.T >= 2 * sm_count ? 4 : 1;
+  const int grid = (a.T + warps - 1) / warps;
+  constexpr int kBytes = V * static_cast<int>(sizeof(LogitT));
+  const bool vec = a.E % V == 0 && (reinterpret_cast<uintptr_t>(a.logits) & (std::min(kBytes, 16) - 1)) == 0;
+  router_topk_kernel<LogitT, V><<<grid, warps * 32, warps * 32 * V * 4, s>>>(a, vec);
+  return cudaGetLastError();
 }
 
 template <typename LogitT>
 cudaError_t launch_topk(const TopkArgs& a, int sm_count, cudaStream_t s) {
-  const int warps = a.T >= 8 * sm_count ? 8 : a.T >= 2 * sm_count ? 4 : 1;
-  const int grid = (a.T + warps - 1) / warps;
-  const size_t smem = a.groups > 1 ? static_cast<size_t>(warps) * a.E * sizeof(float) : 0;
-  auto kernel = a.E <= 32    ? router_topk_kernel<LogitT, 1>
-                : a.E <= 64  ? router_topk_kernel<LogitT, 2>
-                : a.E <= 128 ? router_topk_kernel<LogitT, 4>
-                : a.E <= 256 ? router_topk_kernel<LogitT, 8>
-                : a.E <= 512 ? router_topk_kernel<LogitT, 16>
-                             : router_topk_kernel<LogitT, 32>;
-  kernel<<<grid, warps * 32, smem, s>>>(a);   // at most 8 * 1024 * 4 bytes: 32 KB
-  return cudaGetLastError();
+  return a.E <= 32    ? launch_topk_v<LogitT, 1>(a, sm_count, s)
+         : a.E <= 64  ? launch_topk_v<LogitT, 2>(a, sm_count, s)
+         : a.E <= 128 ? launch_topk_v<LogitT, 4>(a, sm_count, s)
+         : a.E <= 256 ? launch_topk_v<LogitT, 8>(a, sm_count, s)
+         : a.E <= 512 ? launch_topk_v<LogitT, 16>(a, sm_count, s)
+                      : launch_topk_v<LogitT, 32>(a, sm_count, s);
 }
 
 }  // namespace

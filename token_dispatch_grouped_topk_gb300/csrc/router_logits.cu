@@ -2,16 +2,23 @@
 // and weights, products and sums in fp32 on the tensor cores, fp32 logits (a
 // logit rounded to BF16 would tie experts that the choice has to tell apart).
 //
-// A CTA computes one tile of 128 tokens x BN experts over a part of H:
+// A CTA computes one tile of 128 tokens x BN experts:
 //  - one thread streams x and w with TMA (64 elements = one 128-byte swizzle
 //    row per K block) through a ring of stages, one thread issues
-//    tcgen05.mma kind::f16 into a BN-column TMEM accumulator;
+//    tcgen05.mma kind::f16 into TMEM;
+//  - the tensor core truncates its fp32 sums, an error that grows with the
+//    number of steps (8e-6 relative over H = 7168 in one accumulator), so every
+//    512 elements of H go to the other of two accumulators while eight warps
+//    add the finished one to fp32 registers: 5e-7;
 //  - rows past T and experts past E are TMA's zero fill; they cost no traffic
-//    and are never stored;
-//  - with few tokens one tile per SM is far from filling the GPU, so H is split
-//    over the CTAs of a cluster (up to 8) and the partial tiles are summed
-//    through distributed shared memory, each CTA summing its share of the rows
-//    in rank order: one launch, no workspace, the same bits on every run.
+//    and are never stored.
+// With few tokens one tile per SM is far from filling the GPU, so H is split
+// over the CTAs of a cluster (up to 8) and the partial tiles are summed through
+// distributed shared memory, each CTA summing its share of the rows in rank
+// order: one launch, no workspace, the same bits on every run.
+// With many tokens the tiles of two neighbouring CTAs share w: each fetches half
+// of it and multicasts it to both, so L2 is read once per pair (x and w for a
+// 128 x 256 tile are 48 KB a step, of which w is two thirds).
 // Every wait is bounded.  One that runs out makes the whole tile NaN, which the
 // choice of experts masks, and raises MOE_DEV_TIMEOUT where a status is given.
 #include <algorithm>
@@ -28,8 +35,11 @@ constexpr int kBK = 64;             // BF16 elements of one 128-byte swizzle row
 constexpr int kABytes = kBM * 128;
 constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 8;
-constexpr int kLogitThreads = 128;
+constexpr int kEpiWarp0 = 4;
+constexpr int kEpiWarps = 8;
+constexpr int kLogitThreads = (kEpiWarp0 + kEpiWarps) * 32;
 constexpr int kRingBytes = 200 * 1024;
+constexpr int kPromote = 8;   // K blocks summed in TMEM before they join the registers
 
 struct LogitArgs {
   float* out;
@@ -37,22 +47,23 @@ struct LogitArgs {
   int T, H, E;
   int bn, nt;      // experts per tile (a multiple of 16), tiles along E
   int stages;
-  int split;       // cluster size: parts of H
-  int tmem_cols;
+  int split;       // parts of H, one per CTA of a cluster
+  int acc_cols;    // TMEM columns of one accumulator
   int vec;         // 16-byte stores are possible
 };
 
 struct LogitControl {
   uint64_t full[kMaxStages];
   uint64_t empty[kMaxStages];
-  uint64_t done;
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t drain;
   uint32_t tmem_base;
   int abort;
 };
 
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::
-                   : "memory");
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ float4 ld_cluster(uint32_t saddr, uint32_t rank) {
   float4 v;
@@ -64,7 +75,28 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t saddr, uint32_t rank) {
       : "memory");
   return v;
 }
+// 2D tiled load of one box into the same place of both CTAs of the cluster,
+// counted in bytes on the same barrier of each.
+__device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
+                                                 int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".multicast::cluster [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// Arrive on `bar` of both CTAs when every MMA issued so far by this thread completes.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::
+          "r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
 
+// kPair: clusters of two tiles along the tokens that share w (and split = 1);
+// else clusters of `split` parts of H of one tile.
+template <bool kPair>
 __global__ void __launch_bounds__(kLogitThreads, 1)
     router_logits_kernel(const __grid_constant__ CUtensorMap map_x,
                          const __grid_constant__ CUtensorMap map_w, const LogitArgs a) {
@@ -74,33 +106,49 @@ __global__ void __launch_bounds__(kLogitThreads, 1)
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stage_bytes = kABytes + a.bn * 128;
-  const int rank = blockIdx.x % a.split;
-  const int tile = blockIdx.x / a.split;
-  const int m0 = tile / a.nt * kBM, n0 = tile % a.nt * a.bn;
+  const int group = kPair ? 2 : a.split;
+  const int rank = blockIdx.x % group;
+  const int tile = blockIdx.x / group;
+  const int m0 = (kPair ? tile / a.nt * 2 + rank : tile / a.nt) * kBM, n0 = tile % a.nt * a.bn;
   const int nkb = a.H / kBK;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * rank / a.split);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / a.split);
+  const int kb0 = kPair ? 0 : static_cast<int>(static_cast<int64_t>(nkb) * rank / a.split);
+  const int kb1 = kPair ? nkb : static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / a.split);
+  const int n_kb = kb1 - kb0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(&ctl.full[i], 1);
-      mbar_init(&ctl.empty[i], 1);
+      mbar_init(&ctl.empty[i], kPair ? 2 : 1);
     }
-    mbar_init(&ctl.done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.tfull[i], 1);
+      mbar_init(&ctl.tempty[i], kEpiWarps);
+    }
+    mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
     fence_barrier_init();
     tma_prefetch_desc(&map_x);
     tma_prefetch_desc(&map_w);
   }
   if (warp == 2) {
-    tmem_alloc(&ctl.tmem_base, a.tmem_cols);
+    tmem_alloc(&ctl.tmem_base, 2 * a.acc_cols);
     tmem_relinquish();
     tc_fence_before();
   }
-  __syncthreads();
+  __syncwarp();
+  if (kPair) cluster_sync();   // the other CTA copies into this one and signals its barriers
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
   volatile int* abort_flag = &ctl.abort;
+
+  // accumulators of one epilogue thread: its row's columns [c0, c0 + 16 * n16)
+  float acc[8][16];
+  const int half16 = (a.bn / 16 + 1) / 2;
+  const int ch = (warp - kEpiWarp0) >> 2;                      // half of the columns
+  const int c0 = ch ? half16 * 16 : 0;
+  const int n16 = ch ? a.bn / 16 - half16 : half16;
+  const int lq = warp & 3;                                     // TMEM lane quarter
 
   if (warp == 0) {
     if (lane == 0) {
@@ -114,7 +162,12 @@ __global__ void __launch_bounds__(kLogitThreads, 1)
         uint8_t* sa = smem + st * stage_bytes;
         mbar_arrive_expect_tx(&ctl.full[st], stage_bytes);
         tma_load_2d(sa, &map_x, &ctl.full[st], kb * kBK, m0);
-        tma_load_2d(sa + kABytes, &map_w, &ctl.full[st], kb * kBK, n0);
+        if (kPair) {
+          const int rows = a.bn / 2;
+          tma_load_2d_pair(sa + kABytes + rank * rows * 128, &map_w, &ctl.full[st], kb * kBK, n0 + rank * rows);
+        } else {
+          tma_load_2d(sa + kABytes, &map_w, &ctl.full[st], kb * kBK, n0);
+        }
         ++issued;
       }
       // the ring is reused below and the block may exit: no copy in flight
@@ -122,14 +175,18 @@ __global__ void __launch_bounds__(kLogitThreads, 1)
         const int n = issued - 1 - i;
         int none = 0;
         if (!mbar_wait(&ctl.full[n % a.stages], (n / a.stages) & 1, &none)) *abort_flag = 1;
+        // nor a signal of the other CTA's on its way to this one's barriers
+        if (kPair && !mbar_wait(&ctl.empty[n % a.stages], (n / a.stages) & 1, abort_flag)) *abort_flag = 1;
       }
     }
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16_f32(kBM, a.bn);
-      for (int i = 0; i < kb1 - kb0; ++i) {
-        const int st = i % a.stages;
-        if (!mbar_wait(&ctl.full[st], (i / a.stages) & 1, abort_flag)) {
+      for (int i = 0; i < n_kb; ++i) {
+        const int st = i % a.stages, chunk = i / kPromote, buf = chunk & 1;
+        const bool first = i % kPromote == 0;
+        if ((first && !mbar_wait(&ctl.tempty[buf], ((chunk >> 1) & 1) ^ 1, abort_flag)) ||
+            !mbar_wait(&ctl.full[st], (i / a.stages) & 1, abort_flag)) {
           *abort_flag = 1;
           break;
         }
@@ -139,53 +196,74 @@ __global__ void __launch_bounds__(kLogitThreads, 1)
         const uint64_t bd = smem_desc_kmajor_sw128(sa + kABytes);
 #pragma unroll
         for (int k = 0; k < kBK / 16; ++k)   // 16 BF16 = 32 bytes = 2 descriptor units
-          mma_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc, (i > 0 || k > 0) ? 1u : 0u);
-        mma_commit(&ctl.empty[st]);
+          mma_bf16(tmem + buf * a.acc_cols, ad + 2 * k, bd + 2 * k, idesc, (!first || k > 0) ? 1u : 0u);
+        if (kPair) mma_commit_pair(&ctl.empty[st]);
+        else mma_commit(&ctl.empty[st]);
+        if (i + 1 == n_kb || (i + 1) % kPromote == 0) mma_commit(&ctl.tfull[buf]);
       }
-      // completes when every MMA issued above has
-      mma_commit(&ctl.done);
+      mma_commit(&ctl.drain);
       int none = 0;
-      if (!mbar_wait(&ctl.done, 0, &none)) *abort_flag = 1;
+      if (!mbar_wait(&ctl.drain, 0, &none)) *abort_flag = 1;
     }
+  } else if (warp >= kEpiWarp0) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) acc[c][j] = 0.f;
+    const int chunks = (n_kb + kPromote - 1) / kPromote;
+    bool ok = true;
+    for (int i = 0; i < chunks && ok; ++i) {
+      const int buf = i & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl.tfull[buf], (i >> 1) & 1, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t base = tmem + buf * a.acc_cols + c0 + (static_cast<uint32_t>(lq * 32) << 16);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        if (c < n16) {   // the same for the warp
+          uint32_t r[16];
+          tmem_load16_sync(base + c * 16, r);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[c][j] += __uint_as_float(r[j]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.tempty[buf]);
+    }
+    if (!ok) *abort_flag = 1;
   }
   __syncwarp();
   __syncthreads();
-  tc_fence_after();
   const bool ok = ctl.abort == 0;
-
-  // The tile (or its part) from TMEM to shared memory: thread = row, rows
-  // padded by 16 bytes so that eight rows' 16-byte stores hit all banks.
-  float* part = reinterpret_cast<float*>(smem);
-  const int pitch = a.bn + 4;
-  {
-    const int row = warp * 32 + lane;
-    const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    float4* dst = reinterpret_cast<float4*>(part + row * pitch);
-    for (int c = 0; c < a.bn; c += 16) {
-      uint32_t r[16];
-      if (ok) {
-        tmem_load16_sync(t_lane + c, r);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) r[j] = 0x7fffffffu;   // NaN
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        dst[c / 4 + j] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
-                                     __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
-    }
-  }
-  tc_fence_before();
-  if (a.split > 1) cluster_sync();
-  else __syncthreads();
-  __syncwarp();
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tmem, a.tmem_cols);
+    tmem_dealloc(tmem, 2 * a.acc_cols);
   }
 
+  // The tile (or its part) to shared memory: thread = row and half the columns,
+  // rows padded by 16 bytes so that eight rows' 16-byte stores hit all banks.
+  float* part = reinterpret_cast<float*>(smem);
+  const int pitch = a.bn + 4;
+  if (warp >= kEpiWarp0) {
+    float4* dst = reinterpret_cast<float4*>(part + (lq * 32 + lane) * pitch + c0);
+    const float nan = __uint_as_float(0x7fffffffu);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < n16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          dst[c * 4 + j] = ok ? make_float4(acc[c][4 * j], acc[c][4 * j + 1], acc[c][4 * j + 2], acc[c][4 * j + 3])
+                              : make_float4(nan, nan, nan, nan);
+      }
+  }
+  __syncwarp();
+  const bool summed = !kPair && a.split > 1;
+  if (summed) cluster_sync();
+  else __syncthreads();
+
   // This CTA's share of the rows, summed over the parts of H in rank order.
-  const int rows = kBM / a.split, r0 = rank * rows;
+  const int rows = summed ? kBM / a.split : kBM, r0 = summed ? rank * rows : 0;
   const int nv = a.bn / 4;
   const uint32_t part_addr = smem_u32(part);
   for (int i = threadIdx.x; i < rows * nv; i += kLogitThreads) {
@@ -194,7 +272,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1)
     if (t >= a.T || e >= a.E) continue;
     const int off = r * pitch + c;
     float4 v;
-    if (a.split > 1) {
+    if (summed) {
       v = ld_cluster(part_addr + off * 4, 0);
       for (int p = 1; p < a.split; ++p) {
         const float4 u = ld_cluster(part_addr + off * 4, p);
@@ -213,8 +291,29 @@ __global__ void __launch_bounds__(kLogitThreads, 1)
       if (e + 3 < a.E) o[3] = v.w;
     }
   }
-  if (a.split > 1) cluster_sync();   // the others may still read this part
+  __syncwarp();
+  // the others may still read this part, or signal this CTA's barriers
+  if (kPair || summed) cluster_sync();
   if (threadIdx.x == 0 && !ok && a.dev_status != nullptr) atomicOr(a.dev_status, kDevTimeout);
+}
+
+template <bool kPair>
+cudaError_t launch_logits(const CUtensorMap& mx, const CUtensorMap& mw, const LogitArgs& a,
+                          unsigned grid, unsigned cluster, cudaStream_t s) {
+  cudaError_t err = cudaFuncSetAttribute(router_logits_kernel<kPair>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kRingBytes);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kLogitThreads);
+  cfg.dynamicSmemBytes = 1024 + a.stages * (kABytes + a.bn * 128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {cluster, 1, 1};
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, router_logits_kernel<kPair>, mx, mw, a);
 }
 
 }  // namespace
@@ -237,31 +336,18 @@ cudaError_t launch_router_logits(const void* x, const void* w, int T, int H, int
   while (mt * a.nt * a.split * 2 <= sm_count && (E + a.nt - 1) / a.nt > 32) a.nt *= 2;
   a.bn = ((E + a.nt - 1) / a.nt + 15) / 16 * 16;
   a.nt = (E + a.bn - 1) / a.bn;
-  a.tmem_cols = 32;
-  while (a.tmem_cols < a.bn) a.tmem_cols *= 2;
-  const int stage_bytes = kABytes + a.bn * 128;
-  a.stages = std::min(kMaxStages, kRingBytes / stage_bytes);
+  const bool pair = a.split == 1 && mt > 1;
+  a.acc_cols = 32;
+  while (a.acc_cols < a.bn) a.acc_cols *= 2;
+  a.stages = std::min(kMaxStages, kRingBytes / (kABytes + a.bn * 128));
   a.vec = E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15u) == 0;
   CUtensorMap mx, mw;
   cudaError_t err = make_map_rows128(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, H, T, kBM);
   if (err == cudaSuccess)
-    err = make_map_rows128(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w, H, E, a.bn);
+    err = make_map_rows128(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w, H, E, pair ? a.bn / 2 : a.bn);
   if (err != cudaSuccess) return err;
-  const int smem = 1024 + a.stages * stage_bytes;
-  err = cudaFuncSetAttribute(router_logits_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             1024 + kRingBytes);
-  if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(mt * a.nt * a.split));
-  cfg.blockDim = dim3(kLogitThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim = {static_cast<unsigned>(a.split), 1, 1};
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, router_logits_kernel, mx, mw, a);
+  if (pair) return launch_logits<true>(mx, mw, a, static_cast<unsigned>((mt + 1) / 2 * 2 * a.nt), 2, s);
+  return launch_logits<false>(mx, mw, a, static_cast<unsigned>(mt * a.nt * a.split), a.split, s);
 }
 
 }  // namespace moe
