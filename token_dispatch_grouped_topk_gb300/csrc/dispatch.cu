@@ -28,6 +28,7 @@ namespace {
 struct RouteLane {
   int t, k, e;  // e = expert id, or -1 for padding / invalid id / idle lane
   bool active;  // the lane maps to a real route (t < T)
+  bool bad;     // its id is outside [-1, E)
 };
 
 // Router ids are int64 or int32 (IdT); -1 marks a padding route.
@@ -40,27 +41,48 @@ __device__ __forceinline__ RouteLane load_route(const IdT* __restrict__ topk_idx
   r.k = lane % K;
   r.active = (lane < tpw * K) && (r.t < T);
   r.e = -1;
+  r.bad = false;
   if (r.active) {
     const int64_t id = static_cast<int64_t>(topk_idx[static_cast<int64_t>(r.t) * K + r.k]);
     if (id >= 0 && id < E) {
       r.e = static_cast<int>(id);
-    } else if (id != -1 && dev_status != nullptr) {
-      atomicOr(dev_status, kDevBadExpertId);
+    } else if (id != -1) {
+      r.bad = true;
+      if (dev_status != nullptr) atomicOr(dev_status, kDevBadExpertId);
     }
   }
   return r;
 }
 
-template <typename IdT>
+// A kernel of a chain of dependent launches (the e4m3 dispatch): the next may
+// start, and this one has to wait for the one before; both do nothing in an
+// ordinary launch.
+__device__ __forceinline__ void chain_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void chain_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// kOwn: the launch resets the status words itself, and passes a bad id on as
+// bit 30 of the block's count for expert 0, which the scan takes off.
+constexpr int kBadBit = 1 << 30;
+
+template <typename IdT, bool kOwn = false>
 __global__ void __launch_bounds__(kDispatchWarps * 32)
     route_hist_kernel(const IdT* __restrict__ topk_idx, int T, int K, int E, int nblocks,
                       int32_t* __restrict__ hist, int32_t* dev_status) {
   extern __shared__ int s_hist[];  // [E]
+  if (kOwn) chain_start();
   for (int e = threadIdx.x; e < E; e += blockDim.x) s_hist[e] = 0;
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const RouteLane r =
-      load_route(topk_idx, T, K, E, blockIdx.x * kDispatchWarps + warp, lane, dev_status);
+  const RouteLane r = load_route(topk_idx, T, K, E, blockIdx.x * kDispatchWarps + warp, lane,
+                                 kOwn ? nullptr : dev_status);
+  if (kOwn) {
+    if (blockIdx.x == 0 && threadIdx.x < 2) dev_status[threadIdx.x] = 0;
+    if (r.bad) atomicOr(&s_hist[0], kBadBit);
+  }
   const unsigned peers = __match_any_sync(0xffffffffu, r.e);
   if (r.e >= 0 && lane == __ffs(peers) - 1) atomicAdd(&s_hist[r.e], __popc(peers));
   __syncthreads();
@@ -70,15 +92,27 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
 
 constexpr int kScanThreads = 512;
 
+template <bool kOwn = false>
 __global__ void __launch_bounds__(kScanThreads)
     route_scan_kernel(int32_t* __restrict__ hist, int nblocks, int R, int32_t* __restrict__ counts,
                       int32_t* dev_status) {
   __shared__ int s_warp[kScanThreads / 32];
+  if (kOwn) {
+    chain_start();
+    chain_wait();
+  }
   const int e = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int32_t* h = hist + static_cast<size_t>(e) * nblocks;
   const int per = (nblocks + kScanThreads - 1) / kScanThreads;
   const int b0 = threadIdx.x * per;
+  if (kOwn && e == 0) {
+    for (int i = 0; i < per; ++i)
+      if (b0 + i < nblocks && (h[b0 + i] & kBadBit)) {
+        h[b0 + i] &= ~kBadBit;
+        atomicOr(dev_status, kDevBadExpertId);
+      }
+  }
   int local = 0;
   for (int i = 0; i < per; ++i)
     if (b0 + i < nblocks) local += h[b0 + i];
@@ -448,7 +482,11 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
 // norm's 8-bit output): slots, counts and source map of route_scatter_kernel;
 // each token's codes and scales are read once and written to every kept row.
 // A block takes whole 128-groups of its tokens' rows (eight 16-byte vectors
-// of codes and one scale each).
+// of codes and one scale each), U vectors per lane and token (1, 2, 4 or 8).
+// What a row holds does not depend on where it goes, so a warp's first eight
+// vectors and its first scales are requested before the block finds its routes'
+// slots, which takes longer than the loads; further tokens follow eight vectors
+// at a time.
 template <typename IdT, bool kSingle>
 __global__ void __launch_bounds__(kDispatchWarps * 32)
     route_scatter_codes_kernel(const uint4* __restrict__ tq, const float* __restrict__ ts,
@@ -456,21 +494,41 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
                                RowLayout rl, int nblocks, const int32_t* __restrict__ base,
                                int32_t* __restrict__ counts, uint4* __restrict__ xq,
                                float* __restrict__ xs, int32_t* __restrict__ src_map,
-                               int32_t* dev_status, int groups_per_slice) {
+                               int32_t* dev_status, int groups_per_slice, int log_u) {
   extern __shared__ int smem[];
   int* s_cnt = smem;                           // [kDispatchWarps][E]
   int* s_dest = smem + kDispatchWarps * E;     // [kDispatchWarps][32]
   int* s_rows = s_dest + kDispatchWarps * 32;  // [E + 1] packed row bases
   int* s_prev = s_rows + E + 1;                // single pass: [E]
   int* s_tot = s_prev + E;                     //              [E]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gw = blockIdx.x * kDispatchWarps + warp;
+  const int tpw = 32 / K, t0 = gw * tpw;
+  const int G = H / kGroup, nvec = H / 16;
+  const int g0 = blockIdx.y * groups_per_slice, ng = min(G - g0, groups_per_slice);
+  const int v0 = g0 * 8, nv = ng * 8;
+  const int tokens = max(0, min(tpw, T - t0));      // of this warp
+  const int batch = 8 >> log_u;                     // tokens of eight vectors per lane
+  uint4 c[8];
+  auto load = [&](int tt0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int tt = tt0 + (i >> log_u), v = lane + 32 * (i & ((1 << log_u) - 1));
+      if (tt < tokens && v < nv) c[i] = ld_stream(tq + static_cast<size_t>(t0 + tt) * nvec + v0 + v);
+    }
+  };
+  load(0);
+  // scales: lane i takes (token, group) pairs i, i + 32, ...
+  float sc = 0.f;
+  if (lane < tokens * ng) sc = __ldg(ts + static_cast<size_t>(t0 + lane / ng) * G + g0 + lane % ng);
+
   for (int i = threadIdx.x; i < kDispatchWarps * E; i += blockDim.x) s_cnt[i] = 0;
+  if (!kSingle) chain_wait();
   if (kSingle)
     single_pass_bases(topk_idx, T, K, E, rl, s_prev, s_tot, s_rows, counts, dev_status);
   else if (rl.packed)
     expert_prefix(counts, E, rl.R, 1, 1, s_rows, nullptr);
   __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gw = blockIdx.x * kDispatchWarps + warp;
   const RouteLane r = load_route(topk_idx, T, K, E, gw, lane, nullptr);
   const unsigned peers = __match_any_sync(0xffffffffu, r.e);
   const int lane_rank = __popc(peers & ((1u << lane) - 1u));
@@ -487,40 +545,27 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
   s_dest[warp * 32 + lane] = q;
   __syncwarp();
 
-  const int tpw = 32 / K;
-  const int G = H / kGroup, nvec = H / 16;
-  const int g0 = blockIdx.y * groups_per_slice;
-  const int g1 = min(G, g0 + groups_per_slice);
-  const int v0 = g0 * 8, v1 = g1 * 8;
   const int* wdest = s_dest + warp * 32;
-  for (int tt = 0; tt < tpw; ++tt) {
-    const int t = gw * tpw + tt;
-    if (t >= T) break;
-    const int* dq = wdest + tt * K;
-    bool any = false;
-    for (int k = 0; k < K; ++k) any |= dq[k] >= 0;
-    if (!any) continue;
-    const uint4* src = tq + static_cast<size_t>(t) * nvec;
-    for (int v = v0 + lane; v < v1; v += 32 * 8) {
-      uint4 c[8];
+  for (int tt0 = 0; tt0 < tokens; tt0 += batch) {
+    if (tt0 > 0) load(tt0);
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (v + 32 * u < v1) c[u] = ld_stream(src + v + 32 * u);
+    for (int i = 0; i < 8; ++i) {
+      const int tt = tt0 + (i >> log_u), v = lane + 32 * (i & ((1 << log_u) - 1));
+      if (tt >= tokens || v >= nv) continue;
+      const int* dq = wdest + tt * K;
       for (int k = 0; k < K; ++k) {
         const int qq = dq[k];
-        if (qq < 0) continue;
-        uint4* dst = xq + static_cast<size_t>(qq) * nvec;
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          if (v + 32 * u < v1) dst[v + 32 * u] = c[u];
+        if (qq >= 0) xq[static_cast<size_t>(qq) * nvec + v0 + v] = c[i];
       }
     }
-    for (int g = g0 + lane; g < g1; g += 32) {
-      const float sc = __ldg(ts + static_cast<size_t>(t) * G + g);
-      for (int k = 0; k < K; ++k) {
-        const int qq = dq[k];
-        if (qq >= 0) xs[static_cast<size_t>(qq) * G + g] = sc;
-      }
+  }
+  for (int i = lane; i < tokens * ng; i += 32) {
+    const int tt = i / ng, g = i - tt * ng;
+    if (i >= 32) sc = __ldg(ts + static_cast<size_t>(t0 + tt) * G + g0 + g);
+    const int* dq = wdest + tt * K;
+    for (int k = 0; k < K; ++k) {
+      const int qq = dq[k];
+      if (qq >= 0) xs[static_cast<size_t>(qq) * G + g0 + g] = sc;
     }
   }
 }
@@ -759,7 +804,7 @@ cudaError_t dispatch_impl(const void* x, const IdT* topk_idx, int T, int H, int 
           topk_idx, T, K, E, nblocks, hist, dev_status);
       if ((err = cudaGetLastError()) != cudaSuccess) return err;
     }
-    route_scan_kernel<<<E, kScanThreads, 0, s>>>(hist, nblocks, R, counts, dev_status);
+    route_scan_kernel<><<<E, kScanThreads, 0, s>>>(hist, nblocks, R, counts, dev_status);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
     if (nblocks == 0) return cudaSuccess;
   }
@@ -861,7 +906,7 @@ cudaError_t dispatch_quant_impl(const void* x, const IdT* topk_idx, int T, int H
           topk_idx, T, K, E, nblocks, hist, dev_status);
       if ((err = cudaGetLastError()) != cudaSuccess) return err;
     }
-    route_scan_kernel<<<E, kScanThreads, 0, s>>>(hist, nblocks, rl.R, counts, dev_status);
+    route_scan_kernel<><<<E, kScanThreads, 0, s>>>(hist, nblocks, rl.R, counts, dev_status);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
     if (nblocks == 0) return cudaSuccess;
   }
@@ -904,6 +949,23 @@ cudaError_t launch_dispatch_quant(const void* x, const void* topk_idx, int idx_b
 }
 
 namespace {
+// A launch that may start while the one before in the stream still runs.
+template <typename... Params, typename... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                           cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 template <typename IdT>
 cudaError_t dispatch_fp8_impl(const uint8_t* tq, const float* ts, const IdT* topk_idx, int T,
                               int H, int K, int E, RowLayout rl, uint8_t* xq, float* xs,
@@ -912,29 +974,35 @@ cudaError_t dispatch_fp8_impl(const uint8_t* tq, const float* ts, const IdT* top
   const int nblocks = dispatch_blocks(T, K);
   const bool one = single_pass(T, K);
   cudaError_t err;
-  if (!one) {
-    err = cudaMemsetAsync(dev_status, 0, 2 * sizeof(int32_t), s);
-    if (err != cudaSuccess) return err;
-    if (nblocks > 0) {
-      route_hist_kernel<IdT><<<nblocks, kDispatchWarps * 32, E * sizeof(int), s>>>(
-          topk_idx, T, K, E, nblocks, hist, dev_status);
-      if ((err = cudaGetLastError()) != cudaSuccess) return err;
-    }
-    route_scan_kernel<<<E, kScanThreads, 0, s>>>(hist, nblocks, rl.R, counts, dev_status);
-    if ((err = cudaGetLastError()) != cudaSuccess) return err;
-    if (nblocks == 0) return cudaSuccess;
+  if (nblocks == 0) {   // no tokens: counts and status
+    if ((err = cudaMemsetAsync(dev_status, 0, 2 * sizeof(int32_t), s)) != cudaSuccess) return err;
+    return cudaMemsetAsync(counts, 0, E * sizeof(int32_t), s);
   }
-  // slices of four or more whole 128-groups (one 16-byte vector per lane)
+  if (!one) {
+    route_hist_kernel<IdT, true><<<nblocks, kDispatchWarps * 32, E * sizeof(int), s>>>(
+        topk_idx, T, K, E, nblocks, hist, dev_status);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    err = launch_chained(route_scan_kernel<true>, dim3(E), kScanThreads, 0, s, hist, nblocks, rl.R,
+                         counts, dev_status);
+    if (err != cudaSuccess) return err;
+  }
+  // slices of four (one 16-byte vector per lane) to 32 whole 128-groups
   const int G = H / kGroup;
-  int hsplit = row_slices(nblocks, G, 4, sm_count);
+  int hsplit = max(row_slices(nblocks, G, 4, sm_count), (G + 31) / 32);
   const int gps = (G + hsplit - 1) / hsplit;
   hsplit = (G + gps - 1) / gps;
+  const int log_u = gps <= 4 ? 0 : gps <= 8 ? 1 : gps <= 16 ? 2 : 3;
   const size_t smem = (kDispatchWarps * E + kDispatchWarps * 32 + 3 * E + 1) * sizeof(int);
   auto kernel = one ? route_scatter_codes_kernel<IdT, true> : route_scatter_codes_kernel<IdT, false>;
   if ((err = allow_smem(kernel, smem)) != cudaSuccess) return err;
-  kernel<<<dim3(nblocks, hsplit), kDispatchWarps * 32, smem, s>>>(
-      reinterpret_cast<const uint4*>(tq), ts, topk_idx, T, H, K, E, rl, nblocks, hist, counts,
-      reinterpret_cast<uint4*>(xq), xs, src_map, dev_status, gps);
+  const dim3 grid(nblocks, hsplit);
+  const auto* q4 = reinterpret_cast<const uint4*>(tq);
+  auto* x4 = reinterpret_cast<uint4*>(xq);
+  if (!one)
+    return launch_chained(kernel, grid, kDispatchWarps * 32, smem, s, q4, ts, topk_idx, T, H, K, E, rl,
+                          nblocks, hist, counts, x4, xs, src_map, dev_status, gps, log_u);
+  kernel<<<grid, kDispatchWarps * 32, smem, s>>>(q4, ts, topk_idx, T, H, K, E, rl, nblocks, hist, counts,
+                                                 x4, xs, src_map, dev_status, gps, log_u);
   return cudaGetLastError();
 }
 }  // namespace

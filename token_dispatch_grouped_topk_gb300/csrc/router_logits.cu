@@ -16,9 +16,11 @@
 // over the CTAs of a cluster (up to 8) and the partial tiles are summed through
 // distributed shared memory, each CTA summing its share of the rows in rank
 // order: one launch, no workspace, the same bits on every run.
-// With many tokens the tiles of two neighbouring CTAs share w: each fetches half
-// of it and multicasts it to both, so L2 is read once per pair (x and w for a
-// 128 x 256 tile are 48 KB a step, of which w is two thirds).
+// With many tokens two CTAs compute a 256-token tile together (cta_group::2):
+// each holds its own 128 rows of x and half of w, so a step of 64 brings 32 KB
+// into an SM instead of 48.  An SM takes in about 64 bytes a clock and the
+// products of a step last 540 clocks, so 48 KB bound the kernel (the same with w
+// multicast to both CTAs, which spares L2 but not the SM's intake: 67 us).
 // Every wait is bounded.  One that runs out makes the whole tile NaN, which the
 // choice of experts masks, and raises MOE_DEV_TIMEOUT where a status is given.
 #include <algorithm>
@@ -75,27 +77,54 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t saddr, uint32_t rank) {
       : "memory");
   return v;
 }
-// 2D tiled load of one box into the same place of both CTAs of the cluster,
-// counted in bytes on the same barrier of each.
-__device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
+// This CTA's shared address `saddr` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_cluster(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+// The cta_group::2 forms of the pair: a load counted on the leader's barrier,
+// TMEM columns of both CTAs, products of both, arrivals on both.
+__device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorMap* map, uint32_t leader_bar,
                                                  int x, int y) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".multicast::cluster [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y),
-      "h"(static_cast<uint16_t>(3))
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(leader_bar), "r"(x), "r"(y)
       : "memory");
 }
-// Arrive on `bar` of both CTAs when every MMA issued so far by this thread completes.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* smem_dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(smem_dst)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::
           "r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3))
       : "memory");
 }
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 
-// kPair: clusters of two tiles along the tokens that share w (and split = 1);
-// else clusters of `split` parts of H of one tile.
+// kPair: clusters of two CTAs that compute 256 tokens together, rank 0 issuing
+// the products (and split = 1); else clusters of `split` parts of H of one tile.
 template <bool kPair>
 __global__ void __launch_bounds__(kLogitThreads, 1)
     router_logits_kernel(const __grid_constant__ CUtensorMap map_x,
@@ -105,7 +134,8 @@ __global__ void __launch_bounds__(kLogitThreads, 1)
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stage_bytes = kABytes + a.bn * 128;
+  const int w_rows = kPair ? a.bn / 2 : a.bn;   // rows of w that this CTA holds
+  const int stage_bytes = kABytes + w_rows * 128;
   const int group = kPair ? 2 : a.split;
   const int rank = blockIdx.x % group;
   const int tile = blockIdx.x / group;
@@ -118,11 +148,11 @@ __global__ void __launch_bounds__(kLogitThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(&ctl.full[i], 1);
-      mbar_init(&ctl.empty[i], kPair ? 2 : 1);
+      mbar_init(&ctl.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl.tfull[i], 1);
-      mbar_init(&ctl.tempty[i], kEpiWarps);
+      mbar_init(&ctl.tempty[i], (kPair ? 2 : 1) * kEpiWarps);
     }
     mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
@@ -131,8 +161,12 @@ __global__ void __launch_bounds__(kLogitThreads, 1)
     tma_prefetch_desc(&map_w);
   }
   if (warp == 2) {
-    tmem_alloc(&ctl.tmem_base, 2 * a.acc_cols);
-    tmem_relinquish();
+    if (kPair) {
+      tmem_alloc_pair(&ctl.tmem_base, 2 * a.acc_cols);
+    } else {
+      tmem_alloc(&ctl.tmem_base, 2 * a.acc_cols);
+      tmem_relinquish();
+    }
     tc_fence_before();
   }
   __syncwarp();
@@ -150,58 +184,84 @@ __global__ void __launch_bounds__(kLogitThreads, 1)
   const int n16 = ch ? a.bn / 16 - half16 : half16;
   const int lq = warp & 3;                                     // TMEM lane quarter
 
+  // One thread's walk round the ring, without divisions: they would be a third
+  // of its time per stage.
+  struct Slot {
+    int i;
+    uint32_t phase;
+    __device__ void next(int n) {
+      if (++i == n) {
+        i = 0;
+        phase ^= 1;
+      }
+    }
+  };
   if (warp == 0) {
     if (lane == 0) {
+      Slot st{0, 1};
+      const uint32_t leader = kPair ? map_cluster(smem_u32(&ctl.full[0]), 0) : 0u;
+      const int wy = n0 + (kPair ? rank * w_rows : 0);
       int issued = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const int st = issued % a.stages;
-        if (!mbar_wait(&ctl.empty[st], ((issued / a.stages) & 1) ^ 1, abort_flag)) {
+      for (int kb = kb0; kb < kb1; ++kb, ++issued, st.next(a.stages)) {
+        if (!mbar_wait(&ctl.empty[st.i], st.phase, abort_flag)) {
           *abort_flag = 1;
           break;
         }
-        uint8_t* sa = smem + st * stage_bytes;
-        mbar_arrive_expect_tx(&ctl.full[st], stage_bytes);
-        tma_load_2d(sa, &map_x, &ctl.full[st], kb * kBK, m0);
+        uint8_t* sa = smem + st.i * stage_bytes;
         if (kPair) {
-          const int rows = a.bn / 2;
-          tma_load_2d_pair(sa + kABytes + rank * rows * 128, &map_w, &ctl.full[st], kb * kBK, n0 + rank * rows);
+          // both CTAs' copies count on the leader's barrier
+          if (rank == 0) mbar_arrive_expect_tx(&ctl.full[st.i], 2 * stage_bytes);
+          const uint32_t bar = leader + st.i * 8;
+          tma_load_2d_pair(sa, &map_x, bar, kb * kBK, m0);
+          tma_load_2d_pair(sa + kABytes, &map_w, bar, kb * kBK, wy);
         } else {
-          tma_load_2d(sa + kABytes, &map_w, &ctl.full[st], kb * kBK, n0);
+          mbar_arrive_expect_tx(&ctl.full[st.i], stage_bytes);
+          tma_load_2d(sa, &map_x, &ctl.full[st.i], kb * kBK, m0);
+          tma_load_2d(sa + kABytes, &map_w, &ctl.full[st.i], kb * kBK, wy);
         }
-        ++issued;
       }
-      // the ring is reused below and the block may exit: no copy in flight
+      // the ring is reused below and the block may exit: no copy in flight (of a
+      // pair: none that the products, which free the stages, have not read)
       for (int i = 0; i < min(issued, a.stages); ++i) {
         const int n = issued - 1 - i;
         int none = 0;
-        if (!mbar_wait(&ctl.full[n % a.stages], (n / a.stages) & 1, &none)) *abort_flag = 1;
-        // nor a signal of the other CTA's on its way to this one's barriers
-        if (kPair && !mbar_wait(&ctl.empty[n % a.stages], (n / a.stages) & 1, abort_flag)) *abort_flag = 1;
+        uint64_t* bar = kPair ? &ctl.empty[n % a.stages] : &ctl.full[n % a.stages];
+        if (!mbar_wait(bar, (n / a.stages) & 1, &none)) *abort_flag = 1;
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(kBM, a.bn);
-      for (int i = 0; i < n_kb; ++i) {
-        const int st = i % a.stages, chunk = i / kPromote, buf = chunk & 1;
-        const bool first = i % kPromote == 0;
-        if ((first && !mbar_wait(&ctl.tempty[buf], ((chunk >> 1) & 1) ^ 1, abort_flag)) ||
-            !mbar_wait(&ctl.full[st], (i / a.stages) & 1, abort_flag)) {
+    if (lane == 0 && (!kPair || rank == 0)) {
+      const uint32_t idesc = idesc_bf16_f32(kPair ? 2 * kBM : kBM, a.bn);
+      auto commit = [](uint64_t* bar) {
+        if (kPair) mma_commit_pair(bar);
+        else mma_commit(bar);
+      };
+      const uint64_t ad0 = smem_desc_kmajor_sw128(smem_u32(smem));
+      const uint64_t bd0 = smem_desc_kmajor_sw128(smem_u32(smem) + kABytes);
+      Slot st{0, 0}, tb{0, 1};   // ring stage, accumulator
+      for (int i = 0; i < n_kb; ++i, st.next(a.stages)) {
+        const bool first = i % kPromote == 0, last = i % kPromote == kPromote - 1 || i + 1 == n_kb;
+        if ((first && !mbar_wait(&ctl.tempty[tb.i], tb.phase, abort_flag)) ||
+            !mbar_wait(&ctl.full[st.i], st.phase, abort_flag)) {
           *abort_flag = 1;
           break;
         }
         tc_fence_after();
-        const uint32_t sa = smem_u32(smem + st * stage_bytes);
-        const uint64_t ad = smem_desc_kmajor_sw128(sa);
-        const uint64_t bd = smem_desc_kmajor_sw128(sa + kABytes);
+        const uint64_t step = static_cast<uint64_t>(st.i * stage_bytes) >> 4;   // of the descriptors' address
+        const uint32_t d = tmem + tb.i * a.acc_cols;
 #pragma unroll
-        for (int k = 0; k < kBK / 16; ++k)   // 16 BF16 = 32 bytes = 2 descriptor units
-          mma_bf16(tmem + buf * a.acc_cols, ad + 2 * k, bd + 2 * k, idesc, (!first || k > 0) ? 1u : 0u);
-        if (kPair) mma_commit_pair(&ctl.empty[st]);
-        else mma_commit(&ctl.empty[st]);
-        if (i + 1 == n_kb || (i + 1) % kPromote == 0) mma_commit(&ctl.tfull[buf]);
+        for (int k = 0; k < kBK / 16; ++k) {   // 16 BF16 = 32 bytes = 2 descriptor units
+          const uint32_t more = !first || k > 0 ? 1u : 0u;
+          if (kPair) mma_bf16_pair(d, ad0 + step + 2 * k, bd0 + step + 2 * k, idesc, more);
+          else mma_bf16(d, ad0 + step + 2 * k, bd0 + step + 2 * k, idesc, more);
+        }
+        commit(&ctl.empty[st.i]);
+        if (last) {
+          commit(&ctl.tfull[tb.i]);
+          tb.next(2);
+        }
       }
-      mma_commit(&ctl.drain);
+      commit(&ctl.drain);
       int none = 0;
       if (!mbar_wait(&ctl.drain, 0, &none)) *abort_flag = 1;
     }
@@ -229,7 +289,10 @@ __global__ void __launch_bounds__(kLogitThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.tempty[buf]);
+      if (lane == 0) {
+        if (kPair) mbar_arrive_cluster(map_cluster(smem_u32(&ctl.tempty[buf]), 0));
+        else mbar_arrive(&ctl.tempty[buf]);
+      }
     }
     if (!ok) *abort_flag = 1;
   }
@@ -238,7 +301,8 @@ __global__ void __launch_bounds__(kLogitThreads, 1)
   const bool ok = ctl.abort == 0;
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * a.acc_cols);
+    if (kPair) tmem_dealloc_pair(tmem, 2 * a.acc_cols);
+    else tmem_dealloc(tmem, 2 * a.acc_cols);
   }
 
   // The tile (or its part) to shared memory: thread = row and half the columns,
@@ -273,11 +337,16 @@ __global__ void __launch_bounds__(kLogitThreads, 1)
     const int off = r * pitch + c;
     float4 v;
     if (summed) {
-      v = ld_cluster(part_addr + off * 4, 0);
-      for (int p = 1; p < a.split; ++p) {
-        const float4 u = ld_cluster(part_addr + off * 4, p);
-        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-      }
+      float4 u[kMaxCluster];   // all in flight before the first sum
+#pragma unroll
+      for (int p = 0; p < kMaxCluster; ++p)
+        if (p < a.split) u[p] = ld_cluster(part_addr + off * 4, p);
+      v = u[0];
+#pragma unroll
+      for (int p = 1; p < kMaxCluster; ++p)
+        if (p < a.split) {
+          v.x += u[p].x; v.y += u[p].y; v.z += u[p].z; v.w += u[p].w;
+        }
     } else {
       v = *reinterpret_cast<const float4*>(part + off);
     }
@@ -306,7 +375,8 @@ cudaError_t launch_logits(const CUtensorMap& mx, const CUtensorMap& mw, const Lo
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kLogitThreads);
-  cfg.dynamicSmemBytes = 1024 + a.stages * (kABytes + a.bn * 128);
+  // the ring, which also takes the finished tile
+  cfg.dynamicSmemBytes = 1024 + std::max(a.stages * (kABytes + (kPair ? a.bn / 2 : a.bn) * 128), kBM * (a.bn + 4) * 4);
   cfg.stream = s;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -337,9 +407,13 @@ cudaError_t launch_router_logits(const void* x, const void* w, int T, int H, int
   a.bn = ((E + a.nt - 1) / a.nt + 15) / 16 * 16;
   a.nt = (E + a.bn - 1) / a.bn;
   const bool pair = a.split == 1 && mt > 1;
+  if (pair) {   // products of a pair: experts in steps of 32
+    a.bn = (a.bn + 31) / 32 * 32;
+    a.nt = (E + a.bn - 1) / a.bn;
+  }
   a.acc_cols = 32;
   while (a.acc_cols < a.bn) a.acc_cols *= 2;
-  a.stages = std::min(kMaxStages, kRingBytes / (kABytes + a.bn * 128));
+  a.stages = std::min(kMaxStages, kRingBytes / (kABytes + (pair ? a.bn / 2 : a.bn) * 128));
   a.vec = E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15u) == 0;
   CUtensorMap mx, mw;
   cudaError_t err = make_map_rows128(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, H, T, kBM);
