@@ -5,3 +5,4 @@ behind a small C ABI (``include/moe.h``).  This package is the thin Python
 binding over that library; PyTorch supplies device memory and streams only.
 """
 from .api import *  # noqa: F401,F403
+from .block import RoutedBlock  # noqa: F401

@@ -830,6 +830,19 @@ class MoeLayerBuffers:
                            workspace=self.ws_dispatch, stream=stream,
                            rows=self.rows if self.packed else 0)
 
+    def dispatch_fp8(self, xq, xs, topk_idx, stream=None):
+        """``dispatch_quant`` for rows already in e4m3 (moe_dispatch_fp8):
+        codes ``xq [T, H]`` and scales ``xs [T, H/128]``, as moe_add_rms_norm
+        gives them; ``gemms`` and ``combine`` follow.  Padded and packed
+        layouts."""
+        if self.source_slots:
+            raise ValueError("dispatch_fp8: the padded or packed layout, not per-source slots")
+        oq, os_, _, _ = self.workspace_views()
+        moe_dispatch_fp8(xq, xs, topk_idx, self.E, self.R, xq=oq, xs=os_, counts=self.counts,
+                         src_map=self.src_map, dev_status=self.dev_status,
+                         workspace=self.ws_dispatch, stream=stream,
+                         rows=self.rows if self.packed else 0)
+
     def gemms(self, w13, w13_scale, w2, w2_scale, stream=None, max_ctas=0):
         """Both GEMMs on the FP8 activations dispatch_quant wrote, in the
         library's launch form for the layer (or ``gemm_launch``)."""
