@@ -360,7 +360,17 @@ struct Product {
   int G, units;        // groups of K, units of a tile
   int row_tiles, nb;   // tiles of a pass, runs
   int64_t all;         // units in all
-  __device__ int64_t start(int b) const { return all * b / nb; }
+  // The first unit of run b, and the run of unit u: in 32 bits wherever the
+  // products fit, as 64-bit divisions take about a microsecond of every join.
+  __device__ int64_t start(int b) const {
+    if (all < (1 << 22)) return static_cast<uint32_t>(all) * static_cast<uint32_t>(b) / static_cast<uint32_t>(nb);
+    return all * b / nb;
+  }
+  __device__ int run_of(int64_t u) const {
+    int b = all < (1 << 22) ? static_cast<uint32_t>(u) * static_cast<uint32_t>(nb) / static_cast<uint32_t>(all)
+                            : static_cast<int>(u * nb / all);
+    return start(b + 1) <= u ? b + 1 : b;
+  }
 };
 __device__ __forceinline__ Product product_of(const W4Args& a, bool down, int np) {
   Product p;
@@ -410,8 +420,6 @@ __global__ void __launch_bounds__(kW4Threads, 2)
   const Product prod[2] = {product_of(a, false, np), product_of(a, true, np)};
   const int runs = prod[0].nb + prod[1].nb;
   volatile int* abort_flag = &s_abort;
-  grid_dependency_wait();   // x's operands, the counters, and the readers of old outputs
-
   if (warp == kW4Warps) {
     // ------------------------------------------------------------- producer
     // lane 0 fetches the codes, lane c the operands of column c
@@ -435,7 +443,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
       const int b = down ? run - prod[0].nb : run;
       const int64_t f0 = pr.start(b);
       const int n = static_cast<int>(pr.start(b + 1) - f0);   // units of the run
-      const int tile0 = static_cast<int>(f0 / pr.units), s0 = static_cast<int>(f0 - static_cast<int64_t>(tile0) * pr.units);
+      const int tile0 = static_cast<uint32_t>(f0) / static_cast<uint32_t>(pr.units), s0 = static_cast<int>(f0 - static_cast<int64_t>(tile0) * pr.units);
       const uint8_t* ops = down ? a.zs : a.xs;
       const int64_t op_row = operand_row_bytes(down ? a.I : a.H);
       // Two walks over the run's units: the codes, and the operands, which for
@@ -554,7 +562,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     const int b = down ? run - prod[0].nb : run;
     const int64_t f0 = pr.start(b);
     int left = static_cast<int>(pr.start(b + 1) - f0);
-    int tile = static_cast<int>(f0 / pr.units), s = static_cast<int>(f0 - static_cast<int64_t>(tile) * pr.units);
+    int tile = static_cast<uint32_t>(f0) / static_cast<uint32_t>(pr.units), s = static_cast<int>(f0 - static_cast<int64_t>(tile) * pr.units);
     int t = tile % pr.row_tiles, p = tile / pr.row_tiles;
     const uint16_t* scales = down ? a.s2 : a.s13;
     const int64_t second = static_cast<int64_t>(down ? kBoxRows : a.I) * pr.G;   // the second box's rows
@@ -616,12 +624,9 @@ __global__ void __launch_bounds__(kW4Threads, 2)
       if (lo != 0 || hi != pr.units) {
         // A shared tile: leave the sums, and go on only as the last of its runs.
         const int64_t first = static_cast<int64_t>(tile) * pr.units, last = first + pr.units - 1;
-        int b0 = static_cast<int>(first * pr.nb / pr.all), b1 = static_cast<int>(last * pr.nb / pr.all);
-        int64_t begin = pr.start(b0);
-        for (int64_t n; (n = pr.start(b0 + 1)) <= first; ++b0) begin = n;
-        while (pr.start(b1 + 1) <= last) ++b1;
+        const int b0 = pr.run_of(first), b1 = pr.run_of(last);
         // a run's first tile is its slot 0; only b0 can have begun before this one
-        const int b0_slot = begin < first ? 1 : 0;
+        const int b0_slot = pr.start(b0) < first ? 1 : 0;
         auto part_of = [&](int run_b) {
           return a.part +
                  (((down ? kW4MaxBlocks : 0) + run_b) * 2 + (run_b == b0 ? b0_slot : 0)) * (kW4Warps * kPart) +
@@ -632,9 +637,11 @@ __global__ void __launch_bounds__(kW4Threads, 2)
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int j = 0; j < 4; ++j) part[(k * 4 + j) * 32] = acc[k][j];
-        __threadfence();
         warps_sync();
-        if (threadIdx.x == 0) s_before = atomicAdd(&a.count->tile[down][b0], 1);
+        if (threadIdx.x == 0) {
+          __threadfence();   // over the whole block's sums, which the barrier ordered before
+          s_before = atomicAdd(&a.count->tile[down][b0], 1);
+        }
         warps_sync();
         mine = s_before == b1 - b0;
         if (mine) {
@@ -726,11 +733,10 @@ __global__ void __launch_bounds__(kW4Threads, 2)
           uint8_t* rec = a.zs + routes[pass.off + threadIdx.x] * row_bytes + t * kOpBytes;
           reinterpret_cast<RecordTail*>(rec + 256)->sum = sum * 0x1p-21f;
         }
-        __threadfence();
         fence_proxy_async();
         warps_sync();
         if (threadIdx.x == 0)
-          asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(&a.count->pass[p]) : "memory");
+          asm volatile("fence.acq_rel.gpu;\n\tred.release.gpu.global.add.s32 [%0], 1;" ::"l"(&a.count->pass[p]) : "memory");
       }
       t = tn;
       p = pn;
