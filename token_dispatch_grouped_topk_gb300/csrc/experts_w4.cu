@@ -354,6 +354,11 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+// Brings `bytes` (a multiple of 16, as the address is) into L2.
+__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // One product's tiles and runs.  A tile: a pass's 128-row (gate/up) or
 // 256-row (down) block of weight rows; its units are pairs of groups.
 struct Product {
@@ -461,6 +466,25 @@ __global__ void __launch_bounds__(kW4Threads, 2)
           }
         }
       };
+      // A tile's scales are contiguous per box; the warps read them row by row, 32
+      // bytes at a time, which behind the queue of codes takes longer than a
+      // unit's products, so they are brought into L2 ahead: the run's first
+      // tile before its codes, the next ones a tile ahead.
+      auto prefetch_scales = [&](const Walk& w) {
+        if (lane >= 2 || w.p >= np) return;
+        const int e = unpack_pass(passes[w.p]).e;
+        const int row = down ? e * a.H + w.t * 2 * kBoxRows + lane * kBoxRows
+                             : e * 2 * a.I + w.t * kBoxRows + lane * a.I;
+        if (down && w.t * 2 * kBoxRows + lane * kBoxRows >= a.H) return;
+        bulk_prefetch((down ? a.s2 : a.s13) + static_cast<int64_t>(row) * pr.G, kBoxRows * pr.G * 2);
+      };
+      auto next_tile = [&](Walk w) {
+        w.s = pr.units - 1;
+        step(w);
+        return w;
+      };
+      prefetch_scales(wc);
+      if (s0 + n > pr.units) prefetch_scales(next_tile(wc));
       int have = -1;   // the pass whose z is known to be there
       auto operands = [&](int slot) -> bool {
         if (down && wo.p != have) {
@@ -498,6 +522,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
         }
         __syncwarp();
         step(wc);
+        if (wc.s == 0 && n - u - 1 > pr.units) prefetch_scales(next_tile(wc));
         if (u >= behind) {
           if (!operands(slot)) ok = false;
         } else if (u == behind - 1) {
