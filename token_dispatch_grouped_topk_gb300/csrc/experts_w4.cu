@@ -387,6 +387,31 @@ __device__ __forceinline__ Product product_of(const W4Args& a, bool down, int np
   return p;
 }
 
+// A place in a run: unit s of tile t of pass p, with `left` units to go.
+struct Walk {
+  int s, t, p, tile, left;
+  // On from the tile's unit `end`, which the tile or the run ends at.
+  __device__ void next_tile(const Product& pr, int end) {
+    left -= end - s;
+    s = 0;
+    ++tile;
+    if (++t == pr.row_tiles) {
+      t = 0;
+      ++p;
+    }
+  }
+};
+__device__ __forceinline__ Walk walk_of(const Product& pr, int b) {
+  const int64_t f0 = pr.start(b);
+  Walk w;
+  w.left = static_cast<int>(pr.start(b + 1) - f0);
+  w.tile = static_cast<uint32_t>(f0) / static_cast<uint32_t>(pr.units);
+  w.s = static_cast<int>(f0 - static_cast<int64_t>(w.tile) * pr.units);
+  w.t = w.tile % pr.row_tiles;
+  w.p = w.tile / pr.row_tiles;
+  return w;
+}
+
 // ------------------------------------------------------------------- stream
 struct W4Maps {
   CUtensorMap w13, w2;
@@ -427,8 +452,14 @@ __global__ void __launch_bounds__(kW4Threads, 2)
   volatile int* abort_flag = &s_abort;
   if (warp == kW4Warps) {
     // ------------------------------------------------------------- producer
-    // lane 0 fetches the codes, lane c the operands of column c
-    int issued = 0;
+    // What this warp does between a free stage and the copies into it is on the
+    // stream's critical path: coordinates and addresses are worked out per tile.
+    // Lane 0 fetches the codes and lane c column c of the operands.  Lanes 0
+    // and 1 also bring the two boxes' scales of a tile, which are contiguous,
+    // into L2 a tile ahead: the warps read them row by row, 32 bytes at a time,
+    // which behind the queue of codes takes longer than a unit's products.
+    int slot = 0, issued = 0;
+    uint32_t phase = 1;
     bool ok = true;
     for (int i = 0; ok; ++i) {
       int run = 0;
@@ -445,94 +476,78 @@ __global__ void __launch_bounds__(kW4Threads, 2)
       if (run >= runs) break;
       const bool down = run >= prod[0].nb;
       const Product pr = down ? prod[1] : prod[0];
-      const int b = down ? run - prod[0].nb : run;
-      const int64_t f0 = pr.start(b);
-      const int n = static_cast<int>(pr.start(b + 1) - f0);   // units of the run
-      const int tile0 = static_cast<uint32_t>(f0) / static_cast<uint32_t>(pr.units), s0 = static_cast<int>(f0 - static_cast<int64_t>(tile0) * pr.units);
+      const CUtensorMap* map = down ? &maps.w2 : &maps.w13;
       const uint8_t* ops = down ? a.zs : a.xs;
       const int64_t op_row = operand_row_bytes(down ? a.I : a.H);
-      // Two walks over the run's units: the codes, and the operands, which for
-      // the down product start behind by the stages of the ring.
-      struct Walk {
-        int s, t, p;   // unit of the tile, tile of the pass, pass
+      auto prefetch_scales = [&](const Walk& v) {
+        const int e = unpack_pass(passes[v.p]).e;
+        const int in = down ? v.t * 2 * kBoxRows + lane * kBoxRows : v.t * kBoxRows;   // of the rows
+        if (lane >= 2 || (down && in >= a.H)) return;
+        const int64_t row = down ? static_cast<int64_t>(e) * a.H + in : static_cast<int64_t>(2 * e + lane) * a.I + in;
+        bulk_prefetch((down ? a.s2 : a.s13) + row * pr.G, kBoxRows * pr.G * 2);
       };
-      Walk wc{s0, tile0 % pr.row_tiles, tile0 / pr.row_tiles}, wo = wc;
-      auto step = [&](Walk& w) {
-        if (++w.s == pr.units) {
-          w.s = 0;
-          if (++w.t == pr.row_tiles) {
-            w.t = 0;
-            ++w.p;
-          }
-        }
-      };
-      // A tile's scales are contiguous per box; the warps read them row by row, 32
-      // bytes at a time, which behind the queue of codes takes longer than a
-      // unit's products, so they are brought into L2 ahead: the run's first
-      // tile before its codes, the next ones a tile ahead.
-      auto prefetch_scales = [&](const Walk& w) {
-        if (lane >= 2 || w.p >= np) return;
-        const int e = unpack_pass(passes[w.p]).e;
-        const int row = down ? e * a.H + w.t * 2 * kBoxRows + lane * kBoxRows
-                             : e * 2 * a.I + w.t * kBoxRows + lane * a.I;
-        if (down && w.t * 2 * kBoxRows + lane * kBoxRows >= a.H) return;
-        bulk_prefetch((down ? a.s2 : a.s13) + static_cast<int64_t>(row) * pr.G, kBoxRows * pr.G * 2);
-      };
-      auto next_tile = [&](Walk w) {
-        w.s = pr.units - 1;
-        step(w);
-        return w;
-      };
-      prefetch_scales(wc);
-      if (s0 + n > pr.units) prefetch_scales(next_tile(wc));
+      Walk w = walk_of(pr, down ? run - prod[0].nb : run);
+      prefetch_scales(w);
       int have = -1;   // the pass whose z is known to be there
-      auto operands = [&](int slot) -> bool {
-        if (down && wo.p != have) {
-          if (!__all_sync(0xffffffffu, wait_count(&a.count->pass[wo.p], prod[0].row_tiles, abort_flag)))
-            return false;
-          fence_proxy_async();
-          have = wo.p;
-        }
-        const Pass pass = unpack_pass(passes[wo.p]);
+      while (w.left > 0 && ok) {
+        const Pass pass = unpack_pass(passes[w.p]);
+        const bool both = !down || w.t * 2 * kBoxRows + kBoxRows < a.H;
+        const uint32_t bytes = (both ? 2 : 1) * kBoxBytes + pass.n * kColBytes;
+        const int row = down ? pass.e * a.H + w.t * 2 * kBoxRows : pass.e * 2 * a.I + w.t * kBoxRows;
+        const int row2 = row + (down ? kBoxRows : a.I);
+        const int end = min(w.s + w.left, pr.units);
+        const uint8_t* src = nullptr;
         if (lane < pass.n) {
           const int route = routes[pass.off + lane];
-          bulk_load(cols + (slot * kCols + lane) * kColBytes,
-                    ops + (down ? route : route / a.K) * op_row + wo.s * kColBytes, kColBytes, &s_full[slot]);
+          src = ops + (down ? route : route / a.K) * op_row + w.s * kColBytes;
         }
-        step(wo);
-        return true;
-      };
-      const int behind = down ? min(kStages, n) : 0;
-      for (int u = 0; u < n; ++u, ++issued) {
-        const int slot = issued % kStages;
-        if (!__all_sync(0xffffffffu, mbar_wait(&s_empty[slot], ((issued / kStages) & 1) ^ 1, abort_flag))) {
-          ok = false;
-          break;
+        Walk after = w;
+        after.next_tile(pr, end);
+        if (after.left > 0) prefetch_scales(after);
+        // z may not be there yet, and codes need not wait for it: as many units
+        // as there are stages go out without their operands first
+        const bool wait_z = down && w.p != have;
+        int behind = 0;
+        for (int s = w.s; s < end; ++s, ++issued) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&s_empty[slot], phase, abort_flag))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            uint8_t* dst = ring + slot * 2 * kBoxBytes;
+            mbar_arrive_expect_tx(&s_full[slot], bytes);
+            tma_load_2d(dst, map, &s_full[slot], s * 128, row);
+            if (both) tma_load_2d(dst + kBoxBytes, map, &s_full[slot], s * 128, row2);
+          }
+          __syncwarp();   // the expected bytes stand before an operand's can land
+          if (wait_z && w.p != have) {
+            ++behind;
+            if (behind == kStages || s + 1 == end) {
+              if (!__all_sync(0xffffffffu, wait_count(&a.count->pass[w.p], prod[0].row_tiles, abort_flag))) {
+                ok = false;
+                ++issued;
+                break;
+              }
+              fence_proxy_async();
+              have = w.p;
+              for (int k = 0, at = slot + 1 - behind + (slot + 1 < behind ? kStages : 0); k < behind; ++k) {
+                if (src != nullptr) {
+                  bulk_load(cols + (at * kCols + lane) * kColBytes, src, kColBytes, &s_full[at]);
+                  src += kColBytes;
+                }
+                if (++at == kStages) at = 0;
+              }
+            }
+          } else if (src != nullptr) {
+            bulk_load(cols + (slot * kCols + lane) * kColBytes, src, kColBytes, &s_full[slot]);
+            src += kColBytes;
+          }
+          if (++slot == kStages) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
-        const Pass pass = unpack_pass(passes[wc.p]);
-        if (lane == 0) {
-          uint8_t* dst = ring + slot * 2 * kBoxBytes;
-          const bool both = !down || wc.t * 2 * kBoxRows + kBoxRows < a.H;
-          mbar_arrive_expect_tx(&s_full[slot], (both ? 2 : 1) * kBoxBytes + pass.n * kColBytes);
-          const int row = down ? pass.e * a.H + wc.t * 2 * kBoxRows : pass.e * 2 * a.I + wc.t * kBoxRows;
-          const CUtensorMap* map = down ? &maps.w2 : &maps.w13;
-          tma_load_2d(dst, map, &s_full[slot], wc.s * 128, row);
-          if (both)
-            tma_load_2d(dst + kBoxBytes, map, &s_full[slot], wc.s * 128, row + (down ? kBoxRows : a.I));
-        }
-        __syncwarp();
-        step(wc);
-        if (wc.s == 0 && n - u - 1 > pr.units) prefetch_scales(next_tile(wc));
-        if (u >= behind) {
-          if (!operands(slot)) ok = false;
-        } else if (u == behind - 1) {
-          for (int k = behind - 1; k >= 0 && ok; --k)
-            if (!operands((issued - k) % kStages)) ok = false;
-        }
-        if (!ok) {
-          ++issued;
-          break;
-        }
+        w = after;
       }
     }
     if (!ok) {
@@ -585,10 +600,9 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     const bool down = run >= prod[0].nb;
     const Product pr = down ? prod[1] : prod[0];
     const int b = down ? run - prod[0].nb : run;
-    const int64_t f0 = pr.start(b);
-    int left = static_cast<int>(pr.start(b + 1) - f0);
-    int tile = static_cast<uint32_t>(f0) / static_cast<uint32_t>(pr.units), s = static_cast<int>(f0 - static_cast<int64_t>(tile) * pr.units);
-    int t = tile % pr.row_tiles, p = tile / pr.row_tiles;
+    const Walk w0 = walk_of(pr, b);
+    int left = w0.left, tile = w0.tile, t = w0.t, p = w0.p;
+    const int s = w0.s;
     const uint16_t* scales = down ? a.s2 : a.s13;
     const int64_t second = static_cast<int64_t>(down ? kBoxRows : a.I) * pr.G;   // the second box's rows
     bool both = true;
