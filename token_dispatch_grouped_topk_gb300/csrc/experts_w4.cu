@@ -450,6 +450,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
   const Product prod[2] = {product_of(a, false, np), product_of(a, true, np)};
   const int runs = prod[0].nb + prod[1].nb;
   volatile int* abort_flag = &s_abort;
+  grid_dependency_wait();   // x's operands, the counters, and the readers of old outputs
   if (warp == kW4Warps) {
     // ------------------------------------------------------------- producer
     // What this warp does between a free stage and the copies into it is on the
