@@ -653,6 +653,9 @@ __global__ void __launch_bounds__(kW4Threads, 2)
                    g ? sc[2 * k] & 0xFFFF0000u : sc[2 * k] << 16,
                    g ? sc[2 * k + 1] & 0xFFFF0000u : sc[2 * k + 1] << 16, v, tail0, tail1);
         }
+        // Every lane's reads are over before lane 0 gives the stage back: without
+        // the fence some were seen to come after the copy that the arrival let in.
+        __threadfence_block();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[slot]);
         if (++slot == kStages) {
