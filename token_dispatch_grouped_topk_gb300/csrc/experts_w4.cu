@@ -38,7 +38,8 @@
 // groups of one pass (up to eight tokens of one expert): 128 gate rows and the
 // same 128 up rows, then 256 rows of H.  A producer warp brings the codes with
 // TMA (128-byte swizzled boxes) and the tokens' operands with bulk copies
-// through a ring of stages; each of eight warps takes 2 x 16 of the rows.  The
+// through a ring of stages; each of eight warps takes 2 x 16 of the rows, and a
+// tenth finishes the tiles.  The
 // units of each product in order (tile by tile) are cut into equal runs, about
 // one per block, so every SM reads the same number of bytes whatever the sizes
 // and the routes are.  Of a tile that several runs share each leaves its sums
@@ -63,8 +64,8 @@
 namespace moe {
 namespace {
 
-constexpr int kW4Warps = 8;       // that compute; one more brings the data
-constexpr int kW4Threads = (kW4Warps + 1) * 32;
+constexpr int kW4Warps = 8;       // that compute; one more brings the data, one finishes tiles
+constexpr int kW4Threads = (kW4Warps + 2) * 32;
 constexpr int kPrepThreads = 256;
 constexpr int kCols = 8;          // token columns of one pass
 constexpr int kRows = 16;         // weight rows of one warp in a box
@@ -77,7 +78,9 @@ constexpr int kStages = 3;
 constexpr int kRunUnits = 4;      // a run's units at least
 constexpr int kMaxRoutes = kW4MaxTokens * 32;
 constexpr int kMaxPasses = 1024 + kMaxRoutes / kCols;
-constexpr int kPart = 256;        // sums of one warp in a shared tile
+constexpr int kShareColumns = 3;  // of a run's last tile: as many columns are shared among the warps
+constexpr int kTileRows = 2 * kBoxRows;
+constexpr int kTileSums = kCols * kTileRows;   // a tile's sums, by column
 
 // A pass: up to eight routes of one active expert.
 struct Pass {
@@ -94,7 +97,7 @@ __device__ __forceinline__ Pass unpack_pass(uint32_t p) {
 struct W4Counters {
   int ticket;
   int tile[2][kW4MaxBlocks];   // runs done with the tile that several share and the run begins
-  int pass[kMaxPasses];        // gate/up tiles finished
+  int pass[kMaxPasses];        // columns of gate/up tiles finished
 };
 
 struct W4Args {
@@ -109,7 +112,8 @@ struct W4Args {
   uint8_t* zs;          // [T * K] operand rows of z, by route
   float* o;             // [T * K, H] by route
   W4Counters* count;
-  float* part;          // [2][2 * blocks][warps][kPart] sums of shared tiles
+  float* part;          // [2][blocks][2] sums of shared tiles by run, then
+                        // [blocks][2] of whole tiles, kTileSums each
   int T, H, I, K, E;
   int max_passes;       // bound of the plan's passes
 };
@@ -412,6 +416,111 @@ __device__ __forceinline__ Walk walk_of(const Product& pr, int b) {
   return w;
 }
 
+// Where a tile's sums are: `count` runs' in order from `first` (in units of two
+// slots), the first run's in slot `slot`, the others' in slot 0.
+struct Sums {
+  int first, count, slot;
+};
+
+// Finishes columns [c0, c0 + C) of a tile with one warp, lane i rows 4i..4i+3
+// of both boxes: adds the runs' sums in order and writes the down product's
+// rows, or z of the tile's 128-group as an operand record.
+template <int C>
+__device__ __forceinline__ void w4_finish(const W4Args& a, const Sums& from, bool down, const Walk& at,
+                                          int row_tiles, const Pass& pass, const uint16_t* routes, int c0,
+                                          int lane) {
+  float v[C][8];
+#pragma unroll
+  for (int j = 0; j < C; ++j)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[j][k] = 0.f;
+  for (int b = 0; b < from.count; b += 4) {
+    float4 in[4][C][2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at_slot = (from.first + b + k) * 2 + (b + k == 0 ? from.slot : 0);
+      const float4* p = reinterpret_cast<const float4*>(a.part + static_cast<int64_t>(at_slot) * kTileSums +
+                                                        c0 * kTileRows) + lane;
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          in[k][j][h] = b + k < from.count && c0 + j < pass.n
+                            ? __ldcg(p + j * (kTileRows / 4) + h * (kBoxRows / 4))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          v[j][4 * h] += in[k][j][h].x;
+          v[j][4 * h + 1] += in[k][j][h].y;
+          v[j][4 * h + 2] += in[k][j][h].z;
+          v[j][4 * h + 3] += in[k][j][h].w;
+        }
+  }
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    if (c0 + j >= pass.n) break;
+    const int64_t route = routes[pass.off + c0 + j];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[j][k] *= 0x1p24f;
+    if (down) {
+      float* o = a.o + route * a.H + at.t * kTileRows + 4 * lane;
+      *reinterpret_cast<float4*>(o) = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
+      if (at.t * kTileRows + kBoxRows < a.H)
+        *reinterpret_cast<float4*>(o + kBoxRows) = make_float4(v[j][4], v[j][5], v[j][6], v[j][7]);
+      continue;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float gate = v[j][k];
+      v[j][k] = gate / (1.f + expf(-gate)) * v[j][4 + k];
+      m = max(m, __float_as_uint(v[j][k]) & 0x7fffffffu);
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    RecordTail tail;
+    const float mult = operand_scale(m, &tail.back);
+    float sum = 0.f;
+    uint32_t words[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const __half2 h = __floats2half2_rn(operand_value(v[j][2 * k], mult),
+                                          operand_value(v[j][2 * k + 1], mult) * 0.0625f);
+      const float2 back = __half22float2(h);
+      sum += back.x + back.y * 16.f;
+      words[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+#pragma unroll
+    for (int k = 16; k >= 1; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    // an even lane's elements and the next lane's are the record's pairs
+    const uint32_t next0 = __shfl_xor_sync(0xffffffffu, words[0], 1);
+    const uint32_t next1 = __shfl_xor_sync(0xffffffffu, words[1], 1);
+    uint8_t* rec = a.zs + route * operand_row_bytes(a.I) + at.t * kOpBytes;
+    if ((lane & 1) == 0)
+      *reinterpret_cast<uint4*>(rec + record_word(lane >> 1)) =
+          make_uint4(__byte_perm(words[0], next0, 0x5410), __byte_perm(words[0], next0, 0x7632),
+                     __byte_perm(words[1], next1, 0x5410), __byte_perm(words[1], next1, 0x7632));
+    tail.sum = sum * 0x1p-21f;
+    if (lane == 0) *reinterpret_cast<RecordTail*>(rec + 256) = tail;
+    // the record past an odd number of groups: zeros
+    if ((row_tiles & 1) && at.t == row_tiles - 1 && lane < kOpBytes / 16)
+      *reinterpret_cast<uint4*>(rec + kOpBytes + lane * 16) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// Counts columns of z that the warp has written.
+__device__ __forceinline__ void w4_count(int* pass_count, int columns, int lane) {
+  fence_proxy_async();
+  __syncwarp();
+  if (lane == 0)
+    asm volatile("fence.acq_rel.gpu;\n\tred.release.gpu.global.add.s32 [%0], %1;" ::"l"(pass_count), "r"(columns)
+                 : "memory");
+}
+
 // ------------------------------------------------------------------- stream
 struct W4Maps {
   CUtensorMap w13, w2;
@@ -422,9 +531,10 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     w4_stream_kernel(const __grid_constant__ W4Maps maps, const W4Args a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_full[kStages], s_empty[kStages], s_run_full[2], s_run_empty[2];
-  __shared__ int s_run[2], s_abort, s_before;
-  __shared__ uint32_t s_max[kW4Warps][kCols];
-  __shared__ float s_sum[kW4Warps][kCols];
+  __shared__ uint64_t s_sums[2], s_free[2];   // a tile's sums are there, are done with
+  __shared__ uint64_t s_last;                 // the sums of a run's last tile: s_from
+  __shared__ Sums s_from;
+  __shared__ int s_run[2], s_abort;
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);   // [kStages][2 boxes]
   uint8_t* cols = ring + kStages * 2 * kBoxBytes;                // [kStages][kCols][kColBytes]
@@ -439,8 +549,11 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_run_full[i], 1);
-      mbar_init(&s_run_empty[i], kW4Warps);
+      mbar_init(&s_run_empty[i], kW4Warps + 1);
+      mbar_init(&s_sums[i], kW4Warps);
+      mbar_init(&s_free[i], kW4Warps);
     }
+    mbar_init(&s_last, 1);
     s_abort = 0;
     fence_barrier_init();
     tma_prefetch_desc(&maps.w13);
@@ -524,7 +637,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
           if (wait_z && w.p != have) {
             ++behind;
             if (behind == kStages || s + 1 == end) {
-              if (!__all_sync(0xffffffffu, wait_count(&a.count->pass[w.p], prod[0].row_tiles, abort_flag))) {
+              if (!__all_sync(0xffffffffu, wait_count(&a.count->pass[w.p], prod[0].row_tiles * pass.n, abort_flag))) {
                 ok = false;
                 ++issued;
                 break;
@@ -564,80 +677,123 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     return;
   }
 
+  // Where a tile's sums go: a shared tile's to its run (its first tile is slot
+  // 0, its last slot 1), a whole tile's to the block.
+  auto sums_of = [&](bool shared, bool down, int b, int slot) {
+    const int at = shared ? (down ? kW4MaxBlocks : 0) + b : 2 * kW4MaxBlocks + static_cast<int>(blockIdx.x);
+    return a.part + static_cast<int64_t>(at * 2 + slot) * kTileSums;
+  };
+  // A wait that ran out ends the block: the flag ends every other wait in it.
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag))) return true;
+    *abort_flag = 1;
+    if (lane == 0) atomicOr(a.dev_status, kDevTimeout);
+    return false;
+  };
+  if (warp == kW4Warps + 1) {
+    // -------------------------------------------------------------- finisher
+    // Takes the tiles' sums off the warps that compute, which go on with the
+    // next tile: a join's fence and counter, the other runs' sums and z's
+    // records take microseconds, in which the ring would stand full.
+    for (int i = 0, tiles = 0;; ++i) {
+      if (!wait(&s_run_full[i & 1], (i >> 1) & 1)) return;
+      const int run = s_run[i & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_run_empty[i & 1]);
+      if (run >= runs) return;
+      const bool down = run >= prod[0].nb;
+      const Product pr = down ? prod[1] : prod[0];
+      const int b = down ? run - prod[0].nb : run;
+      Walk w = walk_of(pr, b);
+      for (; w.left > 0; ++tiles) {
+        const Walk at = w;
+        const int end = min(w.s + w.left, pr.units);
+        w.next_tile(pr, end);
+        if (!wait(&s_sums[tiles & 1], (tiles >> 1) & 1)) return;
+        Sums from{2 * kW4MaxBlocks + static_cast<int>(blockIdx.x), 1, tiles & 1};
+        if (at.s != 0 || end != pr.units) {
+          // go on only as the last of the tile's runs
+          const int64_t first = static_cast<int64_t>(at.tile) * pr.units, last = first + pr.units - 1;
+          const int b0 = pr.run_of(first), b1 = pr.run_of(last);
+          int before = 0;
+          if (lane == 0) {
+            __threadfence();   // over the block's sums, which the barrier ordered before
+            before = atomicAdd(&a.count->tile[down][b0], 1);
+          }
+          before = __shfl_sync(0xffffffffu, before, 0);
+          // of the runs only b0 can have begun before the tile
+          from = Sums{(down ? kW4MaxBlocks : 0) + b0, before == b1 - b0 ? b1 - b0 + 1 : 0,
+                      pr.start(b0) < first ? 1 : 0};
+          __threadfence();
+        }
+        const Pass pass = unpack_pass(passes[at.p]);
+        if (w.left == 0 && pass.n >= kShareColumns) {
+          // the run's last tile: the other warps have nothing else to do
+          if (lane == 0) {
+            s_from = from;
+            mbar_arrive(&s_last);
+          }
+          continue;
+        }
+        if (from.count != 0) {
+          for (int c0 = 0; c0 < pass.n; c0 += 2)
+            w4_finish<2>(a, from, down, at, pr.row_tiles, pass, routes, c0, lane);
+          if (!down) w4_count(&a.count->pass[at.p], pass.n, lane);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_n(&s_free[tiles & 1], kW4Warps);
+      }
+    }
+  }
+
   // ------------------------------------------------------------------ products
   const int r = lane >> 2, q = lane & 3;
   const int row = box_row(r);
   // the lane's first row in a box, for the first and the second group
   const int off0 = (warp * kRows + row) * 128 + ((q ^ (row & 7)) << 4), off1 = off0 ^ 64;
   int slot = 0;
-  uint32_t phase = 0;
-  bool ok = true;
-  auto warps_sync = []() { asm volatile("bar.sync 1, %0;" ::"n"(kW4Warps * 32) : "memory"); };
-  auto warps_any = [](bool v) {
-    uint32_t any;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-        "barrier.cta.red.or.pred p, 1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(any)
-        : "r"(static_cast<uint32_t>(v)), "n"(kW4Warps * 32)
-        : "memory");
-    return any != 0;
-  };
-  // A wait that ran out: the block goes on without waiting, on whatever is
-  // there, so that no other warp or block waits for this one.
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (ok && !__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag))) {
-      ok = false;
-      *abort_flag = 1;
-    }
-  };
-  for (int i = 0;; ++i) {
-    wait(&s_run_full[i & 1], (i >> 1) & 1);
-    if (warps_any(!ok)) break;   // all of them: no warp waits in a barrier alone
+  uint32_t phase = 0, last_phase = 0;
+  for (int i = 0, tiles = 0;; ++i) {
+    if (!wait(&s_run_full[i & 1], (i >> 1) & 1)) return;
     const int run = s_run[i & 1];
     __syncwarp();
     if (lane == 0) mbar_arrive(&s_run_empty[i & 1]);
-    if (run >= runs) break;
+    if (run >= runs) return;
     const bool down = run >= prod[0].nb;
     const Product pr = down ? prod[1] : prod[0];
     const int b = down ? run - prod[0].nb : run;
-    const Walk w0 = walk_of(pr, b);
-    int left = w0.left, tile = w0.tile, t = w0.t, p = w0.p;
-    const int s = w0.s;
     const uint16_t* scales = down ? a.s2 : a.s13;
     const int64_t second = static_cast<int64_t>(down ? kBoxRows : a.I) * pr.G;   // the second box's rows
-    bool both = true;
     // The scales of a unit are loaded one unit ahead of their use.
     uint32_t next[4];
-    auto scales_of = [&](int p2, int t2, int s2) {
-      const int e = unpack_pass(passes[p2]).e;
-      const int first = down ? e * a.H + t2 * 2 * kBoxRows : e * 2 * a.I + t2 * kBoxRows;
+    auto scales_of = [&](const Walk& v, int s) {
+      const int e = unpack_pass(passes[v.p]).e;
+      const int first = down ? e * a.H + v.t * kTileRows : e * 2 * a.I + v.t * kBoxRows;
       const uint16_t* sp = scales + static_cast<int64_t>(first + warp * kRows + row) * pr.G;
-      const bool two = !down || t2 * 2 * kBoxRows + kBoxRows < a.H;
-      next[0] = load_scales(sp, 2 * s2, pr.G);
-      next[1] = load_scales(sp + 8 * pr.G, 2 * s2, pr.G);
-      next[2] = two ? load_scales(sp + second, 2 * s2, pr.G) : 0u;
-      next[3] = two ? load_scales(sp + second + 8 * pr.G, 2 * s2, pr.G) : 0u;
+      const bool two = !down || v.t * kTileRows + kBoxRows < a.H;
+      next[0] = load_scales(sp, 2 * s, pr.G);
+      next[1] = load_scales(sp + 8 * pr.G, 2 * s, pr.G);
+      next[2] = two ? load_scales(sp + second, 2 * s, pr.G) : 0u;
+      next[3] = two ? load_scales(sp + second + 8 * pr.G, 2 * s, pr.G) : 0u;
     };
-    scales_of(p, t, s);
-    for (bool begun = true; left > 0; begun = false, ++tile) {
-      const int lo = begun ? s : 0, hi = min(lo + left, pr.units);
-      left -= hi - lo;
-      const Pass pass = unpack_pass(passes[p]);
-      both = !down || t * 2 * kBoxRows + kBoxRows < a.H;
-      const int tn = t + 1 == pr.row_tiles ? 0 : t + 1, pn = t + 1 == pr.row_tiles ? p + 1 : p;
+    Walk w = walk_of(pr, b);
+    scales_of(w, w.s);
+    for (bool begun = true; w.left > 0; begun = false, ++tiles) {
+      const Walk at = w;
+      const int end = min(w.s + w.left, pr.units);
+      w.next_tile(pr, end);
       float acc[2][4];
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[k][j] = 0.f;
-      for (int u = lo; u < hi; ++u) {
+      for (int u = at.s; u < end; ++u) {
         uint32_t sc[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) sc[j] = next[j];
-        if (u + 1 < hi) scales_of(p, t, u + 1);
-        else if (left > 0) scales_of(pn, tn, 0);
-        wait(&s_full[slot], phase);
+        if (u + 1 < end) scales_of(at, u + 1);
+        else if (w.left > 0) scales_of(w, 0);
+        if (!wait(&s_full[slot], phase)) return;
         const uint8_t* box = ring + slot * 2 * kBoxBytes;
         const uint8_t* col = cols + slot * kCols * kColBytes;
 #pragma unroll
@@ -663,129 +819,36 @@ __global__ void __launch_bounds__(kW4Threads, 2)
           phase ^= 1;
         }
       }
-      bool mine = true;   // this run finishes the tile
-      if (lo != 0 || hi != pr.units) {
-        // A shared tile: leave the sums, and go on only as the last of its runs.
-        const int64_t first = static_cast<int64_t>(tile) * pr.units, last = first + pr.units - 1;
-        const int b0 = pr.run_of(first), b1 = pr.run_of(last);
-        // a run's first tile is its slot 0; only b0 can have begun before this one
-        const int b0_slot = pr.start(b0) < first ? 1 : 0;
-        auto part_of = [&](int run_b) {
-          return a.part +
-                 (((down ? kW4MaxBlocks : 0) + run_b) * 2 + (run_b == b0 ? b0_slot : 0)) * (kW4Warps * kPart) +
-                 warp * kPart + lane;
-        };
-        float* part = part_of(b);
+      // the sums of rows (row, row + 8) of both boxes and columns (2q, 2q + 1)
+      if (!wait(&s_free[tiles & 1], ((tiles >> 1) & 1) ^ 1)) return;
+      const int n = unpack_pass(passes[at.p]).n;
+      const bool shared = at.s != 0 || end != pr.units;
+      float* out = sums_of(shared, down, b, shared ? !begun : tiles & 1) + 2 * q * kTileRows + warp * kRows + row;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (2 * q + j >= n) continue;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) part[(k * 4 + j) * 32] = acc[k][j];
-        warps_sync();
-        if (threadIdx.x == 0) {
-          __threadfence();   // over the whole block's sums, which the barrier ordered before
-          s_before = atomicAdd(&a.count->tile[down][b0], 1);
-        }
-        warps_sync();
-        mine = s_before == b1 - b0;
-        if (mine) {
+          for (int h = 0; h < 2; ++h) out[j * kTileRows + k * kBoxRows + 8 * h] = acc[k][2 * h + j];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_sums[tiles & 1]);
+      if (w.left == 0 && n >= kShareColumns) {
+        // a column a warp
+        if (!wait(&s_last, last_phase)) return;
+        last_phase ^= 1;
+        const Sums from = s_from;
+        if (from.count != 0 && warp < n) {
           __threadfence();
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[k][j] = 0.f;
-          // four runs' loads at a time, in run order
-          for (int b2 = b0; b2 <= b1; b2 += 4) {
-            float v[4][8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-              for (int j = 0; j < 8; ++j) v[k][j] = b2 + k <= b1 ? __ldcg(part_of(b2 + k) + j * 32) : 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-              for (int j = 0; j < 8; ++j) acc[j >> 2][j & 3] += v[k][j];
-          }
+          w4_finish<1>(a, from, down, at, pr.row_tiles, unpack_pass(passes[at.p]), routes, warp, lane);
+          if (!down) w4_count(&a.count->pass[at.p], 1, lane);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[tiles & 1]);
       }
-      if (mine && down) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (2 * q + j >= pass.n) continue;
-          float* o = a.o + static_cast<int64_t>(routes[pass.off + 2 * q + j]) * a.H + t * 2 * kBoxRows +
-                     warp * kRows + row;
-          o[0] = acc[0][j] * 0x1p24f;
-          o[8] = acc[0][2 + j] * 0x1p24f;
-          if (both) {
-            o[kBoxRows] = acc[1][j] * 0x1p24f;
-            o[kBoxRows + 8] = acc[1][2 + j] * 0x1p24f;
-          }
-        }
-      } else if (mine) {
-        // z of the lane's rows (row, row + 8) and columns (2q, 2q + 1); the
-        // group's largest by column over the block, then its record
-        float z[2][2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float gate = acc[0][2 * h + j] * 0x1p24f;
-            z[h][j] = gate / (1.f + expf(-gate)) * (acc[1][2 * h + j] * 0x1p24f);
-            m = max(m, __float_as_uint(z[h][j]) & 0x7fffffffu);
-          }
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          if (r == 0) s_max[warp][2 * q + j] = m;
-        }
-        warps_sync();
-        const int64_t row_bytes = operand_row_bytes(a.I);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int cc = 2 * q + j;
-          uint32_t m = 0;
-#pragma unroll
-          for (int w = 0; w < kW4Warps; ++w) m = max(m, s_max[w][cc]);
-          float back;
-          const float mult = operand_scale(m, &back);
-          uint8_t* rec = a.zs + routes[pass.off + min(cc, pass.n - 1)] * row_bytes + t * kOpBytes;
-          float sum = 0.f;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int e = warp * kRows + row + 8 * h;   // element of the group
-            const __half v = __float2half_rn(operand_value(z[h][j], mult) * (e & 1 ? 0.0625f : 1.f));
-            sum += __half2float(v) * (e & 1 ? 16.f : 1.f);
-            if (cc < pass.n)
-              *reinterpret_cast<__half*>(rec + record_word(e >> 3) + (e & 3) * 4 + (e & 4 ? 2 : 0)) = v;
-          }
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (r == 0) s_sum[warp][cc] = sum;
-          if (warp == 0 && cc < pass.n) {
-            if (r == 0) reinterpret_cast<RecordTail*>(rec + 256)->back = back;
-            // the record past an odd number of groups: zeros
-            if ((pr.row_tiles & 1) && t == pr.row_tiles - 1)
-              for (int k = r; k < kOpBytes / 16; k += 8)
-                *reinterpret_cast<uint4*>(rec + kOpBytes + k * 16) = make_uint4(0, 0, 0, 0);
-          }
-        }
-        warps_sync();
-        if (static_cast<int>(threadIdx.x) < pass.n) {
-          float sum = 0.f;
-#pragma unroll
-          for (int w = 0; w < kW4Warps; ++w) sum += s_sum[w][threadIdx.x];
-          uint8_t* rec = a.zs + routes[pass.off + threadIdx.x] * row_bytes + t * kOpBytes;
-          reinterpret_cast<RecordTail*>(rec + 256)->sum = sum * 0x1p-21f;
-        }
-        fence_proxy_async();
-        warps_sync();
-        if (threadIdx.x == 0)
-          asm volatile("fence.acq_rel.gpu;\n\tred.release.gpu.global.add.s32 [%0], 1;" ::"l"(&a.count->pass[p]) : "memory");
-      }
-      t = tn;
-      p = pn;
     }
   }
-  if (!ok && lane == 0) atomicOr(a.dev_status, kDevTimeout);
 }
 
 // ------------------------------------------------------------------ combine
@@ -840,7 +903,7 @@ W4Workspace w4_workspace(int T, int K, int H, int I) {
   w.zs = take(n * operand_row_bytes(I));
   w.o = take(n * H * 4);
   w.count = take(sizeof(W4Counters));
-  w.part = take(static_cast<size_t>(kW4MaxBlocks) * 4 * kW4Warps * kPart * 4);
+  w.part = take(static_cast<size_t>(kW4MaxBlocks) * 6 * kTileSums * 4);
   w.total = off;
   return w;
 }
