@@ -48,9 +48,8 @@ struct TopkArgs {
 
 // Order-preserving key of c; 0 for what can never be chosen (-inf, NaN).
 __device__ __forceinline__ uint32_t choice_key(float c) {
-  if (!(c > -INFINITY)) return 0u;
-  const uint32_t u = __float_as_uint(__fadd_rn(c, 0.f));   // -0 and +0 are one value
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const int u = __float_as_int(__fadd_rn(c, 0.f));   // -0 and +0 are one value
+  return c > -INFINITY ? static_cast<uint32_t>(u ^ ((u >> 31) | static_cast<int>(0x80000000u))) : 0u;
 }
 template <typename LogitT>
 __device__ __forceinline__ float logit_value(LogitT v) {
@@ -96,9 +95,9 @@ struct Best {
   }
 };
 
-template <typename LogitT, int V>
-__global__ void router_topk_kernel(const TopkArgs a, const bool vec) {
-  extern __shared__ uint32_t s_keys[];   // [warps][32 * V]
+template <typename LogitT, int V, bool kSigmoid>
+__global__ void router_topk_kernel(const TopkArgs a, const bool vec, const bool vec_bias) {
+  extern __shared__ __align__(16) uint32_t s_keys[];   // [warps][32 * V]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * (blockDim.x >> 5) + warp;
   if (t >= a.T) return;
@@ -114,8 +113,8 @@ __global__ void router_topk_kernel(const TopkArgs a, const bool vec) {
   // itself, so an infinite logit takes the whole weight).  Where the largest is
   // always among the chosen and the weights are renormalised, the sum cancels.
   float m = -INFINITY, den = 1.f;
-  const bool need_sum = !a.sigmoid && (biased || sums || !a.renorm);
-  if (!a.sigmoid) {
+  const bool need_sum = !kSigmoid && (biased || sums || !a.renorm);
+  if (!kSigmoid) {
 #pragma unroll
     for (int j = 0; j < V; ++j) m = fmaxf(m, l[j]);
 #pragma unroll
@@ -123,18 +122,17 @@ __global__ void router_topk_kernel(const TopkArgs a, const bool vec) {
   }
   auto score = [&](float x) -> float {   // for softmax before the division by the sum
     if (x == -INFINITY) return 0.f;
-    if (a.sigmoid) return sigmoid(x);
+    if (kSigmoid) return sigmoid(x);
     return x == m ? 1.f : expf(x - m);
   };
   float s[V];
   if (need_sum || biased || sums) {
-    float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      s[j] = score(l[j]);
-      sum += s[j];
-    }
+    for (int j = 0; j < V; ++j) s[j] = score(l[j]);
     if (need_sum) {
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum += s[j];
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
       den = fmaxf(sum, 1e-30f);
@@ -144,10 +142,21 @@ __global__ void router_topk_kernel(const TopkArgs a, const bool vec) {
   uint32_t key[V];
   float value[V];
   if (biased) {
+    float b[V];
+    if (V % 4 == 0 && vec_bias) {
+      if (e0 < E) {
+#pragma unroll
+        for (int j = 0; j < V / 4; ++j)
+          reinterpret_cast<float4*>(b)[j] = __ldg(reinterpret_cast<const float4*>(a.bias + e0) + j);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) b[j] = e0 + j < E ? __ldg(a.bias + e0 + j) : 0.f;
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      if (!a.sigmoid) s[j] = __fdiv_rn(s[j], den);
-      const float c = l[j] == -INFINITY ? -INFINITY : __fadd_rn(s[j], __ldg(a.bias + e0 + j));
+      if (!kSigmoid) s[j] = __fdiv_rn(s[j], den);
+      const float c = l[j] == -INFINITY ? -INFINITY : __fadd_rn(s[j], b[j]);
       key[j] = choice_key(c);
       value[j] = key[j] ? c : -INFINITY;
     }
@@ -186,12 +195,12 @@ __global__ void router_topk_kernel(const TopkArgs a, const bool vec) {
     if (mine) gk = choice_key(a.top == 2 && best.b > -INFINITY ? __fadd_rn(best.a, best.b) : best.a);
     if (aligned) {
       // the lowest lane with the best key is in the lowest such group
-      const int own = lane / span;
+      const int log_span = __ffs(span) - 1, own = lane >> log_span;
       bool kept = false;
       for (int i = 0; i < a.keep; ++i) {
         const uint32_t top = __reduce_max_sync(kFull, gk);
         if (top == 0u) break;
-        const int g = (__ffs(__ballot_sync(kFull, gk == top)) - 1) / span;
+        const int g = (__ffs(__ballot_sync(kFull, gk == top)) - 1) >> log_span;
         if (own == g) {
           kept = true;
           gk = 0u;
@@ -222,10 +231,15 @@ __global__ void router_topk_kernel(const TopkArgs a, const bool vec) {
 
   uint32_t lm = 0;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    lm = max(lm, key[j]);
-    // the lane's keys as V lanes read them: no bank twice for V <= 32
-    keys[e0 + j] = key[j];
+  for (int j = 0; j < V; ++j) lm = max(lm, key[j]);
+  // the lane's keys, which V lanes read at once: no bank twice for V <= 32
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int j = 0; j < V; j += 4)
+      *reinterpret_cast<uint4*>(keys + e0 + j) = make_uint4(key[j], key[j + 1], key[j + 2], key[j + 3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) keys[e0 + j] = key[j];
   }
   __syncwarp();
   int id = -1;
@@ -271,7 +285,9 @@ cudaError_t launch_topk_v(const TopkArgs& a, int sm_count, cudaStream_t s) {
   const int grid = (a.T + warps - 1) / warps;
   constexpr int kBytes = V * static_cast<int>(sizeof(LogitT));
   const bool vec = a.E % V == 0 && (reinterpret_cast<uintptr_t>(a.logits) & (std::min(kBytes, 16) - 1)) == 0;
-  router_topk_kernel<LogitT, V><<<grid, warps * 32, warps * 32 * V * 4, s>>>(a, vec);
+  const bool vec_bias = V % 4 == 0 && a.E % V == 0 && (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0;
+  auto* kernel = a.sigmoid ? router_topk_kernel<LogitT, V, true> : router_topk_kernel<LogitT, V, false>;
+  kernel<<<grid, warps * 32, warps * 32 * V * 4, s>>>(a, vec, vec_bias);
   return cudaGetLastError();
 }
 
