@@ -155,7 +155,7 @@ cudaError_t launch_ep_result(const int32_t* route_msg, const int32_t* route_pos,
 // residual null: no addition; y, yq/ys, residual_out may each be null.
 cudaError_t launch_add_rms_norm(const void* x, const void* residual, int residual_bits,
                                 const void* weight, int weight_bits, float eps, int T, int H,
-                                void* y, uint8_t* yq, float* ys, void* residual_out, int sm_count,
+                                void* y, uint8_t* yq, float* ys, void* residual_out,
                                 cudaStream_t s);
 cudaError_t launch_router_logits(const void* x, const void* w, int T, int H, int E, float* logits,
                                  int32_t* dev_status, int sm_count, cudaStream_t s);
@@ -163,7 +163,7 @@ constexpr int kMaxRouterGroups = 32;
 cudaError_t launch_router_topk(const void* logits, int logits_bits, const float* bias, int T,
                                int E, int K, int sigmoid, int groups, int topk_groups,
                                int group_top, int renorm, float scale, void* topk_idx,
-                               int idx_bits, float* topk_w, int sm_count, cudaStream_t s);
+                               int idx_bits, float* topk_w, cudaStream_t s);
 
 // ----- dispatch of rows already in e4m3 (xq [T, H], xs [T, H/128])
 cudaError_t launch_dispatch_fp8(const uint8_t* tq, const float* ts, const void* topk_idx,

@@ -430,7 +430,7 @@ moe_status moe_add_rms_norm(const void* x, const void* residual, int residual_bi
   const DeviceInfo* dev = nullptr;
   if (moe_status st = check_device(&dev); st != MOE_OK) return st;
   return from_cuda(launch_add_rms_norm(x, residual, residual_bits, weight, weight_bits, eps, T, H,
-                                       y, yq, ys, residual_out, dev->sm_count,
+                                       y, yq, ys, residual_out,
                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -466,7 +466,7 @@ moe_status moe_router_topk(const void* logits, int logits_bits, const float* bia
   return from_cuda(launch_router_topk(logits, logits_bits, bias, T, E, K,
                                       score == MOE_SCORE_SIGMOID ? 1 : 0, groups, topk_groups,
                                       group_top, renormalize ? 1 : 0, scale, topk_idx, idx_bits,
-                                      topk_w, dev->sm_count,
+                                      topk_w,
                                       reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -10,9 +10,16 @@
 //
 // One pass: a row stays in its threads' registers between the sum of squares
 // and the outputs, so every input is read once and every output written once.
-// Rows up to 1024 elements take a warp each (no block barrier); longer rows
-// take a block.  A half-warp holds whole 128-element groups (16 lanes x 8
-// elements), so a group's maximum is a 4-step shuffle.
+// Rows up to 256 elements take a warp each (no block barrier); longer rows
+// take a block, with as many threads as give each one vector of eight elements
+// up to 8192 elements and two beyond: more loads in flight per thread leave
+// fewer rows on an SM and were slower from one row to 16384.  A half-warp holds
+// whole 128-element groups (16 lanes x 8 elements), so a group's maximum is a
+// 4-step shuffle.
+//
+// Bound by HBM with many rows: 16384 rows of 7168 with a BF16 residual and both
+// outputs, 1.06 GB, take 175 us, 6.05 TB/s.  With few rows by latency: 2 to 4 us
+// (one row of 7168: 2.8).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -21,7 +28,9 @@
 namespace moe {
 namespace {
 
-constexpr int kWarpRowMax = 1024;  // elements of a row that one warp takes
+// Elements of a row that one warp takes.  Against a block per row: 65536 rows of
+// 128 take 15 us for 35, of 256 24 for 36; of 512, the other way, 46 for 49 us.
+constexpr int kWarpRowMax = 256;
 constexpr int kRowWarps = 8;       // rows (= warps) per block of the warp form
 
 struct NormArgs {
@@ -155,21 +164,19 @@ __global__ void norm_kernel(const NormArgs a) {
 }
 
 template <int kResidual>
-cudaError_t launch_norm(const NormArgs& a, int sm_count, cudaStream_t s) {
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
   const int nvec = a.H / 8;
   if (a.H <= kWarpRowMax) {
     const int grid = (a.T + kRowWarps - 1) / kRowWarps;
     norm_kernel<kResidual, kWarpRowMax / 256, true><<<grid, kRowWarps * 32, 0, s>>>(a);
     return cudaGetLastError();
   }
-  const int v = a.T < 2 * sm_count ? (nvec <= 1024 ? 1 : 2) : 4;
+  const int v = nvec <= 1024 ? 1 : 2;
   const int threads = ((nvec + v - 1) / v + 31) / 32 * 32;
   if (v == 1)
     norm_kernel<kResidual, 1, false><<<a.T, threads, 0, s>>>(a);
-  else if (v == 2)
-    norm_kernel<kResidual, 2, false><<<a.T, threads, 0, s>>>(a);
   else
-    norm_kernel<kResidual, 4, false><<<a.T, threads, 0, s>>>(a);
+    norm_kernel<kResidual, 2, false><<<a.T, threads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -177,15 +184,15 @@ cudaError_t launch_norm(const NormArgs& a, int sm_count, cudaStream_t s) {
 
 cudaError_t launch_add_rms_norm(const void* x, const void* residual, int residual_bits,
                                 const void* weight, int weight_bits, float eps, int T, int H,
-                                void* y, uint8_t* yq, float* ys, void* residual_out, int sm_count,
+                                void* y, uint8_t* yq, float* ys, void* residual_out,
                                 cudaStream_t s) {
   if (T == 0) return cudaSuccess;
   const NormArgs a{static_cast<const uint4*>(x), residual, residual_out, weight,
                    static_cast<uint4*>(y), reinterpret_cast<uint2*>(yq), ys, T, H,
                    weight_bits == 32 ? 1 : 0, eps};
-  if (residual == nullptr) return launch_norm<0>(a, sm_count, s);
-  if (residual_bits == 16) return launch_norm<16>(a, sm_count, s);
-  return launch_norm<32>(a, sm_count, s);
+  if (residual == nullptr) return launch_norm<0>(a, s);
+  if (residual_bits == 16) return launch_norm<16>(a, s);
+  return launch_norm<32>(a, s);
 }
 
 }  // namespace moe
