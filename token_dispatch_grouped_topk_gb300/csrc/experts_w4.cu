@@ -75,7 +75,9 @@ constexpr int kOpBytes = 288;     // operand record of a group: 256 bytes, its t
 constexpr int kColBytes = 2 * kOpBytes;     // one column of a unit (64 mod 128: no bank conflicts)
 constexpr int kStageBytes = 2 * kBoxBytes + kCols * kColBytes;
 constexpr int kStages = 3;
-constexpr int kRunUnits = 4;      // a run's units at least
+// A run's units at least.  One token, one expert of 7168 x 2048: 24 us; with four
+// 28, with eight 32; with one the joins cost more (two experts 34 us for 31).
+constexpr int kRunUnits = 2;
 constexpr int kMaxRoutes = kW4MaxTokens * 32;
 constexpr int kMaxPasses = 1024 + kMaxRoutes / kCols;
 constexpr int kShareColumns = 3;  // of a run's last tile: as many columns are shared among the warps
