@@ -38,14 +38,19 @@
 // groups of one pass (up to eight tokens of one expert): 128 gate rows and the
 // same 128 up rows, then 256 rows of H.  A producer warp brings the codes with
 // TMA (128-byte swizzled boxes) and the tokens' operands with bulk copies
-// through a ring of stages; each of eight warps takes 2 x 16 of the rows, and a
-// tenth finishes the tiles.  The
+// through a ring of stages; each of eight warps takes 2 x 16 of the rows.  The
 // units of each product in order (tile by tile) are cut into equal runs, about
 // one per block, so every SM reads the same number of bytes whatever the sizes
-// and the routes are.  Of a tile that several runs share each leaves its sums
-// in the workspace, and the last to finish adds them in run order, so the
-// order of every sum is fixed by the routes alone.  A finished gate/up tile is
-// one 128-group of z, stored at once as operands of the down product; a down
+// and the routes are.  (Runs cut two or three times finer, to even out the blocks,
+// were slower: 146 us to 149 and 153 with 48 tokens; so was handing the last
+// quarter out in shorter runs.)  The sums of a tile are left in the workspace; of
+// a tile that several runs share the last to finish adds them in run order, so
+// the order of every sum is fixed by the routes alone.  A warp of its own does
+// that, as a join and what follows it take about 5 us in which the ring would
+// stand full (8 tokens, 64 experts of 4096 x 1536: 90 -> 85 us); at a run's last
+// tile, where the other warps have nothing to do, they take a column each.  A
+// finished gate/up tile is one 128-group of z, stored as operands of the down
+// product; a down
 // unit's codes are fetched whether or not z is there, and its operands once
 // every gate/up tile of its pass has been counted.  Runs are handed out by a
 // ticket, gate/up before down, to the blocks that are running, so a block
@@ -53,6 +58,16 @@
 //
 // A small launch before it writes x as operands, one after it adds the
 // routes' rows, both overlapped (programmatic dependent launch).
+//
+// Measured: 48 tokens on 64 experts of 4096 x 1536 (623 MB) take 146 us, 4.3
+// TB/s; one token on eight experts of 7168 x 2048 (182 MB) 54 us, 3.4 TB/s; the
+// smallest calls 14 us.  About 25 us of each large call are latency: the plan and
+// the first codes 5 to 10, each product's last joins 5, two launches 5.  The
+// stream between them runs at 5.8 TB/s; a ninth token on an expert is a second
+// pass over its codes (8 of the 48-token call's 72 passes), as one pass of
+// sixteen columns needs the registers or a second read of shared memory: 190 us.
+// Bringing the down product's codes into L2 while z is awaited takes bandwidth
+// from the gate/up runs still under way: 148 us and more.
 #include "common.cuh"
 #include "kernels.h"
 #include "tensormap.h"
@@ -74,13 +89,15 @@ constexpr int kBoxBytes = kBoxRows * 128;   // two 128-groups of a box's codes
 constexpr int kOpBytes = 288;     // operand record of a group: 256 bytes, its tail, padding
 constexpr int kColBytes = 2 * kOpBytes;     // one column of a unit (64 mod 128: no bank conflicts)
 constexpr int kStageBytes = 2 * kBoxBytes + kCols * kColBytes;
-constexpr int kStages = 3;
+constexpr int kStages = 3;        // three or two: the same within 1 % (146 and 145 us with 48 tokens)
 // A run's units at least.  One token, one expert of 7168 x 2048: 24 us; with four
 // 28, with eight 32; with one the joins cost more (two experts 34 us for 31).
 constexpr int kRunUnits = 2;
 constexpr int kMaxRoutes = kW4MaxTokens * 32;
 constexpr int kMaxPasses = 1024 + kMaxRoutes / kCols;
-constexpr int kShareColumns = 3;  // of a run's last tile: as many columns are shared among the warps
+// Columns of a run's last tile from which on its warps share the finish: 48 tokens
+// 146 us (154 without), one token, one column, 53.4 (54.5 with).
+constexpr int kShareColumns = 3;
 constexpr int kTileRows = 2 * kBoxRows;
 constexpr int kTileSums = kCols * kTileRows;   // a tile's sums, by column
 

@@ -23,6 +23,13 @@
 // largest by one more redux, where the lane alone would walk its registers.
 // Scores are computed up front only where they choose (a bias, or sums of two);
 // otherwise lane k computes the k-th chosen one at the end, from its logit.
+// The two score functions are kernels of their own: the test for which, per
+// expert, was a twelfth of the time.
+//
+// Measured: 16384 tokens x 256 experts (sigmoid, bias, the best 4 of 8 groups by
+// sums of two, K = 8; 18 MB) take 17.5 us, 1 TB/s, at 3 instructions a clock; 256
+// tokens x 64 experts 3.3 us, launch latency.  The lane with the maximum walking
+// its own registers instead of shared memory: 23.5 us.
 #include "common.cuh"
 #include "kernels.h"
 
