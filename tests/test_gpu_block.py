@@ -124,3 +124,18 @@ def test_refusals():
         lane.dispatch_fp8(torch.zeros(8, 256, dtype=torch.uint8, device=DEV),
                           torch.zeros(8, 2, device=DEV),
                           torch.zeros(8, 2, dtype=torch.int64, device=DEV))
+
+
+def test_router_status_is_kept():
+    """A forward leaves the projection's status alone: clear if it was, and a
+    timeout until the caller has read it."""
+    x, r, nw, rw = _layer(4, 8, 256, 9, torch.bfloat16)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    w13, s13 = _weights(g, 8, 2 * 128, 256)
+    w2, s2 = _weights(g, 8, 256, 128)
+    block = RoutedBlock(4, 8, 2, 256, 128, nw, rw, w4=True)
+    block.forward(x, r, w13, s13, w2, s2)
+    assert block.router_status.tolist() == [0, 0] and block.dev_status.tolist() == [0, 0]
+    block.router_status[0] = 4
+    block.forward(x, r, w13, s13, w2, s2)
+    assert block.router_status.tolist() == [4, 0] and block.dev_status.tolist() == [0, 0]

@@ -36,6 +36,7 @@ class RoutedBlock:
         self.logits = torch.empty(T, E, dtype=torch.float32, device=d)
         self.topk_idx = torch.empty(T, K, dtype=torch.int32, device=d)
         self.topk_w = torch.empty(T, K, dtype=torch.float32, device=d)
+        self.router_status = torch.zeros(2, dtype=torch.int32, device=d)
         self.hq = self.hs = self.lane = self.workspace = None
         if w4:
             if T > api.W4_MAX_TOKENS:
@@ -54,11 +55,14 @@ class RoutedBlock:
     def forward(self, x, residual, w13, w13_scale, w2, w2_scale, *, stream=None):
         """``x [T, H]`` bf16 (the sublayer before) joins ``residual [T, H]``
         (bf16 or fp32, updated in place).  Returns the routed branch's ``y
-        [T, H]`` bf16, the block's own buffer; ``dev_status`` as of the calls."""
+        [T, H]`` bf16, the block's own buffer; ``dev_status`` as of the calls,
+        and ``router_status``, which keeps a timeout of the projection until
+        the caller clears it."""
         api.moe_add_rms_norm(x, self.norm_weight, self.eps, residual=residual,
                              residual_out=residual, y=self.h, yq=self.hq, ys=self.hs,
                              stream=stream)
-        api.moe_router_logits(self.h, self.router_weight, logits=self.logits, stream=stream)
+        api.moe_router_logits(self.h, self.router_weight, logits=self.logits,
+                              dev_status=self.router_status, stream=stream)
         api.moe_router_topk(self.logits, self.K, topk_idx=self.topk_idx, topk_w=self.topk_w,
                             stream=stream, **self.router)
         if self.w4:
