@@ -59,10 +59,10 @@
 // A small launch before it writes x as operands, one after it adds the
 // routes' rows, both overlapped (programmatic dependent launch).
 //
-// Measured: 48 tokens on 64 experts of 4096 x 1536 (623 MB) take 146 us, 4.3
+// Measured: 48 tokens on 64 experts of 4096 x 1536 (623 MB) take 144 us, 4.3
 // TB/s; one token on eight experts of 7168 x 2048 (182 MB) 54 us, 3.4 TB/s; the
 // smallest calls 14 us.  About 25 us of each large call are latency: the plan and
-// the first codes 5 to 10, each product's last joins 5, two launches 5.  The
+// the first codes 6 to 9, each product's last joins 5, two launches 5.  The
 // stream between them runs at 5.8 TB/s; a ninth token on an expert is a second
 // pass over its codes (8 of the 48-token call's 72 passes), as one pass of
 // sixteen columns needs the registers or a second read of shared memory: 190 us.
@@ -237,29 +237,35 @@ __global__ void __launch_bounds__(kPrepThreads) w4_prepare_kernel(const W4Args a
 
 // --------------------------------------------------------------------- plan
 // The passes in ascending expert and their routes in ascending route id.  A
-// token's second route to one expert is left out (its first stands for both).
-// `scratch` holds 1032 ints and 2 * T * K shorts and is free again afterwards.
-// Returns the number of passes.  Every thread of the block calls it.
+// token's second route to one expert is left out (its first stands for both),
+// so an expert's routes are a set of tokens, and a route's place among them the
+// number of lower ones.  `scratch` holds kPlanScratch bytes and T * K shorts
+// and is free again afterwards.  Returns the number of passes.  Every thread
+// of the block calls it.
+constexpr int kPlanScratch = 1024 * 8 + 1024 * 4 + 8 * 4;
 template <typename IdT>
-__device__ int w4_plan(const W4Args& a, uint32_t* passes, uint16_t* routes, int* scratch) {
+__device__ int w4_plan(const W4Args& a, uint32_t* passes, uint16_t* routes, uint8_t* scratch) {
   const IdT* topk_idx = static_cast<const IdT*>(a.topk_idx);
   const int n = a.T * a.K, E = a.E, tid = threadIdx.x, lane = tid & 31;
-  int* pos = scratch;                       // [1024] counts, then next free place
-  int* warp_sum = scratch + 1024;           // [8]
-  int16_t* ids = reinterpret_cast<int16_t*>(scratch + 1032);   // [n]
-  int16_t* kept = ids + n;                  // [n] -1 for none and for a repeat
-  for (int e = tid; e < 1024; e += blockDim.x) pos[e] = 0;
+  uint64_t* tokens = reinterpret_cast<uint64_t*>(scratch);   // [1024] an expert's tokens
+  int* first = reinterpret_cast<int*>(tokens + 1024);        // [1024] its first route's place
+  int* warp_sum = first + 1024;                              // [8]
+  int16_t* ids = reinterpret_cast<int16_t*>(warp_sum + 8);   // [n]
+  for (int e = tid; e < 1024; e += blockDim.x) tokens[e] = 0;
   for (int i = tid; i < n; i += blockDim.x) {
     const int64_t id = static_cast<int64_t>(topk_idx[i]);
     ids[i] = id >= 0 && id < E ? static_cast<int16_t>(id) : int16_t{-1};
   }
   __syncthreads();
-  for (int i = tid; i < n; i += blockDim.x) {
+  auto kept = [&](int i, int t) {
     int e = ids[i];
-    for (int j = i - i % a.K; j < i; ++j)
+    for (int j = t * a.K; j < i; ++j)
       if (ids[j] == e) e = -1;
-    kept[i] = static_cast<int16_t>(e);
-    if (e >= 0) atomicAdd(&pos[e], 1);
+    return e;
+  };
+  for (int i = tid; i < n; i += blockDim.x) {
+    const int t = i / a.K, e = ids[i];
+    if (e >= 0) atomicOr(reinterpret_cast<uint32_t*>(tokens + e) + (t >> 5), 1u << (t & 31));
   }
   __syncthreads();
   // prefixes of the routes (low half) and the passes (high half): thread i has
@@ -268,7 +274,7 @@ __device__ int w4_plan(const W4Args& a, uint32_t* passes, uint16_t* routes, int*
   if (tid < 256) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      c[j] = pos[4 * tid + j];
+      c[j] = __popcll(tokens[4 * tid + j]);
       sum += c[j] + ((c[j] + kCols - 1) / kCols << 16);
     }
     incl = sum;
@@ -291,21 +297,14 @@ __device__ int w4_plan(const W4Args& a, uint32_t* passes, uint16_t* routes, int*
       const int np = (c[j] + kCols - 1) / kCols, off = at & 0xffff;
       for (int p = 0; p < np; ++p)
         passes[(at >> 16) + p] = pack_pass(4 * tid + j, min(kCols, c[j] - p * kCols), off + p * kCols);
-      pos[4 * tid + j] = off;
+      first[4 * tid + j] = off;
       at += c[j] + (np << 16);
     }
   }
   __syncthreads();
-  if (tid < 32) {
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int i = i0 + lane;
-      const int e = i < n ? kept[i] : -1;
-      const unsigned peers = __match_any_sync(0xffffffffu, e);
-      if (e >= 0) routes[pos[e] + __popc(peers & ((1u << lane) - 1u))] = static_cast<uint16_t>(i);
-      __syncwarp();
-      if (e >= 0 && lane == __ffs(peers) - 1) pos[e] += __popc(peers);
-      __syncwarp();
-    }
+  for (int i = tid; i < n; i += blockDim.x) {
+    const int t = i / a.K, e = kept(i, t);
+    if (e >= 0) routes[first[e] + __popcll(tokens[e] & ((1ull << t) - 1))] = static_cast<uint16_t>(i);
   }
   // the scratch becomes a ring that TMA writes
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -578,7 +577,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     tma_prefetch_desc(&maps.w13);
     tma_prefetch_desc(&maps.w2);
   }
-  const int np = w4_plan<IdT>(a, passes, routes, reinterpret_cast<int*>(ring));
+  const int np = w4_plan<IdT>(a, passes, routes, ring);
   const Product prod[2] = {product_of(a, false, np), product_of(a, true, np)};
   const int runs = prod[0].nb + prod[1].nb;
   volatile int* abort_flag = &s_abort;
@@ -948,7 +947,7 @@ template <typename IdT>
 cudaError_t launch_w4(const W4Args& a, const W4Maps& maps, int sm_count, cudaStream_t s) {
   const int smem = 1024 + kStages * kStageBytes + 4 * a.max_passes + 2 * a.T * a.K;
   constexpr int kMaxSmem = 1024 + kStages * kStageBytes + 4 * kMaxPasses + 2 * kMaxRoutes;
-  static_assert(4 * 1032 + 4 * kMaxRoutes <= kStages * kStageBytes && kMaxSmem <= 200 * 1024,
+  static_assert(kPlanScratch + 2 * kMaxRoutes <= kStages * kStageBytes && kMaxSmem <= 200 * 1024,
                 "the plan's scratch fits the ring, the ring the SM");
   cudaError_t err = cudaFuncSetAttribute(w4_stream_kernel<IdT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
