@@ -200,3 +200,25 @@ def test_workspace_contents_do_not_matter():
     for i in range(100):
         ws.fill_(0xFF if i & 1 else 0x7E)
         assert torch.equal(api.moe_experts_w4(*args, workspace=ws), want)
+
+
+@pytest.mark.parametrize("T,E,K,H,I", [(48, 16, 4, 2048, 1024), (64, 8, 4, 1024, 1408), (20, 64, 2, 4096, 640)])
+def test_same_bits_beside_other_work(T, E, K, H, I):
+    """Whole and shared tiles, passes of every width: the same bits again and
+    again, also while another stream keeps part of the GPU busy."""
+    args = _case(T, E, K, H, I, 17)
+    want = _check(args)
+    other = torch.cuda.Stream()
+    a = torch.randn(2048, 2048, device=DEV)
+    other.wait_stream(torch.cuda.current_stream())
+    for i in range(60):
+        if i >= 30:
+            with torch.cuda.stream(other):
+                a = torch.sin(a)
+        assert torch.equal(api.moe_experts_w4(*args), want)
+    other.synchronize()
+
+
+def test_most_experts_tokens_and_routes():
+    """1024 experts, 64 tokens, 32 routes each: the largest plan."""
+    _check(_case(64, 1024, 32, 128, 128, 23))
