@@ -63,31 +63,56 @@ __device__ __forceinline__ float logit_value(LogitT v) {
   if constexpr (sizeof(LogitT) == 2) return __uint_as_float(static_cast<uint32_t>(v) << 16);
   else return v;
 }
-// The lane's V logits; -inf past E and for NaN.
-template <typename LogitT, int V>
-__device__ __forceinline__ void load_logits(float* l, const LogitT* row, int e0, int E, bool vec) {
-  constexpr int kBytes = V * static_cast<int>(sizeof(LogitT));
-  LogitT raw[V];
-  if (kBytes >= 4 && vec) {
-    if (e0 < E) {
-      if constexpr (kBytes >= 16) {
+// Words of a lane's V values in the warp's shared memory: 16-byte accesses of
+// neighbouring lanes meet different banks.
+__host__ __device__ constexpr int lane_words(int V) { return V >= 8 ? V + 4 : V; }
+template <int V>
+__device__ __forceinline__ int word_of(int e) { return e / V * lane_words(V) + e % V; }
+
+// The lane's V values of a row of E, from e0 on, or `past` beyond it.  vec: whole
+// 16-byte vectors (all V where those are shorter) end with the row and are
+// aligned.  Otherwise long rows come in through the warp's shared memory, as a
+// lane's own values are V apart from the next lane's: 600 experts 22 us without.
+template <int V, typename T>
+__device__ __forceinline__ void load_row(float* v, const T* row, int e0, int E, bool vec, float past,
+                                         float* stage) {
+  constexpr int kVec = V * static_cast<int>(sizeof(T)) >= 16 ? 16 / static_cast<int>(sizeof(T)) : V;
+  const int lane = threadIdx.x & 31;
+  if (kVec * sizeof(T) >= 4 && vec) {
 #pragma unroll
-        for (int i = 0; i < kBytes / 16; ++i)
-          reinterpret_cast<uint4*>(raw)[i] = __ldg(reinterpret_cast<const uint4*>(row + e0) + i);
-      } else if constexpr (kBytes == 8) {
-        *reinterpret_cast<uint2*>(raw) = __ldg(reinterpret_cast<const uint2*>(row + e0));
-      } else if constexpr (kBytes == 4) {
-        *reinterpret_cast<uint32_t*>(raw) = __ldg(reinterpret_cast<const uint32_t*>(row + e0));
+    for (int i = 0; i < V; i += kVec) {
+      T raw[kVec];
+      if (e0 + i < E) {
+        if constexpr (kVec * sizeof(T) == 16)
+          *reinterpret_cast<uint4*>(raw) = __ldg(reinterpret_cast<const uint4*>(row + e0 + i));
+        else if constexpr (kVec * sizeof(T) == 8)
+          *reinterpret_cast<uint2*>(raw) = __ldg(reinterpret_cast<const uint2*>(row + e0 + i));
+        else if constexpr (kVec * sizeof(T) == 4)
+          *reinterpret_cast<uint32_t*>(raw) = __ldg(reinterpret_cast<const uint32_t*>(row + e0 + i));
       }
-    }
 #pragma unroll
-    for (int j = 0; j < V; ++j) l[j] = e0 < E ? logit_value(raw[j]) : -INFINITY;
+      for (int k = 0; k < kVec; ++k) v[i + k] = e0 + i < E ? logit_value(raw[k]) : past;
+    }
+  } else if constexpr (V >= 8) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = 32 * i + lane;
+      stage[word_of<V>(e)] = e < E ? logit_value(__ldg(row + e)) : past;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+      *reinterpret_cast<float4*>(v + i) = *reinterpret_cast<const float4*>(stage + lane * lane_words(V) + i);
+    __syncwarp();
   } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) l[j] = e0 + j < E ? logit_value(__ldg(row + e0 + j)) : -INFINITY;
+    for (int i = 0; i < V; ++i) v[i] = e0 + i < E ? logit_value(__ldg(row + e0 + i)) : past;
   }
-#pragma unroll
-  for (int j = 0; j < V; ++j) l[j] = l[j] == l[j] ? l[j] : -INFINITY;
+}
+template <int V, typename T>
+bool row_vectors(const T* rows, int E) {
+  constexpr int kVec = V * static_cast<int>(sizeof(T)) >= 16 ? 16 / static_cast<int>(sizeof(T)) : V;
+  return E % kVec == 0 && (reinterpret_cast<uintptr_t>(rows) & (kVec * sizeof(T) - 1)) == 0;
 }
 
 // 1 / (1 + exp(-l)): each step rounded to nearest.
@@ -102,20 +127,33 @@ struct Best {
   }
 };
 
+// The best two over each run of `lanes` (a power of two) lanes.
+__device__ __forceinline__ Best best_of(Best best, int lanes) {
+  for (int o = 1; o < lanes; o <<= 1) {
+    const float oa = __shfl_xor_sync(kFull, best.a, o), ob = __shfl_xor_sync(kFull, best.b, o);
+    best.b = fmaxf(fmaxf(best.b, ob), fminf(best.a, oa));
+    best.a = fmaxf(best.a, oa);
+  }
+  return best;
+}
+
 template <typename LogitT, int V, bool kSigmoid>
 __global__ void router_topk_kernel(const TopkArgs a, const bool vec, const bool vec_bias) {
-  extern __shared__ __align__(16) uint32_t s_keys[];   // [warps][32 * V]
+  extern __shared__ __align__(16) uint32_t s_keys[];   // [warps][32 * lane_words(V)]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * (blockDim.x >> 5) + warp;
   if (t >= a.T) return;
   const int E = a.E, e0 = lane * V;
-  uint32_t* keys = s_keys + warp * 32 * V;
+  constexpr int W = lane_words(V);
+  uint32_t* keys = s_keys + warp * 32 * W;
   const LogitT* row = static_cast<const LogitT*>(a.logits) + static_cast<int64_t>(t) * E;
   const bool biased = a.bias != nullptr;
   const bool sums = a.groups > 1 && a.top == 2;   // groups by sums of two scores
 
   float l[V];
-  load_logits<LogitT, V>(l, row, e0, E, vec);
+  load_row<V>(l, row, e0, E, vec, -INFINITY, reinterpret_cast<float*>(keys));
+#pragma unroll
+  for (int j = 0; j < V; ++j) l[j] = l[j] == l[j] ? l[j] : -INFINITY;   // NaN is masked
   // softmax: the maximum, and the sum of the exponentials (1 at the maximum
   // itself, so an infinite logit takes the whole weight).  Where the largest is
   // always among the chosen and the weights are renormalised, the sum cancels.
@@ -150,16 +188,7 @@ __global__ void router_topk_kernel(const TopkArgs a, const bool vec, const bool 
   float value[V];
   if (biased) {
     float b[V];
-    if (V % 4 == 0 && vec_bias) {
-      if (e0 < E) {
-#pragma unroll
-        for (int j = 0; j < V / 4; ++j)
-          reinterpret_cast<float4*>(b)[j] = __ldg(reinterpret_cast<const float4*>(a.bias + e0) + j);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) b[j] = e0 + j < E ? __ldg(a.bias + e0 + j) : 0.f;
-    }
+    load_row<V>(b, a.bias, e0, E, vec_bias, 0.f, reinterpret_cast<float*>(keys));
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       if (!kSigmoid) s[j] = __fdiv_rn(s[j], den);
@@ -184,19 +213,28 @@ __global__ void router_topk_kernel(const TopkArgs a, const bool vec, const bool 
     if (aligned) {
 #pragma unroll
       for (int j = 0; j < V; ++j) best.add(value[j]);
-      for (int o = 1; o < span; o <<= 1) {
-        const float oa = __shfl_xor_sync(kFull, best.a, o), ob = __shfl_xor_sync(kFull, best.b, o);
-        best.b = fmaxf(fmaxf(best.b, ob), fminf(best.a, oa));
-        best.a = fmaxf(best.a, oa);
-      }
+      best = best_of(best, span);
     } else {
+      float* values = reinterpret_cast<float*>(keys);
+      if constexpr (V >= 8) {
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (e0 + j < E) reinterpret_cast<float*>(keys)[e0 + j] = value[j];
+        for (int j = 0; j < V; j += 4)
+          *reinterpret_cast<float4*>(values + lane * W + j) =
+              make_float4(value[j], value[j + 1], value[j + 2], value[j + 3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) values[e0 + j] = value[j];
+      }
       __syncwarp();
-      if (lane < a.groups)
-        for (int i = 0; i < size; ++i) best.add(reinterpret_cast<float*>(keys)[lane * size + i]);
-      __syncwarp();
+      // as many lanes a group as there are (a power of two), group after group
+      const int log_lanes = __clz(a.groups - 1) - 27;
+      const int g = lane >> log_lanes, lanes = 1 << log_lanes;
+      if (g < a.groups)
+        for (int i = lane & (lanes - 1); i < size; i += lanes)
+          best.add(values[word_of<V>(g * size + i)]);
+      best = best_of(best, lanes);
+      best.a = __shfl_sync(kFull, best.a, lane << log_lanes);   // lane g's own
+      best.b = __shfl_sync(kFull, best.b, lane << log_lanes);
     }
     const bool mine = aligned ? e0 < E : lane < a.groups;
     if (mine) gk = choice_key(a.top == 2 && best.b > -INFINITY ? __fadd_rn(best.a, best.b) : best.a);
@@ -243,7 +281,7 @@ __global__ void router_topk_kernel(const TopkArgs a, const bool vec, const bool 
   if constexpr (V % 4 == 0) {
 #pragma unroll
     for (int j = 0; j < V; j += 4)
-      *reinterpret_cast<uint4*>(keys + e0 + j) = make_uint4(key[j], key[j + 1], key[j + 2], key[j + 3]);
+      *reinterpret_cast<uint4*>(keys + lane * W + j) = make_uint4(key[j], key[j + 1], key[j + 2], key[j + 3]);
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j) keys[e0 + j] = key[j];
@@ -254,11 +292,11 @@ __global__ void router_topk_kernel(const TopkArgs a, const bool vec, const bool 
     const uint32_t top = __reduce_max_sync(kFull, lm);
     if (top == 0u) break;
     const int src = __ffs(__ballot_sync(kFull, lm == top)) - 1;
-    uint32_t v = lane < V ? keys[src * V + lane] : 0u;
+    uint32_t v = lane < V ? keys[src * W + lane] : 0u;
     const int j = __ffs(__ballot_sync(kFull, v == top)) - 1;
     if (lane == j) {
       v = 0u;
-      keys[src * V + j] = 0u;
+      keys[src * W + j] = 0u;
     }
     const uint32_t rest = __reduce_max_sync(kFull, v);
     if (lane == src) lm = rest;
@@ -290,11 +328,10 @@ template <typename LogitT, int V>
 cudaError_t launch_topk_v(const TopkArgs& a, cudaStream_t s) {
   constexpr int warps = 8;   // tokens of a block: 16384 x 64 9.1 us (one token a block 11.7, 256 tokens 3.3 and 3.4)
   const int grid = (a.T + warps - 1) / warps;
-  constexpr int kBytes = V * static_cast<int>(sizeof(LogitT));
-  const bool vec = a.E % V == 0 && (reinterpret_cast<uintptr_t>(a.logits) & (std::min(kBytes, 16) - 1)) == 0;
-  const bool vec_bias = V % 4 == 0 && a.E % V == 0 && (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0;
+  const bool vec = row_vectors<V>(static_cast<const LogitT*>(a.logits), a.E);
+  const bool vec_bias = row_vectors<V>(a.bias, a.E);
   auto* kernel = a.sigmoid ? router_topk_kernel<LogitT, V, true> : router_topk_kernel<LogitT, V, false>;
-  kernel<<<grid, warps * 32, warps * 32 * V * 4, s>>>(a, vec, vec_bias);
+  kernel<<<grid, warps * 32, warps * 32 * lane_words(V) * 4, s>>>(a, vec, vec_bias);
   return cudaGetLastError();
 }
 
