@@ -47,8 +47,8 @@
 // a tile that several runs share the last to finish adds them in run order, so
 // the order of every sum is fixed by the routes alone.  A warp of its own does
 // that, as a join and what follows it take about 5 us in which the ring would
-// stand full (8 tokens, 64 experts of 4096 x 1536: 90 -> 85 us); at a run's last
-// tile, where the other warps have nothing to do, they take a column each.  A
+// stand full (8 tokens, 64 experts of 4096 x 1536: 90 -> 85 us); where the other
+// warps have nothing to do, at a run's last tile, they take a column each.  A
 // finished gate/up tile is one 128-group of z, stored as operands of the down
 // product; a down
 // unit's codes are fetched whether or not z is there, and its operands once
@@ -95,8 +95,10 @@ constexpr int kStages = 3;        // three or two: the same within 1 % (146 and 
 constexpr int kRunUnits = 2;
 constexpr int kMaxRoutes = kW4MaxTokens * 32;
 constexpr int kMaxPasses = 1024 + kMaxRoutes / kCols;
-// Columns of a run's last tile from which on its warps share the finish: 48 tokens
-// 146 us (154 without), one token, one column, 53.4 (54.5 with).
+// Columns from which on the warps share the finish of a run's last tile, and of
+// both tiles of a run that is no longer than one: 48 tokens on 64 experts 146 us
+// (154 with the finisher alone), 17 tokens on eight of 2560 x 896 38 (43 with only the
+// last shared); one token, one column, 53.4 (54.5 shared).
 constexpr int kShareColumns = 3;
 constexpr int kTileRows = 2 * kBoxRows;
 constexpr int kTileSums = kCols * kTileRows;   // a tile's sums, by column
@@ -723,10 +725,15 @@ __global__ void __launch_bounds__(kW4Threads, 2)
       const Product pr = down ? prod[1] : prod[0];
       const int b = down ? run - prod[0].nb : run;
       Walk w = walk_of(pr, b);
+      const bool is_short = w.left <= pr.units;
       for (; w.left > 0; ++tiles) {
         const Walk at = w;
         const int end = min(w.s + w.left, pr.units);
         w.next_tile(pr, end);
+        if (down && at.s == 0 && end == pr.units) {   // its rows are stored as they are
+          --tiles;
+          continue;
+        }
         if (!wait(&s_sums[tiles & 1], (tiles >> 1) & 1)) return;
         Sums from{2 * kW4MaxBlocks + static_cast<int>(blockIdx.x), 1, tiles & 1};
         if (at.s != 0 || end != pr.units) {
@@ -745,8 +752,8 @@ __global__ void __launch_bounds__(kW4Threads, 2)
           __threadfence();
         }
         const Pass pass = unpack_pass(passes[at.p]);
-        if (w.left == 0 && pass.n >= kShareColumns) {
-          // the run's last tile: the other warps have nothing else to do
+        if ((w.left == 0 || is_short) && pass.n >= kShareColumns) {
+          // the other warps have nothing else to do, or little
           if (lane == 0) {
             s_from = from;
             mbar_arrive(&s_last);
@@ -795,6 +802,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
       next[3] = two ? load_scales(sp + second + 8 * pr.G, 2 * s, pr.G) : 0u;
     };
     Walk w = walk_of(pr, b);
+    const bool is_short = w.left <= pr.units;
     scales_of(w, w.s);
     for (bool begun = true; w.left > 0; begun = false, ++tiles) {
       const Walk at = w;
@@ -838,8 +846,28 @@ __global__ void __launch_bounds__(kW4Threads, 2)
         }
       }
       // the sums of rows (row, row + 8) of both boxes and columns (2q, 2q + 1)
+      const Pass pass = unpack_pass(passes[at.p]);
+      if (down && at.s == 0 && end == pr.units) {
+        // a whole tile of the last product needs no finish: 37 tokens on 13 experts of
+        // 896 x 256, one unit a tile, 20 us (23 through the finisher)
+        const bool both = at.t * kTileRows + kBoxRows < a.H;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (2 * q + j >= pass.n) continue;
+          float* o = a.o + static_cast<int64_t>(routes[pass.off + 2 * q + j]) * a.H + at.t * kTileRows +
+                     warp * kRows + row;
+          o[0] = acc[0][j] * 0x1p24f;
+          o[8] = acc[0][2 + j] * 0x1p24f;
+          if (both) {
+            o[kBoxRows] = acc[1][j] * 0x1p24f;
+            o[kBoxRows + 8] = acc[1][2 + j] * 0x1p24f;
+          }
+        }
+        --tiles;
+        continue;
+      }
       if (!wait(&s_free[tiles & 1], ((tiles >> 1) & 1) ^ 1)) return;
-      const int n = unpack_pass(passes[at.p]).n;
+      const int n = pass.n;
       const bool shared = at.s != 0 || end != pr.units;
       float* out = sums_of(shared, down, b, shared ? !begun : tiles & 1) + 2 * q * kTileRows + warp * kRows + row;
 #pragma unroll
@@ -852,14 +880,14 @@ __global__ void __launch_bounds__(kW4Threads, 2)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_sums[tiles & 1]);
-      if (w.left == 0 && n >= kShareColumns) {
+      if ((w.left == 0 || is_short) && n >= kShareColumns) {
         // a column a warp
         if (!wait(&s_last, last_phase)) return;
         last_phase ^= 1;
         const Sums from = s_from;
         if (from.count != 0 && warp < n) {
           __threadfence();
-          w4_finish<1>(a, from, down, at, pr.row_tiles, unpack_pass(passes[at.p]), routes, warp, lane);
+          w4_finish<1>(a, from, down, at, pr.row_tiles, pass, routes, warp, lane);
           if (!down) w4_count(&a.count->pass[at.p], 1, lane);
         }
         __syncwarp();
