@@ -59,7 +59,7 @@
 // A small launch before it writes x as operands, one after it adds the
 // routes' rows, both overlapped (programmatic dependent launch).
 //
-// Measured: 48 tokens on 64 experts of 4096 x 1536 (623 MB) take 144 us, 4.3
+// Measured: 48 tokens on 64 experts of 4096 x 1536 (623 MB) take 142 us, 4.4
 // TB/s; one token on eight experts of 7168 x 2048 (182 MB) 54 us, 3.4 TB/s; the
 // smallest calls 14 us.  About 25 us of each large call are latency: the plan and
 // the first codes 6 to 9, each product's last joins 5, two launches 5.  The

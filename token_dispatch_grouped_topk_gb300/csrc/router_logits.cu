@@ -22,9 +22,9 @@
 // products of a step last 540 clocks, so 48 KB bound the kernel (the same with w
 // multicast to both CTAs, which spares L2 but not the SM's intake: 67 us).
 // Measured: 16384 tokens x 256 experts of 7168 (255 MB, 60 GFLOP) take 51 us, 5 TB/s
-// and 1.18 PFLOP/s, with products half the time (one CTA a tile: 54); the first
-// loads and the last tile's epilogue are not hidden, one tile a CTA, and 24 of
-// 152 SMs have none.  256 tokens x 64 experts of 4096 take 7.6 us, one token 6.7:
+// and 1.18 PFLOP/s (one CTA a tile: 54): about 40 us of HBM, the products' 32 behind
+// it; the first loads and the epilogue of a CTA's one tile are not hidden, and 24
+// of 152 SMs have none.  256 tokens x 64 experts of 4096 take 7.6 us, one token 6.7:
 // launch, first load and the sum over the cluster.
 // Every wait is bounded.  One that runs out makes the whole tile NaN, which the
 // choice of experts masks, and raises MOE_DEV_TIMEOUT where a status is given.
