@@ -718,6 +718,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
     for (int i = 0, tiles = 0;; ++i) {
       if (!wait(&s_run_full[i & 1], (i >> 1) & 1)) return;
       const int run = s_run[i & 1];
+      __threadfence_block();   // as for a stage below
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_run_empty[i & 1]);
       if (run >= runs) return;
@@ -781,6 +782,7 @@ __global__ void __launch_bounds__(kW4Threads, 2)
   for (int i = 0, tiles = 0;; ++i) {
     if (!wait(&s_run_full[i & 1], (i >> 1) & 1)) return;
     const int run = s_run[i & 1];
+    __threadfence_block();   // as for a stage below
     __syncwarp();
     if (lane == 0) mbar_arrive(&s_run_empty[i & 1]);
     if (run >= runs) return;
