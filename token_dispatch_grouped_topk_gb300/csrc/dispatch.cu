@@ -489,6 +489,10 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
 // vectors and its first scales are requested before the block finds its routes'
 // slots, which takes longer than the loads; further tokens follow eight vectors
 // at a time.
+// The counting kernels still write `base` and `counts` while this one's first
+// blocks run, so both are read after the wait, from L2, and neither is a const
+// __restrict__ pointer: that would let them be read through the read-only path,
+// which is for data that nobody writes in a kernel's lifetime.
 // Measured: 4096 tokens of 4096 to 8 of 128 skewed experts (127 MB) take 29 us with
 // the counting launches, 4.4 TB/s (33 from call to call; 41 with the loads after
 // the slots and the launches one after the other).  256 tokens to 64 experts, one
@@ -497,16 +501,16 @@ template <typename IdT, bool kSingle>
 __global__ void __launch_bounds__(kDispatchWarps * 32)
     route_scatter_codes_kernel(const uint4* __restrict__ tq, const float* __restrict__ ts,
                                const IdT* __restrict__ topk_idx, int T, int H, int K, int E,
-                               RowLayout rl, int nblocks, const int32_t* __restrict__ base,
-                               int32_t* __restrict__ counts, uint4* __restrict__ xq,
-                               float* __restrict__ xs, int32_t* __restrict__ src_map,
-                               int32_t* dev_status, int groups_per_slice, int log_u) {
+                               RowLayout rl, int nblocks, const int32_t* base, int32_t* counts,
+                               uint4* __restrict__ xq, float* __restrict__ xs,
+                               int32_t* __restrict__ src_map, int32_t* dev_status,
+                               int groups_per_slice, int log_u) {
   extern __shared__ int smem[];
   int* s_cnt = smem;                           // [kDispatchWarps][E]
   int* s_dest = smem + kDispatchWarps * E;     // [kDispatchWarps][32]
   int* s_rows = s_dest + kDispatchWarps * 32;  // [E + 1] packed row bases
   int* s_prev = s_rows + E + 1;                // single pass: [E]
-  int* s_tot = s_prev + E;                     //              [E]
+  int* s_tot = s_prev + E;                     //              [E]; packed: the kept counts
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gw = blockIdx.x * kDispatchWarps + warp;
   const int tpw = 32 / K;
@@ -533,11 +537,16 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
   if (lane < tokens * ng) sc = __ldg(ts + static_cast<size_t>(t0 + lane / ng) * G + g0 + lane % ng);
 
   for (int i = threadIdx.x; i < kDispatchWarps * E; i += blockDim.x) s_cnt[i] = 0;
-  if (!kSingle) chain_wait();
-  if (kSingle)
+  if (kSingle) {
     single_pass_bases(topk_idx, T, K, E, rl, s_prev, s_tot, s_rows, counts, dev_status);
-  else if (rl.packed)
-    expert_prefix(counts, E, rl.R, 1, 1, s_rows, nullptr);
+  } else {
+    chain_wait();
+    if (rl.packed) {
+      for (int e = threadIdx.x; e < E; e += blockDim.x) s_tot[e] = __ldcg(counts + e);
+      __syncthreads();
+      expert_prefix(s_tot, E, rl.R, 1, 1, s_rows, nullptr);
+    }
+  }
   __syncthreads();
   const RouteLane r = load_route(topk_idx, T, K, E, gw, lane, nullptr);
   const unsigned peers = __match_any_sync(0xffffffffu, r.e);
@@ -546,7 +555,8 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
   __syncthreads();
   int q = -1;
   if (r.e >= 0) {
-    int sl = (kSingle ? s_prev[r.e] : base[static_cast<size_t>(r.e) * nblocks + blockIdx.x]) +
+    int sl = (kSingle ? s_prev[r.e]
+                      : __ldcg(base + static_cast<size_t>(r.e) * nblocks + blockIdx.x)) +
              lane_rank;
     for (int w = 0; w < warp; ++w) sl += s_cnt[w * E + r.e];
     if (sl < rl.R) q = (rl.packed ? s_rows[r.e] : r.e * rl.R) + sl;
