@@ -532,8 +532,8 @@ moe_status moe_dispatch_fp8(const uint8_t* tq, const float* ts, const void* topk
  *   w13_scale  device, BF16 [E, 2I, H/128]
  *   w2         device, uint8 [E, H, I/2];  w2_scale device, BF16 [E, H, I/128]
  *              (x, codes and scales 16-byte aligned)
- *   y          device out, BF16 [T, H]: the weighted sum in fp32 over k
- *              ascending; zeros for a token without a route
+ *   y          device out, BF16 [T, H], 8-byte aligned: the weighted sum in fp32
+ *              over k ascending; zeros for a token without a route
  *   dev_status device, int32 [2]: reset, then MOE_DEV_* bits (no capacity, so
  *              nothing is dropped)
  *   workspace  device, moe_experts_w4_workspace_size(T, K, H, I) bytes, 256-byte

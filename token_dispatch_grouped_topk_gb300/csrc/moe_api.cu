@@ -489,7 +489,7 @@ moe_status moe_experts_w4(const void* x, const void* topk_idx, int idx_bits, con
       (T > 0 && (x == nullptr || topk_idx == nullptr || topk_w == nullptr || y == nullptr)))
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w13) || !aligned16(w2) || !aligned16(w13_scale) ||
-      !aligned16(w2_scale))
+      !aligned16(w2_scale) || (reinterpret_cast<uintptr_t>(y) & 7u) != 0)
     return MOE_ERR_INVALID_ARG;
   if (workspace == nullptr || workspace_bytes < moe_experts_w4_workspace_size(T, K, H, I) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
