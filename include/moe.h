@@ -57,7 +57,7 @@ typedef enum {
   MOE_OK = 0,
   MOE_ERR_INVALID_ARG = -1, /* null pointer, negative or inconsistent size */
   MOE_ERR_UNSUPPORTED = -2, /* device is not sm_103, or a size outside the limits above */
-  MOE_ERR_WORKSPACE = -3,   /* workspace pointer null or smaller than *_workspace_size() */
+  MOE_ERR_WORKSPACE = -3,   /* workspace pointer null, misaligned or smaller than *_workspace_size() */
   MOE_ERR_CUDA = -4         /* a CUDA runtime call failed (see cudaGetLastError) */
 } moe_status;
 

@@ -24,6 +24,7 @@ static_assert(kW4MaxTokens == MOE_W4_MAX_TOKENS && kMaxRouterGroups == MOE_MAX_R
               "the header's limits are the kernels'");
 constexpr size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }   // int32 workspaces
 }  // namespace
 
 const DeviceInfo* current_device_info() {
@@ -200,7 +201,7 @@ moe_status moe_dispatch_ex(const void* x, const void* topk_idx, int idx_bits, co
     rl = RowLayout{R, 1, rows};
   }
   const size_t need = moe_dispatch_workspace_size(T, K, E);
-  if (workspace == nullptr || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  if (workspace == nullptr || workspace_bytes < need || !aligned4(workspace)) return MOE_ERR_WORKSPACE;
   const DeviceInfo* dev = nullptr;
   if (moe_status st = check_device(&dev); st != MOE_OK) return st;
   return from_cuda(launch_dispatch(x, topk_idx, idx_bits, T, H, K, E, rl, recv, counts, src_map,
@@ -369,7 +370,7 @@ moe_status moe_dispatch_quant_ex(const void* x, const void* topk_idx, int idx_bi
     rl = RowLayout{R, 1, rows};
   }
   const size_t need = moe_dispatch_workspace_size(T, K, E);
-  if (workspace == nullptr || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  if (workspace == nullptr || workspace_bytes < need || !aligned4(workspace)) return MOE_ERR_WORKSPACE;
   const DeviceInfo* dev = nullptr;
   if (moe_status st = check_device(&dev); st != MOE_OK) return st;
   return from_cuda(launch_dispatch_quant(x, topk_idx, idx_bits, T, H, K, E, rl, xq, xs, counts,
@@ -406,7 +407,7 @@ moe_status moe_dispatch_fp8(const uint8_t* tq, const float* ts, const void* topk
     rl = RowLayout{R, 1, rows};
   }
   const size_t need = moe_dispatch_workspace_size(T, K, E);
-  if (workspace == nullptr || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  if (workspace == nullptr || workspace_bytes < need || !aligned4(workspace)) return MOE_ERR_WORKSPACE;
   const DeviceInfo* dev = nullptr;
   if (moe_status st = check_device(&dev); st != MOE_OK) return st;
   return from_cuda(launch_dispatch_fp8(tq, ts, topk_idx, idx_bits, T, H, K, E, rl, xq, xs, counts,
@@ -570,8 +571,7 @@ moe_status moe_gemm_gateup_down(const uint8_t* xq, const float* xs, const int32_
     return MOE_ERR_INVALID_ARG;
   const RowLayout rl = rows == 0 ? padded_rows(E, R) : RowLayout{R, 1, rows};
   const size_t need = gemm_sync_ints(E, rl);
-  if (sync == nullptr || sync_bytes < need * sizeof(int) ||
-      (reinterpret_cast<uintptr_t>(sync) & 3u) != 0)
+  if (sync == nullptr || sync_bytes < need * sizeof(int) || !aligned4(sync))
     return MOE_ERR_WORKSPACE;
   const DeviceInfo* dev = nullptr;
   if (moe_status st = check_device(&dev); st != MOE_OK) return st;
@@ -748,7 +748,7 @@ moe_status moe_ep_route_offsets(const int32_t* ids, int64_t S, int K, int32_t* o
                                 void* workspace, size_t workspace_bytes, moe_stream_t stream) {
   if (S < 0 || S > (int64_t{1} << 30) || K < 1 || K > 32) return MOE_ERR_INVALID_ARG;
   if (offsets == nullptr || (S > 0 && ids == nullptr)) return MOE_ERR_INVALID_ARG;
-  if (workspace == nullptr || workspace_bytes < moe_ep_offsets_workspace_size(S))
+  if (workspace == nullptr || workspace_bytes < moe_ep_offsets_workspace_size(S) || !aligned4(workspace))
     return MOE_ERR_WORKSPACE;
   const DeviceInfo* dev = nullptr;
   if (moe_status st = check_device(&dev); st != MOE_OK) return st;
