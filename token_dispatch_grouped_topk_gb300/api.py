@@ -2,7 +2,10 @@
 
 PyTorch supplies device memory, tensors' ``data_ptr()`` and the current CUDA
 stream; every computation runs in the library's sm_103a kernels.  Outputs not
-passed in are allocated with torch on the input's device.
+passed in are allocated with torch on the input's device.  With ``stream`` a
+call runs there and nowhere else: the tensors that it allocates itself stay
+whole until both that stream and the current one are done with them, while those
+passed in are the caller's to keep (or to ``record_stream``) and to order.
 """
 from __future__ import annotations
 
@@ -73,8 +76,26 @@ def expert_compute_workspace_layout(E: int, R: int, rows: int, H: int, I: int) -
     return [int(v) for v in off]
 
 
-def _workspace(nbytes, device):
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+def _new(shape, dtype, device, stream, fill=torch.empty):
+    """An output that a call allocates itself.  It is taken on the stream that
+    the call's kernels run on, behind whatever had its memory there, and is
+    marked as in use on the caller's current stream, where it is read: dropped at
+    any time, its memory goes to nobody before both are done with it."""
+    if stream is None or device.type != "cuda":
+        return fill(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = fill(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _workspace(nbytes, device, stream=None):
+    """Scratch of one call, dropped at its end: memory of the stream that the
+    kernels run on, which gives it to nobody before they have ended."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
 def _gemm_flags(w13_interleaved, gemm_launch, max_ctas=0):
@@ -116,15 +137,15 @@ def moe_dispatch(x, topk_idx, topk_w, E: int, R: int, *, recv=None, counts=None,
     bits = _idx_bits(topk_idx)
     _need(topk_idx, topk_idx.dtype, "topk_idx")
     if recv is None:
-        recv = torch.empty(E, R, H, dtype=torch.bfloat16, device=dev)
+        recv = _new((E, R, H), torch.bfloat16, dev, stream)
     if counts is None:
-        counts = torch.empty(E, dtype=torch.int32, device=dev)
+        counts = _new((E,), torch.int32, dev, stream)
     if src_map is None:
-        src_map = torch.empty(T, K, dtype=torch.int32, device=dev)
+        src_map = _new((T, K), torch.int32, dev, stream)
     if dev_status is None:
-        dev_status = torch.empty(2, dtype=torch.int32, device=dev)
+        dev_status = _new((2,), torch.int32, dev, stream)
     if workspace is None:
-        workspace = _workspace(lib.moe_dispatch_workspace_size(T, K, E), dev)
+        workspace = _workspace(lib.moe_dispatch_workspace_size(T, K, E), dev, stream)
     st = lib.moe_dispatch_ex(_p(x), _p(topk_idx), bits, _p(topk_w), T, H, K, E, R, 0, _p(recv),
                              _p(counts), _p(src_map), _p(dev_status), _p(workspace),
                              workspace.numel(), _s(stream))
@@ -147,17 +168,17 @@ def moe_dispatch_quant(x, topk_idx, topk_w, E: int, R: int, *, xq=None, xs=None,
     _need(topk_idx, topk_idx.dtype, "topk_idx")
     lead = (rows,) if rows else (E, R)
     if xq is None:
-        xq = torch.empty(*lead, H, dtype=torch.uint8, device=dev)
+        xq = _new((*lead, H), torch.uint8, dev, stream)
     if xs is None:
-        xs = torch.empty(*lead, H // 128, dtype=torch.float32, device=dev)
+        xs = _new((*lead, H // 128), torch.float32, dev, stream)
     if counts is None:
-        counts = torch.empty(E, dtype=torch.int32, device=dev)
+        counts = _new((E,), torch.int32, dev, stream)
     if src_map is None:
-        src_map = torch.empty(T, K, dtype=torch.int32, device=dev)
+        src_map = _new((T, K), torch.int32, dev, stream)
     if dev_status is None:
-        dev_status = torch.empty(2, dtype=torch.int32, device=dev)
+        dev_status = _new((2,), torch.int32, dev, stream)
     if workspace is None:
-        workspace = _workspace(lib.moe_dispatch_workspace_size(T, K, E), dev)
+        workspace = _workspace(lib.moe_dispatch_workspace_size(T, K, E), dev, stream)
     st = lib.moe_dispatch_quant_ex(_p(x), _p(topk_idx), bits, _p(topk_w), T, H, K, E, R, rows,
                                    _p(_u8(xq)), _p(xs), _p(counts), _p(src_map), _p(dev_status),
                                    _p(workspace), workspace.numel(), _s(stream))
@@ -177,11 +198,11 @@ def moe_expert_compute(recv, counts, w13, w13_scale, w2, w2_scale, *, out=None, 
     I = w13.shape[1] // 2
     dev = recv.device
     if out is None:
-        out = torch.empty(E, R, H, dtype=torch.bfloat16, device=dev)
+        out = _new((E, R, H), torch.bfloat16, dev, stream)
     if dev_status is None:
-        dev_status = torch.zeros(2, dtype=torch.int32, device=dev)
+        dev_status = _new((2,), torch.int32, dev, stream, torch.zeros)
     if workspace is None:
-        workspace = _workspace(lib.moe_expert_compute_workspace_size(E, R, H, I), dev)
+        workspace = _workspace(lib.moe_expert_compute_workspace_size(E, R, H, I), dev, stream)
     st = lib.moe_expert_compute_ex(_p(recv), _p(counts), E, R, 0, H, I, _p(w13), _p(w13_scale),
                                    _p(w2), _p(w2_scale), _p(out), _p(dev_status), _p(workspace),
                                    workspace.numel(),
@@ -206,15 +227,15 @@ def moe_dispatch_source_slots(x, topk_idx, topk_w, E: int, L: int, max_tokens: i
     bits = _idx_bits(topk_idx)
     _need(topk_idx, topk_idx.dtype, "topk_idx")
     if recv is None:
-        recv = torch.empty(E, W * max_tokens, H, dtype=torch.bfloat16, device=dev)
+        recv = _new((E, W * max_tokens, H), torch.bfloat16, dev, stream)
     if counts is None:
-        counts = torch.empty(E, dtype=torch.int32, device=dev)
+        counts = _new((E,), torch.int32, dev, stream)
     if seg_counts is None:
-        seg_counts = torch.empty(E, W, dtype=torch.int32, device=dev)
+        seg_counts = _new((E, W), torch.int32, dev, stream)
     if src_map is None:
-        src_map = torch.empty(T, K, dtype=torch.int32, device=dev)
+        src_map = _new((T, K), torch.int32, dev, stream)
     if dev_status is None:
-        dev_status = torch.empty(2, dtype=torch.int32, device=dev)
+        dev_status = _new((2,), torch.int32, dev, stream)
     st = lib.moe_dispatch_source_slots(_p(x), _p(topk_idx), bits, _p(topk_w), T, H, K, E, L,
                                        max_tokens, _p(rank_offsets), _p(recv), _p(counts),
                                        _p(seg_counts), _p(src_map), _p(dev_status), _s(stream))
@@ -235,11 +256,11 @@ def moe_expert_compute_source_slots(recv, counts, seg_counts, L: int, max_tokens
     I = w13.shape[1] // 2
     dev = recv.device
     if out is None:
-        out = torch.empty(E, R, H, dtype=torch.bfloat16, device=dev)
+        out = _new((E, R, H), torch.bfloat16, dev, stream)
     if dev_status is None:
-        dev_status = torch.zeros(2, dtype=torch.int32, device=dev)
+        dev_status = _new((2,), torch.int32, dev, stream, torch.zeros)
     if workspace is None:
-        workspace = _workspace(lib.moe_expert_compute_workspace_size(E, R, H, I), dev)
+        workspace = _workspace(lib.moe_expert_compute_workspace_size(E, R, H, I), dev, stream)
     st = lib.moe_expert_compute_source_slots(
         _p(recv), _p(counts), _p(seg_counts), E, L, max_tokens, H, I, _p(w13), _p(w13_scale),
         _p(w2), _p(w2_scale), _p(out), _p(dev_status), _p(workspace), workspace.numel(),
@@ -264,17 +285,17 @@ def moe_dispatch_quant_source_slots(x, topk_idx, topk_w, E: int, L: int, max_tok
     bits = _idx_bits(topk_idx)
     _need(topk_idx, topk_idx.dtype, "topk_idx")
     if xq is None:
-        xq = torch.empty(E, W * max_tokens, H, dtype=torch.uint8, device=dev)
+        xq = _new((E, W * max_tokens, H), torch.uint8, dev, stream)
     if xs is None:
-        xs = torch.empty(E, W * max_tokens, H // 128, dtype=torch.float32, device=dev)
+        xs = _new((E, W * max_tokens, H // 128), torch.float32, dev, stream)
     if counts is None:
-        counts = torch.empty(E, dtype=torch.int32, device=dev)
+        counts = _new((E,), torch.int32, dev, stream)
     if seg_counts is None:
-        seg_counts = torch.empty(E, W, dtype=torch.int32, device=dev)
+        seg_counts = _new((E, W), torch.int32, dev, stream)
     if src_map is None:
-        src_map = torch.empty(T, K, dtype=torch.int32, device=dev)
+        src_map = _new((T, K), torch.int32, dev, stream)
     if dev_status is None:
-        dev_status = torch.empty(2, dtype=torch.int32, device=dev)
+        dev_status = _new((2,), torch.int32, dev, stream)
     st = lib.moe_dispatch_quant_source_slots(
         _p(x), _p(topk_idx), bits, _p(topk_w), T, H, K, E, L, max_tokens, _p(rank_offsets),
         _p(_u8(xq)), _p(xs), _p(counts), _p(seg_counts), _p(src_map), _p(dev_status), _s(stream))
@@ -296,11 +317,11 @@ def moe_gemm_source_slots(xq, xs, seg_counts, L: int, max_tokens: int, w13, w13_
     I = w13.shape[1] // 2
     dev = xq.device
     if out is None:
-        out = torch.empty(E, R, H, dtype=torch.bfloat16, device=dev)
+        out = _new((E, R, H), torch.bfloat16, dev, stream)
     if dev_status is None:
-        dev_status = torch.zeros(2, dtype=torch.int32, device=dev)
+        dev_status = _new((2,), torch.int32, dev, stream, torch.zeros)
     if workspace is None:
-        workspace = _workspace(lib.moe_expert_compute_workspace_size(E, R, H, I), dev)
+        workspace = _workspace(lib.moe_expert_compute_workspace_size(E, R, H, I), dev, stream)
     st = lib.moe_gemm_source_slots(
         _p(xq), _p(xs), _p(seg_counts), E, L, max_tokens, H, I, _p(w13), _p(w13_scale), _p(w2),
         _p(w2_scale), _p(out), _p(dev_status), _p(workspace), workspace.numel(),
@@ -330,15 +351,15 @@ def moe_dispatch_packed(x, topk_idx, topk_w, E: int, R: int, *, rows=None, recv=
     if rows is None:
         rows = recv.shape[0] if recv is not None else packed_rows(T, K, E, R)
     if recv is None:
-        recv = torch.empty(rows, H, dtype=torch.bfloat16, device=dev)
+        recv = _new((rows, H), torch.bfloat16, dev, stream)
     if counts is None:
-        counts = torch.empty(E, dtype=torch.int32, device=dev)
+        counts = _new((E,), torch.int32, dev, stream)
     if src_map is None:
-        src_map = torch.empty(T, K, dtype=torch.int32, device=dev)
+        src_map = _new((T, K), torch.int32, dev, stream)
     if dev_status is None:
-        dev_status = torch.empty(2, dtype=torch.int32, device=dev)
+        dev_status = _new((2,), torch.int32, dev, stream)
     if workspace is None:
-        workspace = _workspace(lib.moe_dispatch_workspace_size(T, K, E), dev)
+        workspace = _workspace(lib.moe_dispatch_workspace_size(T, K, E), dev, stream)
     st = lib.moe_dispatch_ex(_p(x), _p(topk_idx), bits, _p(topk_w), T, H, K, E, R, rows, _p(recv),
                              _p(counts), _p(src_map), _p(dev_status), _p(workspace),
                              workspace.numel(), _s(stream))
@@ -357,11 +378,12 @@ def moe_expert_compute_packed(recv, counts, R: int, w13, w13_scale, w2, w2_scale
     I = w13.shape[1] // 2
     dev = recv.device
     if out is None:
-        out = torch.empty(rows, H, dtype=torch.bfloat16, device=dev)
+        out = _new((rows, H), torch.bfloat16, dev, stream)
     if dev_status is None:
-        dev_status = torch.zeros(2, dtype=torch.int32, device=dev)
+        dev_status = _new((2,), torch.int32, dev, stream, torch.zeros)
     if workspace is None:
-        workspace = _workspace(lib.moe_expert_compute_packed_workspace_size(rows, H, I), dev)
+        workspace = _workspace(lib.moe_expert_compute_packed_workspace_size(rows, H, I), dev,
+                               stream)
     st = lib.moe_expert_compute_ex(_p(recv), _p(counts), E, R, rows, H, I, _p(w13), _p(w13_scale),
                                    _p(w2), _p(w2_scale), _p(out), _p(dev_status), _p(workspace),
                                    workspace.numel(), _gemm_flags(w13_interleaved, gemm_launch),
@@ -432,19 +454,19 @@ def moe_add_rms_norm(x, weight, eps: float = 1e-6, *, residual=None, residual_ou
         pr = _check(residual, _HALF_OR_F32, (T, H), dev, "residual")
         rbits = _bits(residual)
         if residual_out is None:
-            residual_out = torch.empty_like(residual)
+            residual_out = _new((T, H), residual.dtype, x.device, stream)
         po = _check(residual_out, (residual.dtype,), (T, H), dev, "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out without residual")
     if y is None and bf16:
-        y = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+        y = _new((T, H), torch.bfloat16, x.device, stream)
     py = None if y is None else _check(y, _BF16, (T, H), dev, "y")
     pq = ps = None
     if quant or yq is not None or ys is not None:
         if yq is None:
-            yq = torch.empty(T, H, dtype=torch.uint8, device=x.device)
+            yq = _new((T, H), torch.uint8, x.device, stream)
         if ys is None:
-            ys = torch.empty(T, H // 128, dtype=torch.float32, device=x.device)
+            ys = _new((T, H // 128), torch.float32, x.device, stream)
         pq = _check(yq, _E4M3, (T, H), dev, "yq")
         ps = _check(ys, _F32, (T, H // 128), dev, "ys")
     st = _lib.load().moe_add_rms_norm(px, pr, rbits, pw, _bits(weight), eps, T, H, py, pq, ps, po,
@@ -460,7 +482,7 @@ def moe_router_logits(x, w, *, logits=None, dev_status=None, stream=None):
     E = w.shape[0]
     dev = x.get_device()
     if logits is None:
-        logits = torch.empty(T, E, dtype=torch.float32, device=x.device)
+        logits = _new((T, E), torch.float32, x.device, stream)
     st = _lib.load().moe_router_logits(
         _check(x, _BF16, (T, H), dev, "x"), _check(w, _BF16, (E, H), dev, "w"), T, H, E,
         _check(logits, _F32, (T, E), dev, "logits"),
@@ -485,9 +507,9 @@ def moe_router_topk(logits, K: int, *, score: str = "softmax", bias=None, groups
     if score not in _lib.SCORES:
         raise ValueError(f"score: 'softmax' or 'sigmoid', not {score!r}")
     if topk_idx is None:
-        topk_idx = torch.empty(T, K, dtype=idx_dtype, device=logits.device)
+        topk_idx = _new((T, K), idx_dtype, logits.device, stream)
     if topk_w is None:
-        topk_w = torch.empty(T, K, dtype=torch.float32, device=logits.device)
+        topk_w = _new((T, K), torch.float32, logits.device, stream)
     st = _lib.load().moe_router_topk(
         _check(logits, _HALF_OR_F32, (T, E), dev, "logits"), _bits(logits),
         None if bias is None else _check(bias, _F32, (E,), dev, "bias"), T, E, K,
@@ -510,17 +532,17 @@ def moe_dispatch_fp8(tq, ts, topk_idx, E: int, R: int, *, xq=None, xs=None, coun
     dev = tq.get_device()
     lead = (rows,) if rows else (E, R)
     if xq is None:
-        xq = torch.empty(*lead, H, dtype=torch.uint8, device=tq.device)
+        xq = _new((*lead, H), torch.uint8, tq.device, stream)
     if xs is None:
-        xs = torch.empty(*lead, H // 128, dtype=torch.float32, device=tq.device)
+        xs = _new((*lead, H // 128), torch.float32, tq.device, stream)
     if counts is None:
-        counts = torch.empty(E, dtype=torch.int32, device=tq.device)
+        counts = _new((E,), torch.int32, tq.device, stream)
     if src_map is None:
-        src_map = torch.empty(T, K, dtype=torch.int32, device=tq.device)
+        src_map = _new((T, K), torch.int32, tq.device, stream)
     if dev_status is None:
-        dev_status = torch.empty(2, dtype=torch.int32, device=tq.device)
+        dev_status = _new((2,), torch.int32, tq.device, stream)
     if workspace is None:
-        workspace = _workspace(lib.moe_dispatch_workspace_size(T, K, E), tq.device)
+        workspace = _workspace(lib.moe_dispatch_workspace_size(T, K, E), tq.device, stream)
     st = lib.moe_dispatch_fp8(
         _check(tq, _E4M3, (T, H), dev, "tq"), _check(ts, _F32, (T, H // 128), dev, "ts"),
         _check(topk_idx, _IDS, (T, K), dev, "topk_idx"), _bits(topk_idx), T, H, K, E, R, rows,
@@ -549,11 +571,11 @@ def moe_experts_w4(x, topk_idx, topk_w, w13, w13_scale, w2, w2_scale, *, y=None,
     I = n13 // 2
     dev = x.get_device()
     if y is None:
-        y = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+        y = _new((T, H), torch.bfloat16, x.device, stream)
     if dev_status is None:
-        dev_status = torch.empty(2, dtype=torch.int32, device=x.device)
+        dev_status = _new((2,), torch.int32, x.device, stream)
     if workspace is None:
-        workspace = _workspace(lib.moe_experts_w4_workspace_size(T, K, H, I), x.device)
+        workspace = _workspace(lib.moe_experts_w4_workspace_size(T, K, H, I), x.device, stream)
     st = lib.moe_experts_w4(
         _check(x, _BF16, (T, H), dev, "x"), _check(topk_idx, _IDS, (T, K), dev, "topk_idx"),
         _bits(topk_idx), _check(topk_w, _F32, (T, K), dev, "topk_w"), T, H, I, K, E,
@@ -579,7 +601,7 @@ def moe_layer_stats(topk_idx, counts, L: int, R: int, *, rank_offsets=None, stat
     T, K = topk_idx.shape
     E = counts.shape[0]
     if stats is None:
-        stats = torch.empty(len(LAYER_STATS), dtype=torch.int64, device=counts.device)
+        stats = _new((len(LAYER_STATS),), torch.int64, counts.device, stream)
     st = lib.moe_layer_stats(_p(topk_idx), _idx_bits(topk_idx), _p(counts), T, K, E, L, R,
                              _p(rank_offsets), _p(stats), _s(stream))
     _lib.check("moe_layer_stats", st)
@@ -604,7 +626,7 @@ def moe_combine_packed(out, src_map, topk_w, *, y=None, stream=None):
     rows, H = out.shape
     T, K = src_map.shape
     if y is None:
-        y = torch.empty(T, H, dtype=torch.bfloat16, device=out.device)
+        y = _new((T, H), torch.bfloat16, out.device, stream)
     st = lib.moe_combine_packed(_p(out), rows, _p(src_map), _p(topk_w), T, H, K, _p(y), _s(stream))
     _lib.check("moe_combine_packed", st)
     return y
@@ -616,7 +638,7 @@ def moe_combine(out, src_map, topk_w, *, y=None, stream=None):
     E, R, H = out.shape
     T, K = src_map.shape
     if y is None:
-        y = torch.empty(T, H, dtype=torch.bfloat16, device=out.device)
+        y = _new((T, H), torch.bfloat16, out.device, stream)
     st = lib.moe_combine(_p(out), _p(src_map), _p(topk_w), T, H, K, E, R, _p(y), _s(stream))
     _lib.check("moe_combine", st)
     return y
@@ -628,9 +650,9 @@ def moe_quantize_fp8(recv, counts, *, xq=None, xs=None, stream=None):
     lib = _lib.load()
     E, R, H = recv.shape
     if xq is None:
-        xq = torch.empty(E, R, H, dtype=torch.uint8, device=recv.device)
+        xq = _new((E, R, H), torch.uint8, recv.device, stream)
     if xs is None:
-        xs = torch.empty(E, R, H // 128, dtype=torch.float32, device=recv.device)
+        xs = _new((E, R, H // 128), torch.float32, recv.device, stream)
     st = lib.moe_quantize_fp8(_p(recv), _p(counts), E, R, H, _p(xq), _p(xs), _s(stream))
     _lib.check("moe_quantize_fp8", st)
     return xq, xs
@@ -645,11 +667,11 @@ def moe_gemm_gateup_silu(xq, xs, counts, w13, w13_scale, *, zq=None, zs=None, de
     I = w13.shape[1] // 2
     dev = xq.device
     if zq is None:
-        zq = torch.empty(E, R, I, dtype=torch.uint8, device=dev)
+        zq = _new((E, R, I), torch.uint8, dev, stream)
     if zs is None:
-        zs = torch.empty(E, R, I // 128, dtype=torch.float32, device=dev)
+        zs = _new((E, R, I // 128), torch.float32, dev, stream)
     if dev_status is None:
-        dev_status = torch.zeros(2, dtype=torch.int32, device=dev)
+        dev_status = _new((2,), torch.int32, dev, stream, torch.zeros)
     st = lib.moe_gemm_gateup_silu(_p(_u8(xq)), _p(xs), _p(counts), E, R, H, I, _p(w13),
                                   _p(w13_scale), _p(zq), _p(zs), _p(dev_status), _s(stream))
     _lib.check("moe_gemm_gateup_silu", st)
@@ -664,9 +686,9 @@ def moe_gemm_down(zq, zs, counts, w2, w2_scale, *, out=None, dev_status=None, st
     H = w2.shape[1]
     dev = zq.device
     if out is None:
-        out = torch.empty(E, R, H, dtype=torch.bfloat16, device=dev)
+        out = _new((E, R, H), torch.bfloat16, dev, stream)
     if dev_status is None:
-        dev_status = torch.zeros(2, dtype=torch.int32, device=dev)
+        dev_status = _new((2,), torch.int32, dev, stream, torch.zeros)
     st = lib.moe_gemm_down(_p(_u8(zq)), _p(zs), _p(counts), E, R, H, I, _p(w2), _p(w2_scale),
                            _p(out), _p(dev_status), _s(stream))
     _lib.check("moe_gemm_down", st)
@@ -694,15 +716,15 @@ def moe_gemm_gateup_down(xq, xs, counts, w13, w13_scale, w2, w2_scale, *, R=None
         rows, H = xq.shape
         lead = (rows,)
     if zq is None:
-        zq = torch.empty(*lead, I, dtype=torch.uint8, device=dev)
+        zq = _new((*lead, I), torch.uint8, dev, stream)
     if zs is None:
-        zs = torch.empty(*lead, I // 128, dtype=torch.float32, device=dev)
+        zs = _new((*lead, I // 128), torch.float32, dev, stream)
     if out is None:
-        out = torch.empty(*lead, H, dtype=torch.bfloat16, device=dev)
+        out = _new((*lead, H), torch.bfloat16, dev, stream)
     if dev_status is None:
-        dev_status = torch.zeros(2, dtype=torch.int32, device=dev)
+        dev_status = _new((2,), torch.int32, dev, stream, torch.zeros)
     if sync is None:
-        sync = _workspace(lib.moe_gemm_gateup_down_sync_size(E, R, rows), dev)
+        sync = _workspace(lib.moe_gemm_gateup_down_sync_size(E, R, rows), dev, stream)
     st = lib.moe_gemm_gateup_down(_p(_u8(xq)), _p(xs), _p(counts), E, R, rows, H, I, _p(w13),
                                   _p(w13_scale), _p(w2), _p(w2_scale), _p(zq), _p(zs), _p(out),
                                   _p(dev_status), _p(sync), sync.numel() * sync.element_size(),
