@@ -18,8 +18,8 @@
 // 4-step shuffle.
 //
 // Bound by HBM with many rows: 16384 rows of 7168 with a BF16 residual and both
-// outputs, 1.06 GB, take 175 us, 6.05 TB/s.  With few rows by latency: 2 to 4 us
-// (one row of 7168: 2.8).
+// outputs, 1.06 GB, take 176 us, 6.0 TB/s.  With few rows by latency: 2 to 4 us
+// (one row of 7168: 2.6).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -119,16 +119,36 @@ __global__ void norm_kernel(const NormArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = fmaf(f[i][j], f[i][j], ss);
   }
+  auto sum_row = [&](float v) {   // over the row, the same in every thread
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if constexpr (!kWarp) {
-    if (lane == 0) s_part[warp] = ss;
-    __syncthreads();
-    ss = lane < (nthr >> 5) ? s_part[lane] : 0.f;
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if constexpr (!kWarp) {
+      if (lane == 0) s_part[warp] = v;
+      __syncthreads();
+      v = lane < (nthr >> 5) ? s_part[lane] : 0.f;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    }
+    return v;
+  };
+  ss = sum_row(ss);
+  float mean = ss / static_cast<float>(a.H);
+  if (ss == INFINITY) {
+    // The sum of up to 2^14 squares leaves the range before their mean does: once
+    // more with every element times 2^-7.
+    constexpr float kDown = 0x1p-7f;
+    ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (i * nthr + tid >= nvec) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(f[i][j] * kDown, f[i][j] * kDown, ss);
+    }
+    if constexpr (!kWarp) __syncthreads();   // s_part has been read
+    ss = sum_row(ss);
+    mean = ss / static_cast<float>(a.H) * (1.f / (kDown * kDown));
   }
-  const float rstd = rsqrtf(ss / static_cast<float>(a.H) + a.eps);
+  const float rstd = rsqrtf(mean + a.eps);
 
 #pragma unroll
   for (int i = 0; i < V; ++i) {
