@@ -232,6 +232,7 @@ __global__ void router_topk_kernel(const TopkArgs a, const bool vec, const bool 
       if (g < a.groups)
         for (int i = lane & (lanes - 1); i < size; i += lanes)
           best.add(values[word_of<V>(g * size + i)]);
+      __syncwarp();   // the keys take the values' place
       best = best_of(best, lanes);
       best.a = __shfl_sync(kFull, best.a, lane << log_lanes);   // lane g's own
       best.b = __shfl_sync(kFull, best.b, lane << log_lanes);
