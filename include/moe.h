@@ -517,10 +517,13 @@ moe_status moe_dispatch_fp8(const uint8_t* tq, const float* ts, const void* topk
  * moe_experts_w4 -- the routed branch for a few tokens with 4-bit weights:
  * dispatch, gated-SiLU expert ("SGLang Expert Compute Backend", §1.1) and
  * weighted combine ("SGLang、NCCL 与 MoE EP", §1.1) of T <= MOE_W4_MAX_TOKENS
- * tokens as matrix-vector products; every active expert's weights are read
- * once.  x enters exactly (down to 2^-27 of the largest of its 128), SiLU(g) * u
- * with eleven significant bits (down to 2^-24 of the largest of its 128);
- * products and sums are fp32.  A token with a NaN or an infinity gets NaN.
+ * tokens as matrix-vector products; an active expert's weights are read once
+ * for every eight of its tokens.  x enters exactly (down to 2^-27 of the largest
+ * of its 128), SiLU(g) * u with eleven significant bits (down to 2^-24 of the
+ * largest of its 128); products and sums are fp32.  A 128's sum of code * x and
+ * eight times its sum of x are subtracted, so the error goes by the sum of
+ * (code + 8) * |x|, also where code - 8 is small; sums are held times 2^-24, so
+ * below 2^-102 they lose bits.  A token with a NaN or an infinity gets NaN.
  *   weight = (code - 8) * scale, 4-bit codes along the contraction, two a byte
  *   (the even element in the low four bits), one BF16 scale per output row and
  *   128 elements of the contraction.
@@ -538,7 +541,8 @@ moe_status moe_dispatch_fp8(const uint8_t* tq, const float* ts, const void* topk
  *              nothing is dropped)
  *   workspace  device, moe_experts_w4_workspace_size(T, K, H, I) bytes, 256-byte
  *              aligned: scratch, not shared with another call in flight
- * More tokens: MOE_ERR_INVALID_ARG (the FP8 layer is the faster form there).
+ * More tokens: MOE_ERR_INVALID_ARG (the FP8 layer takes any number; its weights
+ * are e4m3).
  * ------------------------------------------------------------------------- */
 #define MOE_W4_MAX_TOKENS 64
 size_t moe_experts_w4_workspace_size(int T, int K, int H, int I);

@@ -477,7 +477,8 @@ def moe_add_rms_norm(x, weight, eps: float = 1e-6, *, residual=None, residual_ou
 
 def moe_router_logits(x, w, *, logits=None, dev_status=None, stream=None):
     """The router's projection (moe_router_logits): ``x [T, H]`` and ``w [E,
-    H]`` bf16 to fp32 ``logits [T, E]``, fp32 products and sums."""
+    H]`` bf16 to fp32 ``logits [T, E]``, fp32 products and sums.  A timeout is
+    ORed into ``dev_status`` where one is given (the logits are NaN then)."""
     T, H = x.shape
     E = w.shape[0]
     dev = x.get_device()
@@ -563,7 +564,9 @@ def moe_experts_w4(x, topk_idx, topk_w, w13, w13_scale, w2, w2_scale, *, y=None,
     """The routed branch for up to ``W4_MAX_TOKENS`` tokens with 4-bit weights
     (moe_experts_w4): ``w13 [E, 2I, H/2]`` and ``w2 [E, H, I/2]`` uint8, two
     codes a byte, with bf16 scales ``[E, 2I, H/128]`` and ``[E, H, I/128]``; a
-    weight is (code - 8) * scale.  Returns ``y [T, H]`` bf16."""
+    weight is (code - 8) * scale.  Returns ``y [T, H]`` bf16; bad ids and
+    timeouts are reported in ``dev_status`` and are seen only by a caller who
+    passes one."""
     lib = _lib.load()
     T, H = x.shape
     K = topk_idx.shape[1]

@@ -493,10 +493,10 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
 // blocks run, so both are read after the wait, from L2, and neither is a const
 // __restrict__ pointer: that would let them be read through the read-only path,
 // which is for data that nobody writes in a kernel's lifetime.
-// Measured: 4096 tokens of 4096 to 8 of 128 skewed experts (127 MB) take 29 us with
-// the counting launches, 4.4 TB/s (33 from call to call; 41 with the loads after
+// Measured: 4096 tokens of 4096 to 8 of 128 skewed experts (127 MB) take 30 us with
+// the counting launches, 4.2 TB/s (34 from call to call; 41 with the loads after
 // the slots and the launches one after the other).  256 tokens to 64 experts, one
-// launch, take 6.6 us (9.2).  Bound by latency: the counts, the slots, the stores.
+// launch, take 6.8 us (9.2).  Bound by latency: the counts, the slots, the stores.
 template <typename IdT, bool kSingle>
 __global__ void __launch_bounds__(kDispatchWarps * 32)
     route_scatter_codes_kernel(const uint4* __restrict__ tq, const float* __restrict__ ts,

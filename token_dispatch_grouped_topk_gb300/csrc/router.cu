@@ -27,9 +27,11 @@
 // expert, was a twelfth of the time.
 //
 // Measured: 16384 tokens x 256 experts (sigmoid, bias, the best 4 of 8 groups by
-// sums of two, K = 8; 18 MB) take 17.5 us, 1 TB/s, at 3 instructions a clock; 256
-// tokens x 64 experts 3.3 us, launch latency.  The lane with the maximum walking
-// its own registers instead of shared memory: 23.5 us.
+// sums of two, K = 8; 18 MB) take 17.3 us, 1 TB/s, at 3 instructions a clock: 990
+// warp instructions a token, 264 of them the scores and the bias, 191 the groups,
+// 35 each of the eight rounds, the rest loads, keys and outputs.  256 tokens x 64
+// experts take 3.1 us, launch latency.  The lane with the maximum walking its own
+// registers instead of shared memory: 23.5 us.
 #include "common.cuh"
 #include "kernels.h"
 
