@@ -553,6 +553,80 @@ moe_status moe_experts_w4(const void* x, const void* topk_idx, int idx_bits, con
                           moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Microscaled 4-bit floating point -- the routed branch with weights and
+ * activations in 4 bits, for any number of tokens: the expert of "SGLang Expert
+ * Compute Backend", §1.1, in its own calls, with the block scales applied by the
+ * tensor cores.
+ *
+ * A value is an e2m1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6, the sign in bit 3) times
+ * its block's scale; two codes a byte along the row, the even element in the low
+ * four bits; scales row-major beside them, one byte a block.
+ *   MOE_FP4_NVFP4  blocks of 16, scales in e4m3, and an fp32 scale g over the
+ *                  tensor (over an expert, for weights); a NULL g is 1.
+ *                  s = e4m3(amax / (6 g)), code = e2m1(x * (1 / (s g)))
+ *   MOE_FP4_MXFP4  blocks of 32, scales in e8m0 (2^(byte - 127)), no g (NULL).
+ *                  s = 2^(floor(log2 amax) - 2), code = e2m1(x / s)
+ * in fp32, each step rounded to nearest; codes to nearest, ties to the even
+ * code, beyond 6 to 6; an e4m3 scale beyond 448 to 448.  A block whose scale
+ * rounds to zero has zero codes.  A block with a NaN or an infinity gets the
+ * scale NaN, and so NaN in every product with it.  g is positive and finite,
+ * with amax / g and s g inside fp32's normal range.
+ *
+ * moe_quantize_fp4      x device BF16 (x_bits = 16) or fp32 (32) [rows, H] to xq
+ *   device [rows, H/2] and xs device [rows, H/16] (NVFP4) or [rows, H/32].
+ *   gscale device fp32: one for every rows_per_gscale rows (>= 1; the last may
+ *   cover fewer), or NULL.  x 16-byte, xq 8-byte, xs 4-byte aligned.  Weights
+ *   [E, N, K] are E * N rows, N of them a gscale.
+ * moe_dequantize_fp4    code * s * g, rounded to out's type: out device BF16
+ *   (out_bits = 16) or fp32 (32) [rows, H].  The same alignments.
+ *
+ * moe_dispatch_quant_fp4  moe_dispatch_quant_ex in 4 bits: each token row is
+ *   quantised once and its codes and scales are written to every kept row of xq
+ *   [E, R, H/2] / xs [E, R, H/16 or H/32] (rows = 0) or [rows, ...] (packed).
+ *   x_gscale device fp32 [1] or NULL.  xq 8-byte, xs 4-byte aligned (16-byte for
+ *   the products below).  All else as there.
+ *
+ * moe_grouped_gemm_fp4  out[r] = bf16(ga * gw[e] * sum_k a[r, k] w[e, n, k]) for
+ *   the rows r < counts[e] of each expert e, sums in fp32; other rows untouched.
+ *   a device [E, R, K/2] and a_scale [E, R, K/16 or K/32] (rows = 0: padded) or
+ *   [rows, ...] (packed); w device [E, N, K/2], w_scale [E, N, K/16 or K/32];
+ *   a_gscale [1], w_gscale [E] fp32 or NULL; out device BF16 [E, R, N] or
+ *   [rows, N].  K and N multiples of 128 up to 16384.
+ * moe_gemm_gateup_fp4   the gate/up product, SiLU(gate) * up in fp32 and its
+ *   quantisation with z_gscale [1] or NULL: xq, xs, x_gscale, w13 [E, 2I, H/2]
+ *   (gate rows, then up rows), w13_scale, w13_gscale [E] as above; zq device
+ *   [E, R, I/2] (or [rows, I/2]) and zs [.., I/16 or I/32] out.  Then
+ *   moe_grouped_gemm_fp4 with w2 [E, H, I/2] and a_gscale = z_gscale is the down
+ *   product.
+ *   Codes, scales and out of both products 16-byte aligned.  dev_status device
+ *   int32 [2]: MOE_DEV_TIMEOUT may be ORed in.  flags: 0 or MOE_GEMM_MAX_CTAS(n).
+ * ------------------------------------------------------------------------- */
+#define MOE_FP4_NVFP4 0
+#define MOE_FP4_MXFP4 1
+moe_status moe_quantize_fp4(const void* x, int x_bits, const float* gscale,
+                            int64_t rows_per_gscale, int64_t rows, int H, int format, uint8_t* xq,
+                            uint8_t* xs, moe_stream_t stream);
+moe_status moe_dequantize_fp4(const uint8_t* xq, const uint8_t* xs, const float* gscale,
+                              int64_t rows_per_gscale, int64_t rows, int H, int format, void* out,
+                              int out_bits, moe_stream_t stream);
+moe_status moe_dispatch_quant_fp4(const void* x, const void* topk_idx, int idx_bits, int T, int H,
+                                  int K, int E, int R, int64_t rows, int format,
+                                  const float* x_gscale, uint8_t* xq, uint8_t* xs, int32_t* counts,
+                                  int32_t* src_map, int32_t* dev_status, void* workspace,
+                                  size_t workspace_bytes, moe_stream_t stream);
+moe_status moe_gemm_gateup_fp4(const uint8_t* xq, const uint8_t* xs, const float* x_gscale,
+                               const int32_t* counts, int E, int R, int64_t rows, int H, int I,
+                               const uint8_t* w13, const uint8_t* w13_scale,
+                               const float* w13_gscale, const float* z_gscale, int format,
+                               uint8_t* zq, uint8_t* zs, int32_t* dev_status, int flags,
+                               moe_stream_t stream);
+moe_status moe_grouped_gemm_fp4(const uint8_t* a, const uint8_t* a_scale, const float* a_gscale,
+                                const int32_t* counts, int E, int R, int64_t rows, int K, int N,
+                                const uint8_t* w, const uint8_t* w_scale, const float* w_gscale,
+                                int format, void* out, int32_t* dev_status, int flags,
+                                moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * moe_layer_stats -- the counts the pages account a layer by, for one routing:
  * "SGLang、NCCL 与 MoE EP", §5.3 (each token sends one payload per distinct
  * destination rank, D_t of them, §2.3.2; routes to an expert on another logical

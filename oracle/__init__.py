@@ -17,4 +17,5 @@ Sources (page title, then the section on that page):
 * "DeepEP 架构与实现笔记" -- §11 (the per-token FP8 cast rule) and §9.6 (combine
   applies the router weights in a weighted reduce).
 """
+from .fp4 import *  # noqa: F401,F403
 from .moe_oracle import *  # noqa: F401,F403

@@ -26,6 +26,8 @@ __all__ = [
     "moe_dispatch_quant_source_slots", "moe_gemm_source_slots",
     "moe_add_rms_norm", "moe_router_logits", "moe_router_topk", "moe_dispatch_fp8",
     "moe_experts_w4", "experts_w4_workspace_size", "W4_MAX_TOKENS",
+    "moe_quantize_fp4", "moe_dequantize_fp4", "moe_dispatch_quant_fp4", "moe_gemm_gateup_fp4",
+    "moe_grouped_gemm_fp4", "FP4_BLOCK",
     "moe_layer_stats", "layer_stats_dict", "LAYER_STATS",
     "packed_rows", "MoeLayerBuffers", "HostPipeline", "TwoBatchOverlap", "DEV_BAD_EXPERT_ID",
     "DEV_CAPACITY_DROPPED", "DEV_TIMEOUT",
@@ -36,6 +38,7 @@ DEV_BAD_EXPERT_ID = _lib.DEV_BAD_EXPERT_ID
 DEV_CAPACITY_DROPPED = _lib.DEV_CAPACITY_DROPPED
 DEV_TIMEOUT = _lib.DEV_TIMEOUT
 W4_MAX_TOKENS = _lib.W4_MAX_TOKENS
+FP4_BLOCK = _lib.FP4_BLOCK
 
 
 def _p(t):
@@ -592,6 +595,194 @@ def moe_experts_w4(x, topk_idx, topk_w, w13, w13_scale, w2, w2_scale, *, y=None,
     return y
 
 
+def _fp4(format):
+    """(the library's number of a 4-bit format, its block)."""
+    if format not in _lib.FP4_FORMATS:
+        raise ValueError(f"format: 'nvfp4' or 'mxfp4', not {format!r}")
+    return _lib.FP4_FORMATS[format], _lib.FP4_BLOCK[format]
+
+
+# block scales: a byte each, e4m3 (nvfp4) or e8m0 (mxfp4)
+_FP4_SCALES = {"nvfp4": (torch.uint8, torch.float8_e4m3fn),
+               "mxfp4": (torch.uint8, torch.float8_e8m0fnu)}
+
+
+def _gscale(g, n, dev, name):
+    """Address of the fp32 scales over a tensor (None: 1)."""
+    return None if g is None else _check(g, _F32, (n,), dev, name)
+
+
+def _gscale_rows(gscale, lead):
+    """(scales over the tensor, rows of each) of rows [*lead]: one over all of
+    them, or one per leading index of three-dimensional ones."""
+    rows = 1
+    for n in lead:
+        rows *= n
+    if gscale is None or gscale.numel() == 1 or len(lead) < 2:
+        return 1, max(rows, 1), rows
+    return lead[0], max(rows // max(lead[0], 1), 1), rows
+
+
+def moe_quantize_fp4(x, *, format: str = "nvfp4", gscale=None, xq=None, xs=None, stream=None):
+    """Rows ``x [..., H]`` bf16 or fp32 to microscaled 4 bits (moe_quantize_fp4):
+    ``"nvfp4"`` (blocks of 16, e4m3 scales, ``gscale`` fp32 over the tensor:
+    ``[1]``, or ``[E]`` for ``x [E, N, H]``; None is 1) or ``"mxfp4"`` (blocks of
+    32, power-of-two scales, no ``gscale``).  Returns ``(xq [..., H/2], xs [...,
+    H/16 or H/32])`` uint8."""
+    fmt, block = _fp4(format)
+    *lead, H = x.shape
+    dev = x.get_device()
+    n_g, per, rows = _gscale_rows(gscale, lead)
+    if xq is None:
+        xq = _new((*lead, H // 2), torch.uint8, x.device, stream)
+    if xs is None:
+        xs = _new((*lead, H // block), torch.uint8, x.device, stream)
+    st = _lib.load().moe_quantize_fp4(
+        _check(x, _HALF_OR_F32, x.shape, dev, "x"), _bits(x), _gscale(gscale, n_g, dev, "gscale"),
+        per, rows, H, fmt, _check(xq, _U8, (*lead, H // 2), dev, "xq"),
+        _check(xs, _FP4_SCALES[format], (*lead, H // block), dev, "xs"), _stream_on(stream, dev))
+    _lib.check("moe_quantize_fp4", st)
+    return xq, xs
+
+
+def moe_dequantize_fp4(xq, xs, *, format: str = "nvfp4", gscale=None, dtype=torch.bfloat16,
+                       out=None, stream=None):
+    """The values of ``moe_quantize_fp4``'s codes and scales (moe_dequantize_fp4):
+    ``out [..., H]`` in ``dtype``, bf16 or fp32."""
+    fmt, block = _fp4(format)
+    *lead, half = xq.shape
+    H = 2 * half
+    dev = xq.get_device()
+    n_g, per, rows = _gscale_rows(gscale, lead)
+    if out is None:
+        out = _new((*lead, H), dtype, xq.device, stream)
+    st = _lib.load().moe_dequantize_fp4(
+        _check(xq, _U8, xq.shape, dev, "xq"),
+        _check(xs, _FP4_SCALES[format], (*lead, H // block), dev, "xs"),
+        _gscale(gscale, n_g, dev, "gscale"), per, rows, H, fmt,
+        _check(out, _HALF_OR_F32, (*lead, H), dev, "out"), _bits(out), _stream_on(stream, dev))
+    _lib.check("moe_dequantize_fp4", st)
+    return out
+
+
+def moe_dispatch_quant_fp4(x, topk_idx, E: int, R: int, *, format: str = "nvfp4", x_gscale=None,
+                           xq=None, xs=None, counts=None, src_map=None, dev_status=None,
+                           workspace=None, stream=None, rows=0):
+    """``moe_dispatch_quant`` in microscaled 4 bits (moe_dispatch_quant_fp4):
+    each token row is quantised once, and its codes and scales go to every kept
+    row of ``xq [E, R, H/2]`` and ``xs [E, R, H/16 or H/32]`` (``rows = 0``) or
+    ``[rows, ...]`` (packed).  Returns ``(xq, xs, counts, src_map,
+    dev_status)``."""
+    lib = _lib.load()
+    fmt, block = _fp4(format)
+    T, H = x.shape
+    K = topk_idx.shape[1]
+    dev = x.get_device()
+    lead = (rows,) if rows else (E, R)
+    if xq is None:
+        xq = _new((*lead, H // 2), torch.uint8, x.device, stream)
+    if xs is None:
+        xs = _new((*lead, H // block), torch.uint8, x.device, stream)
+    if counts is None:
+        counts = _new((E,), torch.int32, x.device, stream)
+    if src_map is None:
+        src_map = _new((T, K), torch.int32, x.device, stream)
+    if dev_status is None:
+        dev_status = _new((2,), torch.int32, x.device, stream)
+    if workspace is None:
+        workspace = _workspace(lib.moe_dispatch_workspace_size(T, K, E), x.device, stream)
+    st = lib.moe_dispatch_quant_fp4(
+        _check(x, _BF16, (T, H), dev, "x"), _check(topk_idx, _IDS, (T, K), dev, "topk_idx"),
+        _bits(topk_idx), T, H, K, E, R, rows, fmt, _gscale(x_gscale, 1, dev, "x_gscale"),
+        _check(xq, _U8, (*lead, H // 2), dev, "xq"),
+        _check(xs, _FP4_SCALES[format], (*lead, H // block), dev, "xs"),
+        _check(counts, _I32, (E,), dev, "counts"), _check(src_map, _I32, (T, K), dev, "src_map"),
+        _check(dev_status, _I32, (2,), dev, "dev_status"), *_check_ws(workspace, dev),
+        _stream_on(stream, dev))
+    _lib.check("moe_dispatch_quant_fp4", st)
+    return xq, xs, counts, src_map, dev_status
+
+
+def _fp4_rows(a, R):
+    """(leading shape, R, packed rows) of a padded [E, R, ...] or packed [rows,
+    ...] operand."""
+    if a.dim() == 3:
+        return tuple(a.shape[:2]), a.shape[1], 0
+    if R is None:
+        raise ValueError("the packed layout needs R")
+    return (a.shape[0],), R, a.shape[0]
+
+
+def _cta_flags(max_ctas):
+    return _gemm_flags(False, None, max_ctas)
+
+
+def moe_gemm_gateup_fp4(xq, xs, counts, w13, w13_scale, *, format: str = "nvfp4", x_gscale=None,
+                        w13_gscale=None, z_gscale=None, R=None, zq=None, zs=None, dev_status=None,
+                        stream=None, max_ctas=0):
+    """The gate/up product in 4 bits, SiLU(gate) * up and its quantisation
+    (moe_gemm_gateup_fp4): ``xq [E, R, H/2]`` (or ``[rows, H/2]`` with ``R``
+    given: packed), ``w13 [E, 2I, H/2]`` uint8 with their block scales; scales
+    over the tensors ``x_gscale [1]``, ``w13_gscale [E]``, ``z_gscale [1]``
+    fp32.  Returns ``(zq [..., I/2], zs [..., I/16 or I/32])`` uint8, rows below
+    ``counts`` written."""
+    fmt, block = _fp4(format)
+    lead, R, rows = _fp4_rows(xq, R)
+    H = 2 * xq.shape[-1]
+    E, n13, _ = w13.shape
+    I = n13 // 2
+    dev = xq.get_device()
+    if zq is None:
+        zq = _new((*lead, I // 2), torch.uint8, xq.device, stream)
+    if zs is None:
+        zs = _new((*lead, I // block), torch.uint8, xq.device, stream)
+    if dev_status is None:
+        dev_status = _new((2,), torch.int32, xq.device, stream, torch.zeros)
+    sc = _FP4_SCALES[format]
+    st = _lib.load().moe_gemm_gateup_fp4(
+        _check(xq, _U8, (*((E, R) if not rows else lead), H // 2), dev, "xq"),
+        _check(xs, sc, (*lead, H // block), dev, "xs"), _gscale(x_gscale, 1, dev, "x_gscale"),
+        _check(counts, _I32, (E,), dev, "counts"), E, R, rows, H, I,
+        _check(w13, _U8, (E, 2 * I, H // 2), dev, "w13"),
+        _check(w13_scale, sc, (E, 2 * I, H // block), dev, "w13_scale"),
+        _gscale(w13_gscale, E, dev, "w13_gscale"), _gscale(z_gscale, 1, dev, "z_gscale"), fmt,
+        _check(zq, _U8, (*lead, I // 2), dev, "zq"), _check(zs, sc, (*lead, I // block), dev, "zs"),
+        _check(dev_status, _I32, (2,), dev, "dev_status"), _cta_flags(max_ctas),
+        _stream_on(stream, dev))
+    _lib.check("moe_gemm_gateup_fp4", st)
+    return zq, zs
+
+
+def moe_grouped_gemm_fp4(a, a_scale, counts, w, w_scale, *, format: str = "nvfp4", a_gscale=None,
+                         w_gscale=None, R=None, out=None, dev_status=None, stream=None, max_ctas=0):
+    """Each expert's valid rows times its weights, both in microscaled 4 bits
+    (moe_grouped_gemm_fp4): ``a [E, R, K/2]`` (or ``[rows, K/2]`` with ``R``
+    given: packed) and ``w [E, N, K/2]`` uint8 with their block scales; scales
+    over the tensors ``a_gscale [1]`` and ``w_gscale [E]`` fp32.  Returns ``out
+    [E, R, N]`` (``[rows, N]``) bf16, rows below ``counts`` written."""
+    fmt, block = _fp4(format)
+    lead, R, rows = _fp4_rows(a, R)
+    K = 2 * a.shape[-1]
+    E, N, _ = w.shape
+    dev = a.get_device()
+    if out is None:
+        out = _new((*lead, N), torch.bfloat16, a.device, stream)
+    if dev_status is None:
+        dev_status = _new((2,), torch.int32, a.device, stream, torch.zeros)
+    sc = _FP4_SCALES[format]
+    st = _lib.load().moe_grouped_gemm_fp4(
+        _check(a, _U8, (*((E, R) if not rows else lead), K // 2), dev, "a"),
+        _check(a_scale, sc, (*lead, K // block), dev, "a_scale"),
+        _gscale(a_gscale, 1, dev, "a_gscale"), _check(counts, _I32, (E,), dev, "counts"), E, R, rows,
+        K, N, _check(w, _U8, (E, N, K // 2), dev, "w"),
+        _check(w_scale, sc, (E, N, K // block), dev, "w_scale"), _gscale(w_gscale, E, dev, "w_gscale"),
+        fmt, _check(out, _BF16, (*lead, N), dev, "out"),
+        _check(dev_status, _I32, (2,), dev, "dev_status"), _cta_flags(max_ctas),
+        _stream_on(stream, dev))
+    _lib.check("moe_grouped_gemm_fp4", st)
+    return out
+
+
 LAYER_STATS = ("valid_routes", "kept_routes", "messages", "cross_rank_routes", "tile_blocks",
                "active_experts", "busiest_expert_rows")
 
@@ -759,9 +950,17 @@ class MoeLayerBuffers:
     source_slots: int = 0
     L: int = 1
     rank_offsets: torch.Tensor | None = None
+    # microscaled 4 bits ("nvfp4" or "mxfp4") instead of FP8: w13 [E, 2I, H/2] and w2
+    # [E, H, I/2] uint8 with block scales; fp4_gscales are the scales over x [1],
+    # w13 [E], Z [1] and w2 [E] (each fp32 or None)
+    fp4: str | None = None
+    fp4_gscales: tuple = (None, None, None, None)
 
     def __post_init__(self):
         d, E, R, H, I, T, K = self.device, self.E, self.R, self.H, self.I, self.T, self.K
+        if self.fp4:
+            self._post_init_fp4()
+            return
         if self.source_slots:
             if self.packed or E % self.L or R != (E // self.L) * self.source_slots:
                 raise ValueError("source slots: padded lane with R = (E / L) * max_tokens")
@@ -785,12 +984,37 @@ class MoeLayerBuffers:
         self.ws_dispatch = _workspace(dispatch_workspace_size(T, K, E), d)
         self.ws_compute = _workspace(ws, d)
 
+    def _post_init_fp4(self):
+        d, E, R, H, I, T, K = self.device, self.E, self.R, self.H, self.I, self.T, self.K
+        _, block = _fp4(self.fp4)
+        if self.source_slots or self.w13_interleaved or self.gemm_launch:
+            raise ValueError("a 4-bit lane is padded or packed, W13's gate rows before its up rows, "
+                             "its products two launches")
+        if len(self.fp4_gscales) != 4:
+            raise ValueError("fp4_gscales: the scales over x, w13, Z and w2 (None: 1)")
+        self.rows = packed_rows(T, K, E, R) if self.packed else E * R
+        lead = (self.rows,) if self.packed else (E, R)
+        new = lambda *shape: torch.empty(*lead, *shape, dtype=torch.uint8, device=d)
+        self.fp4_rows = (new(H // 2), new(H // block), new(I // 2), new(I // block))
+        self._recv_shape, self._recv, self._slots = (*lead, H), None, None
+        self.out = torch.empty(*lead, H, dtype=torch.bfloat16, device=d)
+        self.counts = torch.zeros(E, dtype=torch.int32, device=d)
+        self.src_map = torch.empty(T, K, dtype=torch.int32, device=d)
+        self.dev_status = torch.zeros(2, dtype=torch.int32, device=d)
+        self.y = torch.empty(T, H, dtype=torch.bfloat16, device=d)
+        self.ws_dispatch = _workspace(dispatch_workspace_size(T, K, E), d)
+
+    def _not_fp4(self, what):
+        if self.fp4:
+            raise ValueError(f"{what}: not on a 4-bit lane")
+
     @property
     def recv(self):
         """The BF16 receive buffer of the separate path, allocated on first
         use (the default fused path never forms it: 15 GB saved at the large
         padded layer).  Touch it before capturing a separate-path forward into
         a CUDA graph."""
+        self._not_fp4("recv")
         if self._recv is None:
             self._recv = torch.empty(*self._recv_shape, dtype=torch.bfloat16, device=self.device)
         return self._recv
@@ -802,6 +1026,7 @@ class MoeLayerBuffers:
         their valid rows into its workspace), allocated on first use.  Touch it
         before capturing a fused forward of a per-source lane into a CUDA
         graph."""
+        self._not_fp4("slots_fp8")
         if self._slots is None:
             E, R, H = self.E, self.R, self.H
             self._slots = (torch.empty(E, R, H, dtype=torch.uint8, device=self.device),
@@ -812,6 +1037,7 @@ class MoeLayerBuffers:
         """Byte offsets of the expert compute workspace's parts, from the
         library (moe_expert_compute_workspace_layout): xq, xs, zq, zs, sync,
         sync bytes, total."""
+        self._not_fp4("workspace_layout")
         return expert_compute_workspace_layout(self.E, self.R, self.rows if self.packed else 0,
                                                self.H, self.I)
 
@@ -840,7 +1066,15 @@ class MoeLayerBuffers:
         """The layer's first stage on the fused path: moe_dispatch_quant_ex
         into the workspace's FP8 activations (the BF16 receive buffer is not
         used); on the per-source layout moe_dispatch_quant_source_slots into
-        ``slots_fp8``."""
+        ``slots_fp8``; on a 4-bit lane moe_dispatch_quant_fp4 into ``fp4_rows``
+        (codes and scales of x, then of Z)."""
+        if self.fp4:
+            moe_dispatch_quant_fp4(x, topk_idx, self.E, self.R, format=self.fp4,
+                                   x_gscale=self.fp4_gscales[0], xq=self.fp4_rows[0],
+                                   xs=self.fp4_rows[1], counts=self.counts, src_map=self.src_map,
+                                   dev_status=self.dev_status, workspace=self.ws_dispatch,
+                                   stream=stream, rows=self.rows if self.packed else 0)
+            return
         if self.source_slots:
             sq, ss = self.slots_fp8
             moe_dispatch_quant_source_slots(x, topk_idx, topk_w, self.E, self.L,
@@ -860,6 +1094,7 @@ class MoeLayerBuffers:
         codes ``xq [T, H]`` and scales ``xs [T, H/128]``, as moe_add_rms_norm
         gives them; ``gemms`` and ``combine`` follow.  Padded and packed
         layouts."""
+        self._not_fp4("dispatch_fp8")
         if self.source_slots:
             raise ValueError("dispatch_fp8: the padded or packed layout, not per-source slots")
         oq, os_, _, _ = self.workspace_views()
@@ -869,8 +1104,18 @@ class MoeLayerBuffers:
                          rows=self.rows if self.packed else 0)
 
     def gemms(self, w13, w13_scale, w2, w2_scale, stream=None, max_ctas=0):
-        """Both GEMMs on the FP8 activations dispatch_quant wrote, in the
+        """Both GEMMs on the FP8 (4-bit) activations dispatch_quant wrote, in the
         library's launch form for the layer (or ``gemm_launch``)."""
+        if self.fp4:
+            xq, xs, zq, zs = self.fp4_rows
+            gx, g13, gz, g2 = self.fp4_gscales
+            kw = dict(format=self.fp4, R=self.R, dev_status=self.dev_status, stream=stream,
+                      max_ctas=max_ctas)
+            moe_gemm_gateup_fp4(xq, xs, self.counts, w13, w13_scale, x_gscale=gx, w13_gscale=g13,
+                                z_gscale=gz, zq=zq, zs=zs, **kw)
+            moe_grouped_gemm_fp4(zq, zs, self.counts, w2, w2_scale, a_gscale=gz, w_gscale=g2,
+                                 out=self.out, **kw)
+            return
         if self.source_slots:
             sq, ss = self.slots_fp8
             moe_gemm_source_slots(sq, ss, self.seg_counts, self.L, self.source_slots, w13,
@@ -915,6 +1160,7 @@ class MoeLayerBuffers:
             self.gemms(w13, w13_scale, w2, w2_scale, stream=stream)
             self.combine(topk_w, y, stream=stream)
             return y
+        self._not_fp4("forward(fused=False)")
         if self.source_slots:
             moe_dispatch_source_slots(x, topk_idx, topk_w, self.E, self.L, self.source_slots,
                                       rank_offsets=self.rank_offsets, recv=self.recv,
@@ -1051,15 +1297,19 @@ class TwoBatchOverlap:
     Both produce the same bytes.  The stages are those of
     ``MoeLayerBuffers.forward``: with ``fused`` (default) dispatch+quantisation,
     GEMMs, combine; without, dispatch, expert compute (quantisation and GEMMs),
-    combine."""
+    combine.  ``fp4`` and ``fp4_gscales`` make both lanes 4-bit ones."""
 
     def __init__(self, T: int, E: int, K: int, H: int, I: int, R: int, device, gemm_ctas: int = 0,
-                 fused: bool = True):
+                 fused: bool = True, fp4: str | None = None,
+                 fp4_gscales: tuple = (None, None, None, None)):
+        if fp4 and not fused:
+            raise ValueError("4-bit lanes have the fused path only")
         self.gemm_ctas = gemm_ctas   # > 0: the expert compute's GEMMs take at most this many SMs
         self.fused = fused
         self.half = T // 2
         self.sizes = (self.half, T - self.half)
-        self.lanes = [MoeLayerBuffers(n, E, K, H, I, R, device) for n in self.sizes]
+        self.lanes = [MoeLayerBuffers(n, E, K, H, I, R, device, fp4=fp4, fp4_gscales=fp4_gscales)
+                      for n in self.sizes]
         self.streams = [torch.cuda.Stream(device=device), torch.cuda.Stream(device=device)]
         self.y = torch.empty(T, H, dtype=torch.bfloat16, device=device)
         # each lane's combine writes straight into its half of y

@@ -20,7 +20,7 @@ LIB_NAME = "libmoe_gb300.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 SOURCES = ["moe_api.cu", "dispatch.cu", "quant.cu", "gemm.cu", "combine.cu", "dispatch_noalloc.cu",
            "selftest.cu", "stats.cu", "ep.cu", "norm.cu", "router.cu", "router_logits.cu",
-           "experts_w4.cu"]
+           "experts_w4.cu", "quant_fp4.cu", "gemm_fp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include")]

@@ -18,6 +18,7 @@
 // base_e the prefix of the clamped counts (packed layout, §2.6 of "SGLang
 // Expert Compute Backend": the valid rows of all experts back to back).
 #include "common.cuh"
+#include "fp4.cuh"
 #include "kernels.h"
 
 namespace moe {
@@ -591,6 +592,121 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
   }
 }
 
+// Dispatch fused with the quantisation to microscaled 4 bits (fp4.cuh): each
+// token row is read and quantised once and its codes and scales are written to
+// every kept row.  The block's work is route_scatter_codes_kernel's: whole
+// 128-groups of its tokens' rows, shared evenly among its warps, the first
+// loads (and here the quantisation, which does not depend on where a row goes)
+// before the block finds its routes' slots.  A lane takes 16 values (two
+// 16-byte loads, 8 bytes of codes), a warp 512 at a time, 1, 2 or 4 times a token.
+template <typename IdT, int kFmt, bool kSingle>
+__global__ void __launch_bounds__(kDispatchWarps * 32)
+    route_scatter_fp4_kernel(const uint4* __restrict__ x, const float* xg,
+                             const IdT* __restrict__ topk_idx, int T, int H, int K, int E,
+                             RowLayout rl, int nblocks, const int32_t* base, int32_t* counts,
+                             uint2* __restrict__ xq, uint32_t* __restrict__ xs,
+                             int32_t* __restrict__ src_map, int32_t* dev_status,
+                             int groups_per_slice, int log_u) {
+  extern __shared__ int smem[];
+  int* s_cnt = smem;                           // [kDispatchWarps][E]
+  int* s_dest = smem + kDispatchWarps * E;     // [kDispatchWarps][32]
+  int* s_rows = s_dest + kDispatchWarps * 32;  // [E + 1] packed row bases
+  int* s_prev = s_rows + E + 1;                // single pass: [E]
+  int* s_tot = s_prev + E;                     //              [E]; packed: the kept counts
+  constexpr int kWordLanes = kFmt == kNvfp4 ? 4 : 8;   // lanes that share a word of scales
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gw = blockIdx.x * kDispatchWarps + warp;
+  const int tpw = 32 / K;
+  // the block's rows, this warp's share of them and its first
+  const int rows = min(kDispatchWarps * tpw, T - static_cast<int>(blockIdx.x) * kDispatchWarps * tpw);
+  const int share = (rows + kDispatchWarps - 1) / kDispatchWarps;
+  const int t0 = blockIdx.x * kDispatchWarps * tpw + warp * share;
+  const int nch = H / 16;                           // 16-value chunks of a row
+  const int g0 = blockIdx.y * groups_per_slice, ng = min(H / kGroup - g0, groups_per_slice);
+  const int c0 = g0 * 8, nc = ng * 8;
+  const int tokens = max(0, min(share, rows - warp * share));
+  const int batch = 4 >> log_u;                     // tokens of four chunks per lane
+  if (kSingle) chain_start();
+  const float g = xg ? __ldcg(xg) : 1.f;
+  const float six_g = __fmul_rn(6.f, g);
+  uint4 v[8];
+  uint2 codes[4];
+  uint32_t word[4];
+  auto load = [&](int tt0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tt = tt0 + (i >> log_u), c = lane + 32 * (i & ((1 << log_u) - 1));
+      const bool on = tt < tokens && c < nc;
+      const uint4* p = x + (static_cast<size_t>(t0 + tt) * nch + c0 + c) * 2;
+      v[2 * i] = on ? ld_stream(p) : make_uint4(0, 0, 0, 0);
+      v[2 * i + 1] = on ? ld_stream(p + 1) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto quantise = [&]() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float f[16];
+      bf16x8_to_f32(v[2 * i], f);
+      bf16x8_to_f32(v[2 * i + 1], f + 8);
+      codes[i] = fp4_quantize16<kFmt>(f, g, six_g, lane, &word[i]);
+    }
+  };
+  load(0);
+
+  for (int i = threadIdx.x; i < kDispatchWarps * E; i += blockDim.x) s_cnt[i] = 0;
+  if (kSingle) {
+    single_pass_bases(topk_idx, T, K, E, rl, s_prev, s_tot, s_rows, counts, dev_status);
+  } else {
+    chain_wait();
+    chain_start();
+    if (rl.packed) {
+      for (int e = threadIdx.x; e < E; e += blockDim.x) s_tot[e] = __ldcg(counts + e);
+      __syncthreads();
+      expert_prefix(s_tot, E, rl.R, 1, 1, s_rows, nullptr);
+    }
+  }
+  quantise();
+  __syncthreads();
+  const RouteLane r = load_route(topk_idx, T, K, E, gw, lane, nullptr);
+  const unsigned peers = __match_any_sync(0xffffffffu, r.e);
+  const int lane_rank = __popc(peers & ((1u << lane) - 1u));
+  if (r.e >= 0 && lane == __ffs(peers) - 1) s_cnt[warp * E + r.e] = __popc(peers);
+  __syncthreads();
+  int q = -1;
+  if (r.e >= 0) {
+    int sl = (kSingle ? s_prev[r.e]
+                      : __ldcg(base + static_cast<size_t>(r.e) * nblocks + blockIdx.x)) +
+             lane_rank;
+    for (int w = 0; w < warp; ++w) sl += s_cnt[w * E + r.e];
+    if (sl < rl.R) q = (rl.packed ? s_rows[r.e] : r.e * rl.R) + sl;
+  }
+  if (blockIdx.y == 0 && r.active) src_map[static_cast<int64_t>(r.t) * K + r.k] = q;
+  if (lane < tpw * K) s_dest[warp * tpw * K + lane] = q;   // the block's routes in order
+  if (share == tpw) __syncwarp();   // each warp's rows are the ones it found the slots of
+  else __syncthreads();
+
+  const int* wdest = s_dest + warp * share * K;
+  for (int tt0 = 0; tt0 < tokens; tt0 += batch) {
+    if (tt0 > 0) {
+      load(tt0);
+      quantise();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tt = tt0 + (i >> log_u), c = lane + 32 * (i & ((1 << log_u) - 1));
+      if (tt >= tokens || c >= nc) continue;
+      const int* dq = wdest + tt * K;
+      for (int k = 0; k < K; ++k) {
+        const int qq = dq[k];
+        if (qq < 0) continue;
+        const size_t at = static_cast<size_t>(qq) * nch + c0 + c;
+        xq[at] = codes[i];
+        if (lane % kWordLanes == 0) xs[at / kWordLanes] = word[i];
+      }
+    }
+  }
+}
+
 // Per-source fixed-slot dispatch ("DeepEP 架构与实现笔记", §9.5): expert e's
 // R = W * mt rows are W ranges of mt slots, one per source rank, and route
 // (t, k) of source rank r goes to slot r * mt + p, p its position among r's
@@ -1037,6 +1153,70 @@ cudaError_t launch_dispatch_fp8(const uint8_t* tq, const float* ts, const void* 
                              counts, src_map, dev_status, hist, sm_count, s);
   return dispatch_fp8_impl(tq, ts, static_cast<const int64_t*>(topk_idx), T, H, K, E, rl, xq, xs,
                            counts, src_map, dev_status, hist, sm_count, s);
+}
+
+namespace {
+template <typename IdT, int kFmt>
+cudaError_t dispatch_fp4_impl(const void* x, const IdT* topk_idx, int T, int H, int K, int E,
+                              RowLayout rl, const float* xg, uint8_t* xq, uint8_t* xs,
+                              int32_t* counts, int32_t* src_map, int32_t* dev_status,
+                              int32_t* hist, int sm_count, cudaStream_t s) {
+  const int nblocks = dispatch_blocks(T, K);
+  const bool one = single_pass(T, K);
+  cudaError_t err;
+  if (nblocks == 0) {   // no tokens: counts and status
+    if ((err = cudaMemsetAsync(dev_status, 0, 2 * sizeof(int32_t), s)) != cudaSuccess) return err;
+    return cudaMemsetAsync(counts, 0, E * sizeof(int32_t), s);
+  }
+  if (!one) {
+    route_hist_kernel<IdT, true><<<nblocks, kDispatchWarps * 32, E * sizeof(int), s>>>(
+        topk_idx, T, K, E, nblocks, hist, dev_status);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    err = launch_chained(route_scan_kernel<true>, dim3(E), kScanThreads, 0, s, hist, nblocks, rl.R,
+                         counts, dev_status);
+    if (err != cudaSuccess) return err;
+  }
+  // slices of four (512 values, one chunk per lane) to 16 whole 128-groups
+  const int G = H / kGroup;
+  int hsplit = max(row_slices(nblocks, G, 4, sm_count), (G + 15) / 16);
+  const int gps = (G + hsplit - 1) / hsplit;
+  hsplit = (G + gps - 1) / gps;
+  const int log_u = gps <= 4 ? 0 : gps <= 8 ? 1 : 2;
+  const size_t smem = (kDispatchWarps * E + kDispatchWarps * 32 + 3 * E + 1) * sizeof(int);
+  auto kernel = one ? route_scatter_fp4_kernel<IdT, kFmt, true> : route_scatter_fp4_kernel<IdT, kFmt, false>;
+  if ((err = allow_smem(kernel, smem)) != cudaSuccess) return err;
+  const dim3 grid(nblocks, hsplit);
+  const auto* x4 = static_cast<const uint4*>(x);
+  auto* q2 = reinterpret_cast<uint2*>(xq);
+  auto* s4 = reinterpret_cast<uint32_t*>(xs);
+  if (!one)
+    return launch_chained(kernel, grid, kDispatchWarps * 32, smem, s, x4, xg, topk_idx, T, H, K, E, rl,
+                          nblocks, hist, counts, q2, s4, src_map, dev_status, gps, log_u);
+  kernel<<<grid, kDispatchWarps * 32, smem, s>>>(x4, xg, topk_idx, T, H, K, E, rl, nblocks, hist, counts,
+                                                 q2, s4, src_map, dev_status, gps, log_u);
+  return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_dispatch_quant_fp4(const void* x, const void* topk_idx, int idx_bits, int T,
+                                      int H, int K, int E, RowLayout rl, int format,
+                                      const float* xg, uint8_t* xq, uint8_t* xs, int32_t* counts,
+                                      int32_t* src_map, int32_t* dev_status, int32_t* hist,
+                                      int sm_count, cudaStream_t s) {
+  if (idx_bits == 32) {
+    const auto* ids = static_cast<const int32_t*>(topk_idx);
+    return format == kNvfp4
+               ? dispatch_fp4_impl<int32_t, kNvfp4>(x, ids, T, H, K, E, rl, xg, xq, xs, counts, src_map,
+                                                    dev_status, hist, sm_count, s)
+               : dispatch_fp4_impl<int32_t, kMxfp4>(x, ids, T, H, K, E, rl, xg, xq, xs, counts, src_map,
+                                                    dev_status, hist, sm_count, s);
+  }
+  const auto* ids = static_cast<const int64_t*>(topk_idx);
+  return format == kNvfp4
+             ? dispatch_fp4_impl<int64_t, kNvfp4>(x, ids, T, H, K, E, rl, xg, xq, xs, counts, src_map,
+                                                  dev_status, hist, sm_count, s)
+             : dispatch_fp4_impl<int64_t, kMxfp4>(x, ids, T, H, K, E, rl, xg, xq, xs, counts, src_map,
+                                                  dev_status, hist, sm_count, s);
 }
 
 }  // namespace moe

@@ -181,6 +181,31 @@ cudaError_t launch_experts_w4(const void* x, const void* topk_idx, int idx_bits,
                               const void* w2_scale, void* workspace, void* y,
                               int32_t* dev_status, int sm_count, cudaStream_t s);
 
+// ----- microscaled 4-bit floating point (format: 0 NVFP4, 1 MXFP4)
+cudaError_t launch_quantize_fp4(const void* x, int x_bits, const float* gscale,
+                                int64_t rows_per_gscale, int64_t rows, int H, int format,
+                                uint8_t* xq, uint8_t* xs, int sm_count, cudaStream_t s);
+cudaError_t launch_dequantize_fp4(const uint8_t* xq, const uint8_t* xs, const float* gscale,
+                                  int64_t rows_per_gscale, int64_t rows, int H, int format,
+                                  void* out, int out_bits, int sm_count, cudaStream_t s);
+// dispatch fused with the quantisation: codes xq [rows, H / 2] and scales xs
+// [rows, H / 16 or H / 32]; xg [1] the scale over x, or null
+cudaError_t launch_dispatch_quant_fp4(const void* x, const void* topk_idx, int idx_bits, int T,
+                                      int H, int K, int E, RowLayout rl, int format,
+                                      const float* xg, uint8_t* xq, uint8_t* xs, int32_t* counts,
+                                      int32_t* src_map, int32_t* dev_status, int32_t* hist,
+                                      int sm_count, cudaStream_t s);
+// rows of ragged experts times their weights; null scales over a tensor: 1
+cudaError_t launch_gemm_gateup_fp4(const uint8_t* xq, const uint8_t* xs, const float* xg,
+                                   const int32_t* counts, int E, RowLayout rl, int H, int I,
+                                   const uint8_t* w13, const uint8_t* s13, const float* g13,
+                                   const float* zg, int format, uint8_t* zq, uint8_t* zs,
+                                   int32_t* dev_status, int sm_count, cudaStream_t s);
+cudaError_t launch_grouped_gemm_fp4(const uint8_t* aq, const uint8_t* as, const float* ag,
+                                    const int32_t* counts, int E, RowLayout rl, int K, int N,
+                                    const uint8_t* w, const uint8_t* ws, const float* wg, int format,
+                                    void* out, int32_t* dev_status, int sm_count, cudaStream_t s);
+
 // ----- layer statistics of one routing (kLayerStats 64-bit counters):
 // [0] valid routes, [1] kept routes, [2] messages (sum over tokens of the
 // distinct destination ranks), [3] cross-rank routes, [4] 128-row blocks of

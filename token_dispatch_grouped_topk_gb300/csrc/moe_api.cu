@@ -471,6 +471,130 @@ moe_status moe_router_topk(const void* logits, int logits_bits, const float* bia
                                       reinterpret_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+// A known format, and no scale over the tensor where it has none.
+bool valid_fp4(int format, const float* g0, const float* g1 = nullptr, const float* g2 = nullptr) {
+  if (format == MOE_FP4_NVFP4) return true;
+  return format == MOE_FP4_MXFP4 && g0 == nullptr && g1 == nullptr && g2 == nullptr;
+}
+bool valid_fp4_rows(int64_t rows, int64_t rows_per_gscale, int H) {
+  return rows >= 0 && rows <= (int64_t{1} << 30) && rows_per_gscale >= 1 &&
+         rows_per_gscale <= (int64_t{1} << 30) && valid_hidden(H);
+}
+bool valid_cta_flags(int flags) { return (flags & ~MOE_GEMM_MAX_CTAS(0x7FFF)) == 0; }
+int grid_limit(int flags, int sm_count) {
+  const int cap = (flags >> 16) & 0x7FFF;
+  return cap > 0 ? std::min(cap, sm_count) : sm_count;
+}
+}  // namespace
+
+moe_status moe_quantize_fp4(const void* x, int x_bits, const float* gscale,
+                            int64_t rows_per_gscale, int64_t rows, int H, int format, uint8_t* xq,
+                            uint8_t* xs, moe_stream_t stream) {
+  if (!valid_fp4_rows(rows, rows_per_gscale, H) || !valid_fp4(format, gscale)) return MOE_ERR_INVALID_ARG;
+  if (x_bits != 16 && x_bits != 32) return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && (x == nullptr || xq == nullptr || xs == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned8(xq) || !aligned4(xs) || !aligned4(gscale)) return MOE_ERR_INVALID_ARG;
+  const DeviceInfo* dev = nullptr;
+  if (moe_status st = check_device(&dev); st != MOE_OK) return st;
+  return from_cuda(launch_quantize_fp4(x, x_bits, gscale, rows_per_gscale, rows, H, format, xq, xs,
+                                       dev->sm_count, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_dequantize_fp4(const uint8_t* xq, const uint8_t* xs, const float* gscale,
+                              int64_t rows_per_gscale, int64_t rows, int H, int format, void* out,
+                              int out_bits, moe_stream_t stream) {
+  if (!valid_fp4_rows(rows, rows_per_gscale, H) || !valid_fp4(format, gscale)) return MOE_ERR_INVALID_ARG;
+  if (out_bits != 16 && out_bits != 32) return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && (out == nullptr || xq == nullptr || xs == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned8(xq) || !aligned4(xs) || !aligned4(gscale)) return MOE_ERR_INVALID_ARG;
+  const DeviceInfo* dev = nullptr;
+  if (moe_status st = check_device(&dev); st != MOE_OK) return st;
+  return from_cuda(launch_dequantize_fp4(xq, xs, gscale, rows_per_gscale, rows, H, format, out,
+                                         out_bits, dev->sm_count,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_dispatch_quant_fp4(const void* x, const void* topk_idx, int idx_bits, int T, int H,
+                                  int K, int E, int R, int64_t rows, int format,
+                                  const float* x_gscale, uint8_t* xq, uint8_t* xs, int32_t* counts,
+                                  int32_t* src_map, int32_t* dev_status, void* workspace,
+                                  size_t workspace_bytes, moe_stream_t stream) {
+  if (T < 0 || !valid_hidden(H) || !valid_experts(E, R) || K < 1 || K > 32 || K > E)
+    return MOE_ERR_INVALID_ARG;
+  if ((idx_bits != 32 && idx_bits != 64) || !valid_fp4(format, x_gscale)) return MOE_ERR_INVALID_ARG;
+  if (counts == nullptr || dev_status == nullptr) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (x == nullptr || topk_idx == nullptr || xq == nullptr || xs == nullptr ||
+                src_map == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!aligned16(x) || !aligned8(xq) || !aligned4(xs) || !aligned4(x_gscale)))
+    return MOE_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(T) * K > (int64_t{1} << 31) - 1) return MOE_ERR_INVALID_ARG;
+  RowLayout rl = padded_rows(E, R);
+  if (rows != 0) {
+    const int64_t need_rows =
+        std::min<int64_t>(static_cast<int64_t>(T) * K, static_cast<int64_t>(E) * R);
+    if (!valid_rows(rows) || rows < need_rows) return MOE_ERR_INVALID_ARG;
+    rl = RowLayout{R, 1, rows};
+  }
+  const size_t need = moe_dispatch_workspace_size(T, K, E);
+  if (workspace == nullptr || workspace_bytes < need || !aligned4(workspace)) return MOE_ERR_WORKSPACE;
+  const DeviceInfo* dev = nullptr;
+  if (moe_status st = check_device(&dev); st != MOE_OK) return st;
+  return from_cuda(launch_dispatch_quant_fp4(x, topk_idx, idx_bits, T, H, K, E, rl, format, x_gscale,
+                                             xq, xs, counts, src_map, dev_status,
+                                             static_cast<int32_t*>(workspace), dev->sm_count,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_gemm_gateup_fp4(const uint8_t* xq, const uint8_t* xs, const float* x_gscale,
+                               const int32_t* counts, int E, int R, int64_t rows, int H, int I,
+                               const uint8_t* w13, const uint8_t* w13_scale,
+                               const float* w13_gscale, const float* z_gscale, int format,
+                               uint8_t* zq, uint8_t* zs, int32_t* dev_status, int flags,
+                               moe_stream_t stream) {
+  if (!valid_experts(E, R) || !valid_hidden(H) || !valid_hidden(I) ||
+      !valid_fp4(format, x_gscale, w13_gscale, z_gscale) || !valid_cta_flags(flags))
+    return MOE_ERR_INVALID_ARG;
+  if (rows != 0 && !valid_rows(rows)) return MOE_ERR_INVALID_ARG;
+  if (xq == nullptr || xs == nullptr || counts == nullptr || w13 == nullptr || w13_scale == nullptr ||
+      zq == nullptr || zs == nullptr || dev_status == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(xq) || !aligned16(xs) || !aligned16(w13) || !aligned16(w13_scale) || !aligned16(zq) ||
+      !aligned16(zs) || !aligned4(x_gscale) || !aligned4(w13_gscale) || !aligned4(z_gscale))
+    return MOE_ERR_INVALID_ARG;
+  const DeviceInfo* dev = nullptr;
+  if (moe_status st = check_device(&dev); st != MOE_OK) return st;
+  return from_cuda(launch_gemm_gateup_fp4(
+      xq, xs, x_gscale, counts, E, rows != 0 ? RowLayout{R, 1, rows} : padded_rows(E, R), H, I, w13,
+      w13_scale, w13_gscale, z_gscale, format, zq, zs, dev_status, grid_limit(flags, dev->sm_count),
+      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_grouped_gemm_fp4(const uint8_t* a, const uint8_t* a_scale, const float* a_gscale,
+                                const int32_t* counts, int E, int R, int64_t rows, int K, int N,
+                                const uint8_t* w, const uint8_t* w_scale, const float* w_gscale,
+                                int format, void* out, int32_t* dev_status, int flags,
+                                moe_stream_t stream) {
+  if (!valid_experts(E, R) || !valid_hidden(K) || !valid_hidden(N) ||
+      !valid_fp4(format, a_gscale, w_gscale) || !valid_cta_flags(flags))
+    return MOE_ERR_INVALID_ARG;
+  if (rows != 0 && !valid_rows(rows)) return MOE_ERR_INVALID_ARG;
+  if (a == nullptr || a_scale == nullptr || counts == nullptr || w == nullptr || w_scale == nullptr ||
+      out == nullptr || dev_status == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(a_scale) || !aligned16(w) || !aligned16(w_scale) || !aligned16(out) ||
+      !aligned4(a_gscale) || !aligned4(w_gscale))
+    return MOE_ERR_INVALID_ARG;
+  const DeviceInfo* dev = nullptr;
+  if (moe_status st = check_device(&dev); st != MOE_OK) return st;
+  return from_cuda(launch_grouped_gemm_fp4(
+      a, a_scale, a_gscale, counts, E, rows != 0 ? RowLayout{R, 1, rows} : padded_rows(E, R), K, N, w,
+      w_scale, w_gscale, format, out, dev_status, grid_limit(flags, dev->sm_count),
+      reinterpret_cast<cudaStream_t>(stream)));
+}
+
 size_t moe_experts_w4_workspace_size(int T, int K, int H, int I) {
   if (T < 0 || T > kW4MaxTokens || K < 1 || K > 32 || !valid_hidden(H) || !valid_hidden(I)) return 0;
   return experts_w4_workspace(T, K, H, I);
