@@ -148,6 +148,21 @@ __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) 
                : "memory");
 }
 
+// One lane of a converged warp.  TMA and tcgen05 instructions take their operands
+// from uniform registers; where a single lane has branched off on its own lane
+// number the compiler moves every operand there one by one (50 to 70 clocks an
+// instruction), where the warp runs together up to here it does not.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+// A bounded wait of a whole warp: true in every lane, or in none.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
 // The async proxy (TMA, tcgen05) sees this thread's shared-memory stores.
 __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -17,7 +17,7 @@
 //    adjacent in the walk;
 //  - warp 0 streams codes with TMA: stages of K = 256, 128 bytes a row, the
 //    128-byte swizzle; kStages of them in a ring;
-//  - warps 4-6 lay the scales of a stage out in shared memory as tcgen05.cp
+//  - warps 2-7 lay the scales of a stage out in shared memory as tcgen05.cp
 //    wants them.  Scales are stored [row, K / B] like the codes, 16 (8) bytes a
 //    stage and row, while the MMA takes for every 64 of K one 32-bit word a row,
 //    the words of rows r, r + 32, r + 64, r + 96 side by side: a lane loads the
@@ -47,18 +47,17 @@ constexpr int kBN = 256;
 constexpr int kBK = 256;         // elements of a stage: 128 bytes of codes a row
 constexpr int kRowBytes = kBK / 2;
 constexpr int kStages = 3;
-constexpr int kScaleWarp0 = 4;   // warp 4: the rows' scales, 5 and 6: the weights'
-constexpr int kScaleWarps = 3;
+constexpr int kScaleWarp0 = 2;   // two each for the rows' scales and both halves of the columns'
+constexpr int kScaleWarps = 6;
 constexpr int kEpiWarp0 = 8;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
-// Register split: launched at 128 a thread; the producer's and the MMA's
-// warpgroup keeps 56, the scales' 72, the two epilogue warpgroups take 192.
+// Register split: launched at 128 a thread; the two warpgroups that feed the
+// tensor cores keep 72, the two epilogue warpgroups take 184.
 constexpr int kLaunchRegs = 128;
-constexpr int kCtrlRegs = 56;
-constexpr int kScaleRegs = 72;
-constexpr int kEpiRegs = 192;
-static_assert(kCtrlRegs + kScaleRegs + 2 * kEpiRegs == 4 * kLaunchRegs, "register split must fit the launch");
+constexpr int kCtrlRegs = 72;
+constexpr int kEpiRegs = 184;
+static_assert(2 * kCtrlRegs + 2 * kEpiRegs == 4 * kLaunchRegs, "register split must fit the launch");
 // BF16 rows are staged per epilogue warp: 32 rows x 64 bytes, padded to 80.
 constexpr int kStageRowBytes = 80;
 constexpr int kStageWarpBytes = 32 * kStageRowBytes;
@@ -175,30 +174,97 @@ __device__ __forceinline__ void tile_prefixes(const Fp4Args& a, Control* ctl) {
   __syncthreads();
 }
 
-// The kScales bytes of one row and stage as 32-bit words, in the widest loads
-// that the row pitch aligns; past the end of the row (the last stage of an odd
-// K / 128) zeros.  Through L2: the rows' scales are the launch before's.
-template <int kScales>
+// kWords 32-bit words of a row's scales (one stage's) in the widest loads that
+// the row pitch aligns; past the end of the row zeros.  Through L2: the rows'
+// scales are the launch before's.
+template <int kWords>
 __device__ __forceinline__ void load_scales(const uint8_t* row, int off, int pitch, uint32_t* w) {
-  if constexpr (kScales == 16) {
-    if ((pitch & 15) == 0) {
+#pragma unroll
+  for (int j = 0; j < kWords; ++j) w[j] = 0;
+  if (kWords == 4 && (pitch & 15) == 0) {
+    if (off < pitch) {
       const uint4 v = __ldcg(reinterpret_cast<const uint4*>(row + off));
       w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else {
-      const uint2 v = __ldcg(reinterpret_cast<const uint2*>(row + off));
-      const uint2 u = off + 8 < pitch ? __ldcg(reinterpret_cast<const uint2*>(row + off + 8))
-                                      : make_uint2(0, 0);
-      w[0] = v.x, w[1] = v.y, w[2] = u.x, w[3] = u.y;
     }
+  } else if ((pitch & 7) == 0) {
+#pragma unroll
+    for (int j = 0; j < kWords; j += 2)
+      if (off + 4 * j < pitch) {
+        const uint2 v = __ldcg(reinterpret_cast<const uint2*>(row + off + 4 * j));
+        w[j] = v.x, w[j + 1] = v.y;
+      }
   } else {
-    if ((pitch & 7) == 0) {
-      const uint2 v = __ldcg(reinterpret_cast<const uint2*>(row + off));
-      w[0] = v.x, w[1] = v.y;
-    } else {
-      w[0] = __ldcg(reinterpret_cast<const uint32_t*>(row + off));
-      w[1] = off + 4 < pitch ? __ldcg(reinterpret_cast<const uint32_t*>(row + off + 4)) : 0u;
-    }
+#pragma unroll
+    for (int j = 0; j < kWords; ++j)
+      if (off + 4 * j < pitch) w[j] = __ldcg(reinterpret_cast<const uint32_t*>(row + off + 4 * j));
   }
+}
+
+// One of the warps that lay scales out: block sw (0: the tile's rows, 1 and 2:
+// the halves of its columns), pairs of stages `par`, par + 2, ... of those that
+// each tile's stages make.  Lanes 2i and 2i + 1 take the first and the second
+// stage of rows i, 16 + i, ..., 112 + i (for NVFP4 a load asks for whole
+// sectors), so a stage's words of four rows 32 apart are one lane's.
+// Pairs, not more: a parity tells a slot's current use only from the one before,
+// and of the stages between a warp's own, which the other warp waits for, there
+// may be kStages - 1.
+template <int kFmt, bool kGateUp>
+__device__ __forceinline__ bool lay_out_scales(const Fp4Args& args, Control* ctl, uint8_t* smem,
+                                               int sw, int par, int tiles, int nkb, int lane) {
+  using L = Layout<kFmt>;
+  static_assert(kStages >= 3, "a pair of stages may lie between a warp's own");
+  const int pitch = args.K / kFp4Block<kFmt>;
+  const int nch = (nkb + 1) / 2;          // pairs of a tile
+  const int i = lane >> 1, h = lane & 1;
+  const uint8_t* base = nullptr;
+  int last = 0, at = -1;                  // the tile's last row, and its number
+  uint32_t w[8][L::kAtoms];
+  auto load = [&](int it, int ch) {
+    if (it >= tiles) return;
+    if (it != at) {
+      const Tile tl = decode_tile<kGateUp>(ctl, args, blockIdx.x + it * gridDim.x);
+      // rows past the tile's (and columns past N) repeat one: their products
+      // are not stored
+      last = sw == 0 ? tl.rows - 1 : (sw == 2 && tl.cols < kBN ? 0 : 127);
+      const long long first = sw == 0 ? tl.base : weight_row<kGateUp>(args, tl, last ? sw - 1 : 0);
+      base = (sw == 0 ? args.as : args.ws) + first * pitch;
+      at = it;
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      load_scales<L::kAtoms>(base + min(16 * t + i, last) * pitch, (2 * ch + h) * L::kScales, pitch, w[t]);
+  };
+  int it = par / nch, ch = par % nch;
+  load(it, ch);
+  while (it < tiles) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int kb = 2 * ch + p;
+      if (kb >= nkb) break;
+      const int n = it * nkb + kb, stage = n % kStages;
+      if (!warp_wait(&ctl->empty[stage], ((n / kStages) & 1) ^ 1, &ctl->abort)) return false;
+      if (h == p) {
+        // atom j of the rows at 512 j; of column half x at 1024 j + 512 x
+        uint8_t* dst = smem + stage * L::kStageBytes + L::kABytes + L::kBBytes +
+                       (sw == 0 ? 0 : L::kSaBytes + 512 * (sw - 1)) + 16 * i;
+        const int step = sw == 0 ? 512 : 1024;
+#pragma unroll
+        for (int j = 0; j < L::kAtoms; ++j) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            *reinterpret_cast<uint4*>(dst + j * step + 256 * t) =
+                make_uint4(w[t][j], w[t + 2][j], w[t + 4][j], w[t + 6][j]);
+        }
+        fence_proxy_async_shared();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->full[stage]);
+    }
+    ch += 2;
+    while (ch >= nch && it < tiles) ch -= nch, ++it;
+    load(it, ch);
+  }
+  return true;
 }
 
 template <int kFmt, bool kGateUp>
@@ -215,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_start();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&ctl->full[i], 1 + kScaleWarps);
+      mbar_init(&ctl->full[i], 1 + kScaleWarps / 2);   // a stage's scales: one of each two
       mbar_init(&ctl->empty[i], 1);
     }
     mbar_init(&ctl->tfull, 1);
@@ -244,153 +310,103 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     warpgroup_reg_dealloc<kCtrlRegs>();
-    if (lane == 0) {
-      int issued = 0;
-      bool ok = true;
-      for (int it = 0; it < tiles && ok; ++it) {
-        const Tile tl = decode_tile<kGateUp>(ctl, args, blockIdx.x + it * gridDim.x);
-        const int b0 = static_cast<int>(weight_row<kGateUp>(args, tl, 0));
-        const int b1 = static_cast<int>(weight_row<kGateUp>(args, tl, 1));
-        // only the valid rows are fetched (32, 64 or 128): the rest of the A
-        // tile keeps stale bytes, which reach only rows that are never stored
-        const int a_box = tl.rows <= 32 ? 32 : (tl.rows <= 64 ? 64 : kBM);
-        const CUtensorMap* ma = &maps.a[a_box == kBM ? 0 : (a_box == 64 ? 1 : 2)];
-        const uint32_t bytes = (a_box + tl.cols) * kRowBytes;
-        for (int kb = 0; kb < nkb; ++kb) {
-          const int stage = issued % kStages;
-          if (!mbar_wait(&ctl->empty[stage], ((issued / kStages) & 1) ^ 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sa = smem + stage * L::kStageBytes;
-          uint8_t* sb = sa + L::kABytes;
+    int issued = 0;
+    bool ok = true;
+    for (int it = 0; it < tiles && ok; ++it) {
+      const Tile tl = decode_tile<kGateUp>(ctl, args, blockIdx.x + it * gridDim.x);
+      const int b0 = static_cast<int>(weight_row<kGateUp>(args, tl, 0));
+      const int b1 = static_cast<int>(weight_row<kGateUp>(args, tl, 1));
+      // only the valid rows are fetched (32, 64 or 128): the rest of the A
+      // tile keeps stale bytes, which reach only rows that are never stored
+      const int a_box = tl.rows <= 32 ? 32 : (tl.rows <= 64 ? 64 : kBM);
+      const CUtensorMap* ma = &maps.a[a_box == kBM ? 0 : (a_box == 64 ? 1 : 2)];
+      const uint32_t bytes = (a_box + tl.cols) * kRowBytes;
+      for (int kb = 0; kb < nkb; ++kb) {
+        const int stage = issued % kStages;
+        if (!warp_wait(&ctl->empty[stage], ((issued / kStages) & 1) ^ 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sa = smem + stage * L::kStageBytes;
+        uint8_t* sb = sa + L::kABytes;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&ctl->full[stage], bytes);
           tma_load_2d(sa, ma, &ctl->full[stage], kb * kRowBytes, tl.base);
           tma_load_2d(sb, &maps.b, &ctl->full[stage], kb * kRowBytes, b0);
           if (tl.cols == kBN)
             tma_load_2d(sb + 128 * kRowBytes, &maps.b, &ctl->full[stage], kb * kRowBytes, b1);
-          ++issued;
         }
+        __syncwarp();
+        ++issued;
       }
-      if (!ok) *abort_flag = 1;
-      // No copy may land after the block exits.  full also takes the scale
-      // warps' arrivals, which an abort leaves out, so this wait is bounded too
-      // and then the copies have had the whole wait limit to land.
-      for (int i = 0; i < min(issued, kStages); ++i) {
-        const int n = issued - 1 - i;
-        drain_wait(&ctl->full[n % kStages], (n / kStages) & 1);
-      }
+    }
+    if (!ok) *abort_flag = 1;
+    // No copy may land after the block exits.  full also takes the scale
+    // warps' arrivals, which an abort leaves out, so this wait is bounded too
+    // and then the copies have had the whole wait limit to land.
+    for (int i = 0; i < min(issued, kStages); ++i) {
+      const int n = issued - 1 - i;
+      drain_wait(&ctl->full[n % kStages], (n / kStages) & 1);
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA
     warpgroup_reg_dealloc<kCtrlRegs>();
-    if (lane == 0) {
-      int consumed = 0;
-      bool ok = true;
-      for (int it = 0; it < tiles && ok; ++it) {
-        const int n_blk = (blockIdx.x + it * gridDim.x) % args.nt;
-        const int cols = kGateUp ? kBN : min(kBN, args.N - n_blk * kBN);
-        if (!mbar_wait(&ctl->tempty, (it & 1) ^ 1, abort_flag)) {
+    const uint32_t acc = __shfl_sync(0xffffffffu, tmem, 0);   // uniform
+    int consumed = 0;
+    bool ok = true;
+    for (int it = 0; it < tiles && ok; ++it) {
+      const int n_blk = (blockIdx.x + it * gridDim.x) % args.nt;
+      const int cols = kGateUp ? kBN : min(kBN, args.N - n_blk * kBN);
+      if (!warp_wait(&ctl->tempty, (it & 1) ^ 1, abort_flag)) {
+        ok = false;
+        break;
+      }
+      for (int kb = 0; kb < nkb; ++kb) {
+        const int stage = consumed % kStages;
+        if (!warp_wait(&ctl->full[stage], (consumed / kStages) & 1, abort_flag)) {
           ok = false;
           break;
         }
-        for (int kb = 0; kb < nkb; ++kb) {
-          const int stage = consumed % kStages;
-          if (!mbar_wait(&ctl->full[stage], (consumed / kStages) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * L::kStageBytes);
-          const uint32_t sfa = sa + L::kABytes + L::kBBytes, sfb = sfa + L::kSaBytes;
-          const uint64_t adesc = smem_desc_kmajor_sw128(sa);
-          const uint64_t bdesc = smem_desc_kmajor_sw128(sa + L::kABytes);
-#pragma unroll
-          for (int j = 0; j < L::kAtoms; ++j) {
-            tmem_copy_scales(tmem + kSfaCol + 4 * j, smem_desc_scales(sfa + 512 * j));
-            tmem_copy_scales(tmem + kSfbCol + 8 * j, smem_desc_scales(sfb + 1024 * j));
-            tmem_copy_scales(tmem + kSfbCol + 8 * j + 4, smem_desc_scales(sfb + 1024 * j + 512));
-          }
-          const int steps = half_end && kb == nkb - 1 ? 2 : 4;
+        tc_fence_after();
+        const uint32_t sa = smem_u32(smem) + stage * L::kStageBytes;
+        const uint32_t sfa = sa + L::kABytes + L::kBBytes, sfb = sfa + L::kSaBytes;
+        const uint64_t adesc = smem_desc_kmajor_sw128(sa);
+        const uint64_t bdesc = smem_desc_kmajor_sw128(sa + L::kABytes);
+        const int steps = half_end && kb == nkb - 1 ? 2 : 4;
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {   // 64 elements = 32 bytes = 2 descriptor units
             if (k >= steps) break;
             const int atom = k * L::kAtoms / 4, id = kFmt == kMxfp4 ? 2 * (k & 1) : 0;
+            if (k * L::kAtoms % 4 == 0) {
+              tmem_copy_scales(acc + kSfaCol + 4 * atom, smem_desc_scales(sfa + 512 * atom));
+              tmem_copy_scales(acc + kSfbCol + 8 * atom, smem_desc_scales(sfb + 1024 * atom));
+              tmem_copy_scales(acc + kSfbCol + 8 * atom + 4, smem_desc_scales(sfb + 1024 * atom + 512));
+            }
             const uint32_t idesc = cols == kBN ? idesc_fp4<kFmt>(kBM, kBN, id)
                                                : idesc_fp4<kFmt>(kBM, 128, id);
-            mma_fp4<kFmt>(tmem, adesc + 2 * k, bdesc + 2 * k, idesc, tmem + kSfaCol + 4 * atom,
-                          tmem + kSfbCol + 8 * atom, (kb | k) > 0 ? 1u : 0u);
+            mma_fp4<kFmt>(acc, adesc + 2 * k, bdesc + 2 * k, idesc, acc + kSfaCol + 4 * atom,
+                          acc + kSfbCol + 8 * atom, (kb | k) > 0 ? 1u : 0u);
           }
           mma_commit(&ctl->empty[stage]);
-          ++consumed;
+          if (kb == nkb - 1) mma_commit(&ctl->tfull);
         }
-        if (ok) mma_commit(&ctl->tfull);
-      }
-      if (!ok) *abort_flag = 1;
-      if (consumed > 0) {
-        mma_commit(&ctl->drain);
-        drain_wait(&ctl->drain, 0);
+        __syncwarp();
+        ++consumed;
       }
     }
-  } else if (warp < kScaleWarp0) {
-    warpgroup_reg_dealloc<kCtrlRegs>();   // warp 2 owns TMEM, warp 3 is spare
+    if (!ok) *abort_flag = 1;
+    if (consumed > 0) {
+      if (elect_one()) mma_commit(&ctl->drain);
+      __syncwarp();
+      drain_wait(&ctl->drain, 0);
+    }
   } else if (warp < kEpiWarp0) {
     // -------------------------------------------------------------- scales
-    warpgroup_reg_dealloc<kScaleRegs>();
-    const int sw = warp - kScaleWarp0;   // 0: the rows, 1 and 2: halves of the columns
-    if (sw < kScaleWarps) {
-      constexpr int kWords = L::kAtoms;          // 32-bit words of a row and stage
-      constexpr int kAhead = 2;                  // stages whose loads are in flight
-      const int pitch = args.K / kFp4Block<kFmt>;
-      const int n_total = tiles * nkb;
-      const uint8_t* row[4];
-      uint32_t w[kAhead][4][kWords];
-      int l_it = 0, l_kb = 0;                    // next stage to load
-      auto load = [&](uint32_t (*v)[kWords]) {
-        if (l_it >= tiles) return;
-        if (l_kb == 0) {
-          const Tile tl = decode_tile<kGateUp>(ctl, args, blockIdx.x + l_it * gridDim.x);
-          // rows past the tile's (and its columns past N) repeat its last one:
-          // their products are not stored
-          const int n = sw == 0 ? tl.rows : (sw == 2 && tl.cols < kBN ? 0 : 128);
-          const long long first = sw == 0 ? tl.base : weight_row<kGateUp>(args, tl, n ? sw - 1 : 0);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            row[q] = (sw == 0 ? args.as : args.ws) +
-                     (first + min(lane + 32 * q, max(n, 1) - 1)) * pitch;
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) load_scales<L::kScales>(row[q], l_kb * L::kScales, pitch, v[q]);
-        if (++l_kb == nkb) l_kb = 0, ++l_it;
-      };
-#pragma unroll
-      for (int d = 0; d < kAhead; ++d) load(w[d]);
-      bool ok = true;
-      for (int n0 = 0; n0 < n_total && ok; n0 += kAhead) {
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d) {
-          const int n = n0 + d;
-          if (n >= n_total || !ok) break;
-          const int stage = n % kStages;
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait(&ctl->empty[stage], ((n / kStages) & 1) ^ 1, abort_flag));
-          if (!ok) break;
-          // atom j of the rows at 512 j; of column half h at 1024 j + 512 h
-          uint8_t* dst = smem + stage * L::kStageBytes + L::kABytes + L::kBBytes +
-                         (sw == 0 ? 0 : L::kSaBytes + 512 * (sw - 1)) + 16 * lane;
-          const int step = sw == 0 ? 512 : 1024;
-#pragma unroll
-          for (int j = 0; j < kWords; ++j)
-            *reinterpret_cast<uint4*>(dst + j * step) =
-                make_uint4(w[d][0][j], w[d][1][j], w[d][2][j], w[d][3][j]);
-          fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->full[stage]);
-          load(w[d]);
-        }
-      }
-      if (!ok && lane == 0) *abort_flag = 1;
-    }
+    warpgroup_reg_dealloc<kCtrlRegs>();
+    const int sw = warp - kScaleWarp0;
+    if (!lay_out_scales<kFmt, kGateUp>(args, ctl, smem, sw % 3, sw / 3, tiles, nkb, lane) && lane == 0)
+      *abort_flag = 1;
   } else {
     // ------------------------------------------------------------ epilogue
     warpgroup_reg_alloc<kEpiRegs>();
