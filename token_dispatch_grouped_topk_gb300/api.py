@@ -612,15 +612,14 @@ def _gscale(g, n, dev, name):
     return None if g is None else _check(g, _F32, (n,), dev, name)
 
 
-def _gscale_rows(gscale, lead):
-    """(scales over the tensor, rows of each) of rows [*lead]: one over all of
-    them, or one per leading index of three-dimensional ones."""
-    rows = 1
-    for n in lead:
-        rows *= n
-    if gscale is None or gscale.numel() == 1 or len(lead) < 2:
-        return 1, max(rows, 1), rows
-    return lead[0], max(rows // max(lead[0], 1), 1), rows
+def _gscale_rows(gscale, t, rows, dev):
+    """(address of the scales over the tensor, rows of each) for the ``rows``
+    rows of ``t``: one scale over all of them, or one per leading index of a
+    three-dimensional ``t``."""
+    if gscale is None:
+        return None, rows or 1
+    n = t.shape[0] if t.dim() >= 3 and gscale.numel() != 1 else 1
+    return _check(gscale, _F32, (n,), dev, "gscale"), (rows // n if n else rows) or 1
 
 
 def moe_quantize_fp4(x, *, format: str = "nvfp4", gscale=None, xq=None, xs=None, stream=None):
@@ -630,17 +629,21 @@ def moe_quantize_fp4(x, *, format: str = "nvfp4", gscale=None, xq=None, xs=None,
     32, power-of-two scales, no ``gscale``).  Returns ``(xq [..., H/2], xs [...,
     H/16 or H/32])`` uint8."""
     fmt, block = _fp4(format)
-    *lead, H = x.shape
+    shape = x.shape
+    H = shape[-1]
+    lead = shape[:-1]
+    q_shape, s_shape = (*lead, H // 2), (*lead, H // block)
     dev = x.get_device()
-    n_g, per, rows = _gscale_rows(gscale, lead)
+    px = _check(x, _HALF_OR_F32, shape, dev, "x")
+    rows = x.numel() // H if H else 0
+    pg, per = _gscale_rows(gscale, x, rows, dev)
     if xq is None:
-        xq = _new((*lead, H // 2), torch.uint8, x.device, stream)
+        xq = _new(q_shape, torch.uint8, x.device, stream)
     if xs is None:
-        xs = _new((*lead, H // block), torch.uint8, x.device, stream)
+        xs = _new(s_shape, torch.uint8, x.device, stream)
     st = _lib.load().moe_quantize_fp4(
-        _check(x, _HALF_OR_F32, x.shape, dev, "x"), _bits(x), _gscale(gscale, n_g, dev, "gscale"),
-        per, rows, H, fmt, _check(xq, _U8, (*lead, H // 2), dev, "xq"),
-        _check(xs, _FP4_SCALES[format], (*lead, H // block), dev, "xs"), _stream_on(stream, dev))
+        px, _bits(x), pg, per, rows, H, fmt, _check(xq, _U8, q_shape, dev, "xq"),
+        _check(xs, _FP4_SCALES[format], s_shape, dev, "xs"), _stream_on(stream, dev))
     _lib.check("moe_quantize_fp4", st)
     return xq, xs
 
@@ -650,17 +653,19 @@ def moe_dequantize_fp4(xq, xs, *, format: str = "nvfp4", gscale=None, dtype=torc
     """The values of ``moe_quantize_fp4``'s codes and scales (moe_dequantize_fp4):
     ``out [..., H]`` in ``dtype``, bf16 or fp32."""
     fmt, block = _fp4(format)
-    *lead, half = xq.shape
-    H = 2 * half
+    shape = xq.shape
+    H = 2 * shape[-1]
+    lead = shape[:-1]
+    o_shape = (*lead, H)
     dev = xq.get_device()
-    n_g, per, rows = _gscale_rows(gscale, lead)
+    pq = _check(xq, _U8, shape, dev, "xq")
+    rows = 2 * xq.numel() // H if H else 0
+    pg, per = _gscale_rows(gscale, xq, rows, dev)
     if out is None:
-        out = _new((*lead, H), dtype, xq.device, stream)
+        out = _new(o_shape, dtype, xq.device, stream)
     st = _lib.load().moe_dequantize_fp4(
-        _check(xq, _U8, xq.shape, dev, "xq"),
-        _check(xs, _FP4_SCALES[format], (*lead, H // block), dev, "xs"),
-        _gscale(gscale, n_g, dev, "gscale"), per, rows, H, fmt,
-        _check(out, _HALF_OR_F32, (*lead, H), dev, "out"), _bits(out), _stream_on(stream, dev))
+        pq, _check(xs, _FP4_SCALES[format], (*lead, H // block), dev, "xs"), pg, per, rows, H, fmt,
+        _check(out, _HALF_OR_F32, o_shape, dev, "out"), _bits(out), _stream_on(stream, dev))
     _lib.check("moe_dequantize_fp4", st)
     return out
 

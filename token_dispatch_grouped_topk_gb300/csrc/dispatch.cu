@@ -182,7 +182,7 @@ __device__ void single_pass_bases(const IdT* __restrict__ topk_idx, int T, int K
     }
   }
   bad = __syncthreads_or(bad);
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
     int dropped = 0;
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
       counts[e] = min(s_tot[e], rl.R);
@@ -597,7 +597,8 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
 // every kept row.  The block's work is route_scatter_codes_kernel's: whole
 // 128-groups of its tokens' rows, shared evenly among its warps, the first
 // loads (and here the quantisation, which does not depend on where a row goes)
-// before the block finds its routes' slots.  A lane takes 16 values (two
+// before the block finds its routes' slots; with few blocks, blockIdx.z shares a
+// block's rows among several.  A lane takes 16 values (two
 // 16-byte loads, 8 bytes of codes), a warp 512 at a time, 1, 2 or 4 times a token.
 template <typename IdT, int kFmt, bool kSingle>
 __global__ void __launch_bounds__(kDispatchWarps * 32)
@@ -617,10 +618,13 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gw = blockIdx.x * kDispatchWarps + warp;
   const int tpw = 32 / K;
-  // the block's rows, this warp's share of them and its first
-  const int rows = min(kDispatchWarps * tpw, T - static_cast<int>(blockIdx.x) * kDispatchWarps * tpw);
+  // the rows whose slots the block finds, its part of them (blockIdx.z), this
+  // warp's share of that and its first
+  const int found = min(kDispatchWarps * tpw, T - static_cast<int>(blockIdx.x) * kDispatchWarps * tpw);
+  const int part = (found + gridDim.z - 1) / gridDim.z, z0 = blockIdx.z * part;
+  const int rows = max(0, min(part, found - z0));
   const int share = (rows + kDispatchWarps - 1) / kDispatchWarps;
-  const int t0 = blockIdx.x * kDispatchWarps * tpw + warp * share;
+  const int t0 = blockIdx.x * kDispatchWarps * tpw + z0 + warp * share;
   const int nch = H / 16;                           // 16-value chunks of a row
   const int g0 = blockIdx.y * groups_per_slice, ng = min(H / kGroup - g0, groups_per_slice);
   const int c0 = g0 * 8, nc = ng * 8;
@@ -680,12 +684,12 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
     for (int w = 0; w < warp; ++w) sl += s_cnt[w * E + r.e];
     if (sl < rl.R) q = (rl.packed ? s_rows[r.e] : r.e * rl.R) + sl;
   }
-  if (blockIdx.y == 0 && r.active) src_map[static_cast<int64_t>(r.t) * K + r.k] = q;
+  if (blockIdx.y == 0 && blockIdx.z == 0 && r.active) src_map[static_cast<int64_t>(r.t) * K + r.k] = q;
   if (lane < tpw * K) s_dest[warp * tpw * K + lane] = q;   // the block's routes in order
   if (share == tpw) __syncwarp();   // each warp's rows are the ones it found the slots of
   else __syncthreads();
 
-  const int* wdest = s_dest + warp * share * K;
+  const int* wdest = s_dest + (z0 + warp * share) * K;
   for (int tt0 = 0; tt0 < tokens; tt0 += batch) {
     if (tt0 > 0) {
       load(tt0);
@@ -1185,7 +1189,12 @@ cudaError_t dispatch_fp4_impl(const void* x, const IdT* topk_idx, int T, int H, 
   const size_t smem = (kDispatchWarps * E + kDispatchWarps * 32 + 3 * E + 1) * sizeof(int);
   auto kernel = one ? route_scatter_fp4_kernel<IdT, kFmt, true> : route_scatter_fp4_kernel<IdT, kFmt, false>;
   if ((err = allow_smem(kernel, smem)) != cudaSuccess) return err;
-  const dim3 grid(nblocks, hsplit);
+  // few blocks: several copy parts of the rows whose slots each of them finds,
+  // down to a row a warp
+  const int tokens = min(kDispatchWarps * (32 / K), T);
+  const int parts = max(1, min((tokens + kDispatchWarps - 1) / kDispatchWarps,
+                               2 * sm_count / (nblocks * hsplit)));
+  const dim3 grid(nblocks, hsplit, parts);
   const auto* x4 = static_cast<const uint4*>(x);
   auto* q2 = reinterpret_cast<uint2*>(xq);
   auto* s4 = reinterpret_cast<uint32_t*>(xs);

@@ -96,7 +96,7 @@ struct alignas(16) Control {
   uint32_t tmem_base;
   int abort;
   int blk_start[kMaxExperts + 1];
-  int cnt[kMaxExperts + 1];   // padded: clamped counts; packed: their prefix
+  int cnt[kMaxExperts + 1];   // prefix of the clamped counts
 };
 
 template <int kFmt>
@@ -124,7 +124,7 @@ __device__ __forceinline__ Tile decode_tile(const Control* ctl, const Fp4Args& a
   r.n_blk = t - blk * a.nt;
   r.e = find_expert(ctl->blk_start, a.E, blk);
   r.m_blk = blk - ctl->blk_start[r.e];
-  const int count = a.packed ? ctl->cnt[r.e + 1] - ctl->cnt[r.e] : ctl->cnt[r.e];
+  const int count = ctl->cnt[r.e + 1] - ctl->cnt[r.e];
   r.base = (a.packed ? ctl->cnt[r.e] : r.e * a.R) + r.m_blk * kBM;
   r.rows = min(kBM, count - r.m_blk * kBM);
   r.cols = kGateUp ? kBN : min(kBN, a.N - r.n_blk * kBN);   // 128 in the last slice of an odd N / 128
@@ -143,18 +143,20 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   mbar_wait(bar, parity, &dummy);
 }
 
-// First 128-row block of each expert, and its clamped count (padded) or first
-// row (packed), by warp 0; every thread of the block calls it.  The counts may
-// be the launch before's, still written while this one starts: they are read
-// through L2, after the wait.
+// First 128-row block of each expert, and the prefix of the clamped counts; every thread of the block calls it.  The counts may be the
+// launch before's, still written while this one starts: they are read through
+// L2, after the wait, by all threads at once (one round trip).
 __device__ __forceinline__ void tile_prefixes(const Fp4Args& a, Control* ctl) {
+  for (int e = threadIdx.x; e < a.E; e += kThreads)
+    ctl->cnt[e + 1] = max(0, min(__ldcg(a.counts + e), a.R));
+  __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int blocks = 0, rows = 0;
-    if (lane == 0) ctl->blk_start[0] = 0;
+    if (lane == 0) ctl->blk_start[0] = ctl->cnt[0] = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane;
-      const int c = e < a.E ? max(0, min(__ldcg(a.counts + e), a.R)) : 0;
+      const int c = e < a.E ? ctl->cnt[e + 1] : 0;
       int nb = (c + kBM - 1) / kBM, nr = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -163,13 +165,11 @@ __device__ __forceinline__ void tile_prefixes(const Fp4Args& a, Control* ctl) {
       }
       if (e < a.E) {
         ctl->blk_start[e + 1] = blocks + nb;
-        if (a.packed) ctl->cnt[e + 1] = rows + nr;
-        else ctl->cnt[e] = c;
+        ctl->cnt[e + 1] = rows + nr;
       }
       blocks += __shfl_sync(0xffffffffu, nb, 31);
       rows += __shfl_sync(0xffffffffu, nr, 31);
     }
-    if (a.packed && lane == 0) ctl->cnt[0] = 0;
   }
   __syncthreads();
 }

@@ -82,39 +82,54 @@ __global__ void __launch_bounds__(kThreads)
     dequantize_fp4_kernel(const uint2* __restrict__ xq, const uint8_t* __restrict__ xs,
                           const float* __restrict__ gscale, long long per_g, long long n_g,
                           long long chunks, uint4* __restrict__ out) {
+  constexpr int kDeep = 4;   // chunks a lane has in flight
   const long long step = static_cast<long long>(gridDim.x) * kThreads;
-  for (long long c = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; c < chunks; c += step) {
-    const uint2 q = __ldg(xq + c);
-    const uint8_t b = __ldg(xs + (kFmt == kNvfp4 ? c : c >> 1));
-    // 2^(b - 127) as fp32 bits (b = 0: the subnormal 2^-127; 255: NaN)
-    const float s = kFmt == kNvfp4 ? e4m3_to_f32(b)
-                                   : __uint_as_float(b == 255 ? 0x7FFFFFFFu
-                                                     : b == 0 ? 0x00400000u
-                                                              : static_cast<uint32_t>(b) << 23);
-    const float g = over_scale(gscale, per_g, n_g, c);
-    float f[16];
+  for (long long c0 = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; c0 < chunks;
+       c0 += step * kDeep) {
+    uint2 q[kDeep];
+    uint8_t b[kDeep];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t w = i < 4 ? q.x : q.y;
-      const __half2 h = __half2(__nv_cvt_fp4x2_to_halfraw2(
-          static_cast<__nv_fp4x2_storage_t>((w >> (8 * (i & 3))) & 0xFFu), __NV_E2M1));
-      // code * scale is exact (two bits times four), so one rounding by g
-      const float2 p = __half22float2(h);
-      f[2 * i] = p.x * s * g;
-      f[2 * i + 1] = p.y * s * g;
+    for (int u = 0; u < kDeep; ++u) {
+      const long long c = c0 + u * step;
+      if (c < chunks) {
+        q[u] = __ldg(xq + c);
+        b[u] = __ldg(xs + (kFmt == kNvfp4 ? c : c >> 1));
+      }
     }
-    if constexpr (kF32) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        out[4 * c + i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
-                                    __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3]));
-    } else {
+    for (int u = 0; u < kDeep; ++u) {
+      const long long c = c0 + u * step;
+      if (c >= chunks) break;
+      // 2^(b - 127) as fp32 bits (b = 0: the subnormal 2^-127; 255: NaN)
+      const float s = kFmt == kNvfp4 ? e4m3_to_f32(b[u])
+                                     : __uint_as_float(b[u] == 255 ? 0x7FFFFFFFu
+                                                       : b[u] == 0 ? 0x00400000u
+                                                                   : static_cast<uint32_t>(b[u]) << 23);
+      const float g = over_scale(gscale, per_g, n_g, c);
+      float f[16];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        out[2 * c + i] = make_uint4(pack_bf16x2_rn(f[8 * i], f[8 * i + 1]),
-                                    pack_bf16x2_rn(f[8 * i + 2], f[8 * i + 3]),
-                                    pack_bf16x2_rn(f[8 * i + 4], f[8 * i + 5]),
-                                    pack_bf16x2_rn(f[8 * i + 6], f[8 * i + 7]));
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w = i < 4 ? q[u].x : q[u].y;
+        const __half2 h = __half2(__nv_cvt_fp4x2_to_halfraw2(
+            static_cast<__nv_fp4x2_storage_t>((w >> (8 * (i & 3))) & 0xFFu), __NV_E2M1));
+        // code * scale is exact (two bits times four), so one rounding by g
+        const float2 p = __half22float2(h);
+        f[2 * i] = p.x * s * g;
+        f[2 * i + 1] = p.y * s * g;
+      }
+      if constexpr (kF32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          __stcs(out + 4 * c + i, make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
+                                             __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3])));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          __stcs(out + 2 * c + i, make_uint4(pack_bf16x2_rn(f[8 * i], f[8 * i + 1]),
+                                             pack_bf16x2_rn(f[8 * i + 2], f[8 * i + 3]),
+                                             pack_bf16x2_rn(f[8 * i + 4], f[8 * i + 5]),
+                                             pack_bf16x2_rn(f[8 * i + 6], f[8 * i + 7])));
+      }
     }
   }
 }
@@ -148,7 +163,7 @@ cudaError_t launch_dequantize_fp4(const uint8_t* xq, const uint8_t* xs, const fl
   const long long chunks = rows * (H / 16), per_g = rows_per_gscale * (H / 16);
   if (chunks == 0) return cudaSuccess;
   const long long n_g = (chunks + per_g - 1) / per_g;
-  const int grid = blocks_for(chunks, sm_count);
+  const int grid = blocks_for((chunks + 3) / 4, sm_count);
   auto kernel = format == kNvfp4 ? (out_bits == 32 ? dequantize_fp4_kernel<kNvfp4, true>
                                                    : dequantize_fp4_kernel<kNvfp4, false>)
                                  : (out_bits == 32 ? dequantize_fp4_kernel<kMxfp4, true>
