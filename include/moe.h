@@ -600,6 +600,18 @@ moe_status moe_experts_w4(const void* x, const void* topk_idx, int idx_bits, con
  *   product.
  *   Codes, scales and out of both products 16-byte aligned.  dev_status device
  *   int32 [2]: MOE_DEV_TIMEOUT may be ORed in.  flags: 0 or MOE_GEMM_MAX_CTAS(n).
+ *   Packed rows at or past `rows` are never touched, even if counts claim more.
+ *
+ * moe_layer_fp4         the whole branch: moe_dispatch_quant_fp4, both products
+ *   and moe_combine(_packed), on the caller's buffers xq, xs, zq, zs, out, y,
+ *   counts, src_map and dev_status (as above, all but the last three 16-byte
+ *   aligned).  When the gate/up tiles can fill only a few waves of SMs both
+ *   products run in one launch, each down tile starting once its 128-row block's
+ *   Z is written; MOE_GEMM_ONE_LAUNCH and MOE_GEMM_TWO_LAUNCHES in flags force a
+ *   form.  Results are those of the calls one by one, bit for bit.  workspace of
+ *   moe_layer_fp4_workspace_size(T, K, E, R, rows) bytes, int32-aligned scratch,
+ *   not shared with another call in flight.  T == 0: counts are zeroed and the
+ *   status reset.
  * ------------------------------------------------------------------------- */
 #define MOE_FP4_NVFP4 0
 #define MOE_FP4_MXFP4 1
@@ -625,6 +637,15 @@ moe_status moe_grouped_gemm_fp4(const uint8_t* a, const uint8_t* a_scale, const 
                                 const uint8_t* w, const uint8_t* w_scale, const float* w_gscale,
                                 int format, void* out, int32_t* dev_status, int flags,
                                 moe_stream_t stream);
+size_t moe_layer_fp4_workspace_size(int T, int K, int E, int R, int64_t rows);
+moe_status moe_layer_fp4(const void* x, const void* topk_idx, int idx_bits, const float* topk_w,
+                         int T, int H, int I, int K, int E, int R, int64_t rows, int format,
+                         const uint8_t* w13, const uint8_t* w13_scale, const uint8_t* w2,
+                         const uint8_t* w2_scale, const float* x_gscale, const float* w13_gscale,
+                         const float* z_gscale, const float* w2_gscale, uint8_t* xq, uint8_t* xs,
+                         uint8_t* zq, uint8_t* zs, void* out, void* y, int32_t* counts,
+                         int32_t* src_map, int32_t* dev_status, void* workspace,
+                         size_t workspace_bytes, int flags, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * moe_layer_stats -- the counts the pages account a layer by, for one routing:

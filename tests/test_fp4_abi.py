@@ -74,3 +74,25 @@ def test_products_reject_on_host(lib):
                 dict(counts=None), dict(w=None), dict(ws=None), dict(out=None), dict(st=None), dict(a=MIS),
                 dict(a_s=MIS), dict(w=MIS), dict(ws=MIS), dict(out=MIS)):
         assert _call(lib.moe_grouped_gemm_fp4, d, **bad) == -1, bad
+
+
+def test_layer_rejects_on_host(lib):
+    size = lib.moe_layer_fp4_workspace_size
+    assert size(112, 2, 8, 128, 0) >= lib.moe_dispatch_workspace_size(112, 2, 8) + 4 * 9
+    assert size(-1, 2, 8, 128, 0) == 0 and size(4, 33, 64, 8, 0) == 0 and size(4, 2, 8, 128, -1) == 0
+    d = dict(x=FAKE, idx=FAKE, bits=64, tw=FAKE, T=112, H=256, I=128, K=2, E=8, R=128, rows=0, fmt=0,
+             w13=FAKE, s13=FAKE, w2=FAKE, s2=FAKE, xg=FAKE, g13=FAKE, zg=FAKE, g2=FAKE, xq=FAKE, xs=FAKE,
+             zq=FAKE, zs=FAKE, out=FAKE, y=FAKE, counts=FAKE, src=FAKE, st=FAKE, ws=FAKE,
+             ws_bytes=1 << 20, flags=0, stream=None)
+    pointers = ("x", "idx", "tw", "w13", "s13", "w2", "s2", "xq", "xs", "zq", "zs", "out", "y", "counts",
+                "src", "st")
+    bad = [dict(T=-1), dict(H=200), dict(I=64), dict(K=0), dict(K=9), dict(E=0), dict(R=0), dict(rows=223),
+           dict(rows=-1), dict(bits=8), dict(fmt=2), dict(fmt=1), dict(fmt=1, xg=None, g13=None, zg=None),
+           dict(flags=1), dict(flags=6), dict(flags=8), dict(xg=MIS2)]
+    bad += [{k: None} for k in pointers]
+    bad += [{k: MIS} for k in pointers if k not in ("idx", "tw", "counts", "src", "st")]
+    for b in bad:
+        assert _call(lib.moe_layer_fp4, d, **b) == -1, b
+    assert _call(lib.moe_layer_fp4, d, ws=None) == -3
+    assert _call(lib.moe_layer_fp4, d, ws=MIS2) == -3
+    assert _call(lib.moe_layer_fp4, d, ws_bytes=size(112, 2, 8, 128, 0) - 1) == -3

@@ -257,6 +257,24 @@ def test_product(fmt, E, R, K, N, kind, packed):
 
 
 @pytest.mark.parametrize("fmt", FMT)
+def test_packed_rows_end_with_the_buffer(fmt):
+    """Counts that claim more packed rows than there are: those behind the
+    buffer are not touched, the ones inside are right."""
+    E, R, K, N, rows = 4, 200, 384, 256, 300
+    g = _gen(2)
+    room = torch.zeros(rows + 200, K, device=DEV)
+    room[:rows] = _randn(g, rows, K)
+    aq, a_s = api.moe_quantize_fp4(room, format=fmt)
+    w, w_s, wg = weights(E, N, K, 3, fmt)
+    out = torch.full((rows + 200, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    n = torch.tensor([200, 150, 200, 1 << 30], dtype=torch.int32, device=DEV)
+    api.moe_grouped_gemm_fp4(aq[:rows], a_s[:rows], n, w, w_s, format=fmt, w_gscale=wg, R=R, out=out[:rows])
+    assert (out[rows:] == 7.0).all()
+    _, ref, mag = _reference(aq[:rows], a_s[:rows], w, w_s, [200, 100, 0, 0], R, True, fmt, None, wg)
+    _check_product(out[:rows], ref, mag, K)
+
+
+@pytest.mark.parametrize("fmt", FMT)
 def test_product_of_every_code_and_scale(fmt):
     """Each pair of codes and each scale byte, exactly: one nonzero element a row."""
     E, K, N = 1, 256, 256
@@ -424,6 +442,18 @@ def test_layer(fmt, T, E, K, H, I, R, packed):
     other = api.MoeLayerBuffers(T, E, K, H, I, R, torch.device(DEV), packed=not packed, fp4=fmt,
                                 fp4_gscales=gs)
     assert torch.equal(other.forward(x, idx, p, *w), y)
+    # the stages one by one, and both launch forms of the products
+    lane.y.zero_()
+    lane.dispatch_quant(x, idx, p)
+    lane.gemms(*w)
+    lane.combine(p, lane.y)
+    assert torch.equal(lane.y, y)
+    for form in ("one", "two"):
+        lane.gemm_launch = form
+        for _ in range(3):
+            lane.y.zero_()
+            assert torch.equal(lane.forward(x, idx, p, *w), y) and lane.dev_status[0].item() & 4 == 0
+    lane.gemm_launch = None
     # captured and replayed with other tokens and routes
     x2, idx2, p2, _, _ = _layer(T, E, K, H, I, T + 5, fmt, pad=0.3)
     want = other.forward(x2, idx2, p2, *w).clone()

@@ -99,6 +99,9 @@ SIGNATURES = {
     "moe_grouped_gemm_fp4": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int64,
                                      c_int, c_int, c_void_p, c_void_p, c_void_p, c_int, c_void_p,
                                      c_void_p, c_int, c_void_p]),
+    "moe_layer_fp4_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int64]),
+    "moe_layer_fp4": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_int, c_int, c_int, c_int, c_int,
+                              c_int, c_int64, c_int, *[c_void_p] * 18, c_size_t, c_int, c_void_p]),
     "moe_layer_stats": (c_int, [c_void_p, c_int, c_void_p, c_int, c_int, c_int, c_int, c_int,
                                 c_void_p, c_void_p, c_void_p]),
     "moe_expert_compute_gemm_launches": (c_int, [c_int, c_int, c_int64, c_int, c_int]),

@@ -18,10 +18,28 @@ namespace {
 
 constexpr int kCombineWarps = 8;
 
+// A row of the expert outputs, streamed; chained: through L2, as the kernel before
+// writes it while this one already exists (the read-only path is for data that
+// nobody writes in a kernel's lifetime).
+template <bool kChained>
+__device__ __forceinline__ uint4 load_out(const uint4* p) {
+  if constexpr (kChained) {
+    uint4 v;
+    asm volatile("ld.global.cg.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+  } else {
+    return ld_stream(p);
+  }
+}
+
+template <bool kChained>
 __global__ void __launch_bounds__(kCombineWarps * 32)
-    combine_kernel(const uint4* __restrict__ out, const int32_t* __restrict__ src_map,
-                   const float* __restrict__ topk_w, int T, int H, int K, int64_t rows,
-                   uint4* __restrict__ y, int vec_per_slice) {
+    combine_kernel(const uint4* out, const int32_t* src_map, const float* __restrict__ topk_w, int T,
+                   int H, int K, int64_t rows, uint4* y, int vec_per_slice) {
+  if constexpr (kChained) asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ int s_q[kCombineWarps][32];
   __shared__ float s_w[kCombineWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -30,7 +48,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   int q = -1;
   float w = 0.f;
   if (lane < K) {
-    q = src_map[static_cast<int64_t>(t) * K + lane];
+    q = __ldcg(src_map + static_cast<int64_t>(t) * K + lane);
     w = topk_w[static_cast<int64_t>(t) * K + lane];
     if (q >= rows) q = -1;  // not a row of the output buffer: treated as no route
   }
@@ -55,7 +73,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
       uint4 raw[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (k0 + j < nk) raw[j] = ld_stream(out + static_cast<size_t>(s_q[warp][k0 + j]) * nvec + v);
+        if (k0 + j < nk) raw[j] = load_out<kChained>(out + static_cast<size_t>(s_q[warp][k0 + j]) * nvec + v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (k0 + j < nk) {
@@ -79,7 +97,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
 }  // namespace
 
 cudaError_t launch_combine(const void* out, const int32_t* src_map, const float* topk_w, int T,
-                           int H, int K, int64_t rows, void* y, int sm_count, cudaStream_t s) {
+                           int H, int K, int64_t rows, void* y, int sm_count, cudaStream_t s,
+                           bool chained) {
   if (T == 0) return cudaSuccess;
   const int nblocks = (T + kCombineWarps - 1) / kCombineWarps;
   const int nvec = H / 8;
@@ -88,9 +107,24 @@ cudaError_t launch_combine(const void* out, const int32_t* src_map, const float*
   hsplit = max(1, min(hsplit, nvec / 32));
   const int vec_per_slice = (nvec + hsplit - 1) / hsplit;
   hsplit = (nvec + vec_per_slice - 1) / vec_per_slice;
-  combine_kernel<<<dim3(nblocks, hsplit), kCombineWarps * 32, 0, s>>>(
-      static_cast<const uint4*>(out), src_map, topk_w, T, H, K, rows, static_cast<uint4*>(y),
-      vec_per_slice);
+  const dim3 grid(nblocks, hsplit);
+  const auto* o4 = static_cast<const uint4*>(out);
+  auto* y4 = static_cast<uint4*>(y);
+  if (chained) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kCombineWarps * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, combine_kernel<true>, o4, src_map, topk_w, T, H, K, rows, y4,
+                              vec_per_slice);
+  }
+  combine_kernel<false><<<grid, kCombineWarps * 32, 0, s>>>(o4, src_map, topk_w, T, H, K, rows, y4,
+                                                            vec_per_slice);
   return cudaGetLastError();
 }
 

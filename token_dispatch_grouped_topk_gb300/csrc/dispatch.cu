@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
                              RowLayout rl, int nblocks, const int32_t* base, int32_t* counts,
                              uint2* __restrict__ xq, uint32_t* __restrict__ xs,
                              int32_t* __restrict__ src_map, int32_t* dev_status,
-                             int groups_per_slice, int log_u) {
+                             int groups_per_slice, int log_u, int* zero, int n_zero) {
   extern __shared__ int smem[];
   int* s_cnt = smem;                           // [kDispatchWarps][E]
   int* s_dest = smem + kDispatchWarps * E;     // [kDispatchWarps][32]
@@ -656,6 +656,8 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
     }
   };
   load(0);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+    for (int i = threadIdx.x; i < n_zero; i += blockDim.x) zero[i] = 0;
 
   for (int i = threadIdx.x; i < kDispatchWarps * E; i += blockDim.x) s_cnt[i] = 0;
   if (kSingle) {
@@ -1164,7 +1166,8 @@ template <typename IdT, int kFmt>
 cudaError_t dispatch_fp4_impl(const void* x, const IdT* topk_idx, int T, int H, int K, int E,
                               RowLayout rl, const float* xg, uint8_t* xq, uint8_t* xs,
                               int32_t* counts, int32_t* src_map, int32_t* dev_status,
-                              int32_t* hist, int sm_count, cudaStream_t s) {
+                              int32_t* hist, int sm_count, cudaStream_t s, int* zero,
+                              int n_zero) {
   const int nblocks = dispatch_blocks(T, K);
   const bool one = single_pass(T, K);
   cudaError_t err;
@@ -1200,9 +1203,9 @@ cudaError_t dispatch_fp4_impl(const void* x, const IdT* topk_idx, int T, int H, 
   auto* s4 = reinterpret_cast<uint32_t*>(xs);
   if (!one)
     return launch_chained(kernel, grid, kDispatchWarps * 32, smem, s, x4, xg, topk_idx, T, H, K, E, rl,
-                          nblocks, hist, counts, q2, s4, src_map, dev_status, gps, log_u);
+                          nblocks, hist, counts, q2, s4, src_map, dev_status, gps, log_u, zero, n_zero);
   kernel<<<grid, kDispatchWarps * 32, smem, s>>>(x4, xg, topk_idx, T, H, K, E, rl, nblocks, hist, counts,
-                                                 q2, s4, src_map, dev_status, gps, log_u);
+                                                 q2, s4, src_map, dev_status, gps, log_u, zero, n_zero);
   return cudaGetLastError();
 }
 }  // namespace
@@ -1211,21 +1214,21 @@ cudaError_t launch_dispatch_quant_fp4(const void* x, const void* topk_idx, int i
                                       int H, int K, int E, RowLayout rl, int format,
                                       const float* xg, uint8_t* xq, uint8_t* xs, int32_t* counts,
                                       int32_t* src_map, int32_t* dev_status, int32_t* hist,
-                                      int sm_count, cudaStream_t s) {
+                                      int sm_count, cudaStream_t s, int* zero, int n_zero) {
   if (idx_bits == 32) {
     const auto* ids = static_cast<const int32_t*>(topk_idx);
     return format == kNvfp4
                ? dispatch_fp4_impl<int32_t, kNvfp4>(x, ids, T, H, K, E, rl, xg, xq, xs, counts, src_map,
-                                                    dev_status, hist, sm_count, s)
+                                                    dev_status, hist, sm_count, s, zero, n_zero)
                : dispatch_fp4_impl<int32_t, kMxfp4>(x, ids, T, H, K, E, rl, xg, xq, xs, counts, src_map,
-                                                    dev_status, hist, sm_count, s);
+                                                    dev_status, hist, sm_count, s, zero, n_zero);
   }
   const auto* ids = static_cast<const int64_t*>(topk_idx);
   return format == kNvfp4
              ? dispatch_fp4_impl<int64_t, kNvfp4>(x, ids, T, H, K, E, rl, xg, xq, xs, counts, src_map,
-                                                  dev_status, hist, sm_count, s)
+                                                  dev_status, hist, sm_count, s, zero, n_zero)
              : dispatch_fp4_impl<int64_t, kMxfp4>(x, ids, T, H, K, E, rl, xg, xq, xs, counts, src_map,
-                                                  dev_status, hist, sm_count, s);
+                                                  dev_status, hist, sm_count, s, zero, n_zero);
 }
 
 }  // namespace moe

@@ -53,10 +53,10 @@ constexpr int kEpiWarp0 = 8;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
 // Register split: launched at 128 a thread; the two warpgroups that feed the
-// tensor cores keep 72, the two epilogue warpgroups take 184.
+// tensor cores keep 96, the two epilogue warpgroups take 160.
 constexpr int kLaunchRegs = 128;
-constexpr int kCtrlRegs = 72;
-constexpr int kEpiRegs = 184;
+constexpr int kCtrlRegs = 96;
+constexpr int kEpiRegs = 160;
 static_assert(2 * kCtrlRegs + 2 * kEpiRegs == 4 * kLaunchRegs, "register split must fit the launch");
 // BF16 rows are staged per epilogue warp: 32 rows x 64 bytes, padded to 80.
 constexpr int kStageRowBytes = 80;
@@ -65,26 +65,41 @@ constexpr int kMaxExperts = 1024;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSfaCol = 256, kSfbCol = 272;   // scale columns behind the accumulator
 
+// What a launch computes: the gate/up product, the down product (any product),
+// or both, each down tile starting once its block's gate/up tiles are done.
+constexpr int kGateUp = 0;
+constexpr int kDown = 1;
+constexpr int kBoth = 2;
+// A launch of both takes tiles by a ticket and passes them to its warps through
+// a ring of this many slots.
+constexpr int kTileSlots = 8;
+
+struct Product {
+  const uint8_t* as;   // [rows, K / B] scales of the rows
+  const uint8_t* ws;   // [E, weight rows, K / B] scales of the weights
+  const float* ag;     // [1] scale over the rows, or null
+  const float* wg;     // [E] scale over an expert's weights, or null
+  int K, N;            // N: output features (gate/up: I)
+  int nt;              // N slices per 128-row block
+};
+
 struct Fp4Args {
   const int32_t* counts;
-  const uint8_t* as;    // [rows, K / B] scales of the rows
-  const uint8_t* ws;    // [E, weight rows, K / B] scales of the weights
-  const float* ag;      // [1] scale over the rows, or null
-  const float* wg;      // [E] scale over an expert's weights, or null
+  Product g[2];         // [0] gate/up, [1] down
   const float* zg;      // gate/up: [1] scale over Z, or null
-  uint8_t* zq;          // gate/up: [rows, N / 2]
-  uint8_t* zs;          // gate/up: [rows, N / B]
+  uint8_t* zq;          // gate/up: [rows, I / 2]
+  uint8_t* zs;          // gate/up: [rows, I / B]
   __nv_bfloat16* out;   // down: [rows, N]
-  int E, R, K, N;       // N: output features (gate/up: I)
-  int nt;               // N slices per 128-row block
+  int* sched;           // both: [0] tile ticket, [1 + b] epilogue warps done with block b
+  int E, R;
   int packed;
   long long rows;       // buffer rows
   int32_t* dev_status;
 };
 
 struct Fp4Maps {
-  CUtensorMap a[3];   // rows: boxes of 128, 64 and 32
-  CUtensorMap b;
+  CUtensorMap a[2][3];   // rows: boxes of 128, 64 and 32
+  CUtensorMap b[2];
 };
 
 struct alignas(16) Control {
@@ -93,8 +108,11 @@ struct alignas(16) Control {
   uint64_t tfull;
   uint64_t tempty;
   uint64_t drain;
+  uint64_t tile_full[kTileSlots];
+  uint64_t tile_empty[kTileSlots];
   uint32_t tmem_base;
   int abort;
+  int tile_slot[kTileSlots];
   int blk_start[kMaxExperts + 1];
   int cnt[kMaxExperts + 1];   // prefix of the clamped counts
 };
@@ -114,28 +132,61 @@ struct Layout {
 };
 
 struct Tile {
-  int e, m_blk, n_blk, rows, cols, base;
+  int gu;   // a gate/up tile
+  int blk, e, n_blk, rows, cols, base;
+  int nkb;  // stages
 };
 
-template <bool kGateUp>
+// Tile t: the N slices of one 128-row block adjacent; a launch of both lists all
+// gate/up tiles before all down tiles.
+template <int kMode>
 __device__ __forceinline__ Tile decode_tile(const Control* ctl, const Fp4Args& a, int t) {
   Tile r;
-  const int blk = t / a.nt;
-  r.n_blk = t - blk * a.nt;
-  r.e = find_expert(ctl->blk_start, a.E, blk);
-  r.m_blk = blk - ctl->blk_start[r.e];
+  const int gu_tiles = kMode == kBoth ? ctl->blk_start[a.E] * a.g[0].nt : 0;
+  r.gu = kMode == kGateUp || (kMode == kBoth && t < gu_tiles);
+  const Product& g = a.g[r.gu ? 0 : 1];
+  const int local = r.gu ? t : t - gu_tiles;
+  r.blk = local / g.nt;
+  r.n_blk = local - r.blk * g.nt;
+  r.e = find_expert(ctl->blk_start, a.E, r.blk);
+  const int m0 = (r.blk - ctl->blk_start[r.e]) * kBM;
   const int count = ctl->cnt[r.e + 1] - ctl->cnt[r.e];
-  r.base = (a.packed ? ctl->cnt[r.e] : r.e * a.R) + r.m_blk * kBM;
-  r.rows = min(kBM, count - r.m_blk * kBM);
-  r.cols = kGateUp ? kBN : min(kBN, a.N - r.n_blk * kBN);   // 128 in the last slice of an odd N / 128
+  r.base = (a.packed ? ctl->cnt[r.e] : r.e * a.R) + m0;
+  // packed rows past the buffer, which only wrong counts claim, are no rows
+  r.rows = min(min(kBM, count - m0), static_cast<int>(max(0LL, min(static_cast<long long>(kBM), a.rows - r.base))));
+  r.cols = r.gu ? kBN : min(kBN, g.N - r.n_blk * kBN);   // 128 in the last slice of an odd N / 128
+  r.nkb = (g.K + kBK - 1) / kBK;
   return r;
 }
 
 // First weight row of column half h of a tile.
-template <bool kGateUp>
-__device__ __forceinline__ long long weight_row(const Fp4Args& a, const Tile& t, int h) {
-  if (kGateUp) return static_cast<long long>(t.e) * 2 * a.N + static_cast<long long>(h) * a.N + t.n_blk * 128;
-  return static_cast<long long>(t.e) * a.N + t.n_blk * kBN + h * 128;
+__device__ __forceinline__ int weight_row(const Fp4Args& a, const Tile& t, int h) {
+  return t.gu ? (2 * t.e + h) * a.g[0].N + t.n_blk * 128 : t.e * a.g[1].N + t.n_blk * kBN + h * 128;
+}
+
+// A warp's tile number `it`: its number in the list, -1 behind the last, -2 if a
+// wait ran out.
+template <int kMode>
+__device__ __forceinline__ int claim_tile(Control* ctl, int it, int total, int lane) {
+  if (kMode != kBoth) {
+    const int t = blockIdx.x + it * gridDim.x;
+    return t < total ? t : -1;
+  }
+  const int slot = it % kTileSlots;
+  if (!warp_wait(&ctl->tile_full[slot], (it / kTileSlots) & 1, &ctl->abort)) return -2;
+  const int t = ctl->tile_slot[slot];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&ctl->tile_empty[slot]);
+  return t;
+}
+
+// Z is written by ordinary stores and read by TMA, in a launch of both by
+// another block: a proxy fence on either side.
+__device__ __forceinline__ void fence_proxy_async_global() {
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+__device__ __forceinline__ void red_add_release_gpu(int* p, int v) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
@@ -201,73 +252,68 @@ __device__ __forceinline__ void load_scales(const uint8_t* row, int off, int pit
 }
 
 // One of the warps that lay scales out: block sw (0: the tile's rows, 1 and 2:
-// the halves of its columns), pairs of stages `par`, par + 2, ... of those that
-// each tile's stages make.  Lanes 2i and 2i + 1 take the first and the second
-// stage of rows i, 16 + i, ..., 112 + i (for NVFP4 a load asks for whole
-// sectors), so a stage's words of four rows 32 apart are one lane's.
+// the halves of its columns), every other pair of stages of each tile, counted
+// on over the tiles.  Lanes 2i and 2i + 1 take the first and the second stage of
+// rows i, 16 + i, ..., 112 + i (for NVFP4 a load asks for whole sectors), so a
+// stage's words of four rows 32 apart are one lane's.
 // Pairs, not more: a parity tells a slot's current use only from the one before,
 // and of the stages between a warp's own, which the other warp waits for, there
 // may be kStages - 1.
-template <int kFmt, bool kGateUp>
+template <int kFmt, int kMode>
 __device__ __forceinline__ bool lay_out_scales(const Fp4Args& args, Control* ctl, uint8_t* smem,
-                                               int sw, int par, int tiles, int nkb, int lane) {
+                                               int sw, int par, int total, int lane) {
   using L = Layout<kFmt>;
   static_assert(kStages >= 3, "a pair of stages may lie between a warp's own");
-  const int pitch = args.K / kFp4Block<kFmt>;
-  const int nch = (nkb + 1) / 2;          // pairs of a tile
   const int i = lane >> 1, h = lane & 1;
-  const uint8_t* base = nullptr;
-  int last = 0, at = -1;                  // the tile's last row, and its number
-  uint32_t w[8][L::kAtoms];
-  auto load = [&](int it, int ch) {
-    if (it >= tiles) return;
-    if (it != at) {
-      const Tile tl = decode_tile<kGateUp>(ctl, args, blockIdx.x + it * gridDim.x);
-      // rows past the tile's (and columns past N) repeat one: their products
-      // are not stored
-      last = sw == 0 ? tl.rows - 1 : (sw == 2 && tl.cols < kBN ? 0 : 127);
-      const long long first = sw == 0 ? tl.base : weight_row<kGateUp>(args, tl, last ? sw - 1 : 0);
-      base = (sw == 0 ? args.as : args.ws) + first * pitch;
-      at = it;
-    }
+  int pairs = 0, stages = 0;   // of the tiles before
+  for (int it = 0;; ++it) {
+    const int t = claim_tile<kMode>(ctl, it, total, lane);
+    if (t < 0) return t == -1;
+    const Tile tl = decode_tile<kMode>(ctl, args, t);
+    const Product& g = args.g[tl.gu ? 0 : 1];
+    const int pitch = g.K / kFp4Block<kFmt>;
+    // rows past the tile's (and columns past N) repeat one: their products are
+    // not stored
+    const int last = sw == 0 ? max(tl.rows - 1, 0) : (sw == 2 && tl.cols < kBN ? 0 : 127);
+    const long long first = sw == 0 ? min(static_cast<long long>(tl.base), args.rows - 1)
+                                    : weight_row(args, tl, last ? sw - 1 : 0);
+    const uint8_t* base = (sw == 0 ? g.as : g.ws) + first * pitch;
+    const int nch = (tl.nkb + 1) / 2;
+    for (int ch = (par ^ pairs) & 1; ch < nch; ch += 2) {
+      uint32_t w[8][L::kAtoms];
 #pragma unroll
-    for (int t = 0; t < 8; ++t)
-      load_scales<L::kAtoms>(base + min(16 * t + i, last) * pitch, (2 * ch + h) * L::kScales, pitch, w[t]);
-  };
-  int it = par / nch, ch = par % nch;
-  load(it, ch);
-  while (it < tiles) {
+      for (int r = 0; r < 8; ++r)
+        load_scales<L::kAtoms>(base + min(16 * r + i, last) * pitch, (2 * ch + h) * L::kScales, pitch, w[r]);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int kb = 2 * ch + p;
-      if (kb >= nkb) break;
-      const int n = it * nkb + kb, stage = n % kStages;
-      if (!warp_wait(&ctl->empty[stage], ((n / kStages) & 1) ^ 1, &ctl->abort)) return false;
-      if (h == p) {
-        // atom j of the rows at 512 j; of column half x at 1024 j + 512 x
-        uint8_t* dst = smem + stage * L::kStageBytes + L::kABytes + L::kBBytes +
-                       (sw == 0 ? 0 : L::kSaBytes + 512 * (sw - 1)) + 16 * i;
-        const int step = sw == 0 ? 512 : 1024;
+      for (int p = 0; p < 2; ++p) {
+        const int kb = 2 * ch + p;
+        if (kb >= tl.nkb) break;
+        const int n = stages + kb, stage = n % kStages;
+        if (!warp_wait(&ctl->empty[stage], ((n / kStages) & 1) ^ 1, &ctl->abort)) return false;
+        if (h == p) {
+          // atom j of the rows at 512 j; of column half x at 1024 j + 512 x
+          uint8_t* dst = smem + stage * L::kStageBytes + L::kABytes + L::kBBytes +
+                         (sw == 0 ? 0 : L::kSaBytes + 512 * (sw - 1)) + 16 * i;
+          const int step = sw == 0 ? 512 : 1024;
 #pragma unroll
-        for (int j = 0; j < L::kAtoms; ++j) {
+          for (int j = 0; j < L::kAtoms; ++j) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-            *reinterpret_cast<uint4*>(dst + j * step + 256 * t) =
-                make_uint4(w[t][j], w[t + 2][j], w[t + 4][j], w[t + 6][j]);
+            for (int r = 0; r < 2; ++r)
+              *reinterpret_cast<uint4*>(dst + j * step + 256 * r) =
+                  make_uint4(w[r][j], w[r + 2][j], w[r + 4][j], w[r + 6][j]);
+          }
+          fence_proxy_async_shared();
         }
-        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->full[stage]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->full[stage]);
     }
-    ch += 2;
-    while (ch >= nch && it < tiles) ch -= nch, ++it;
-    load(it, ch);
+    pairs += nch;
+    stages += tl.nkb;
   }
-  return true;
 }
 
-template <int kFmt, bool kGateUp>
+template <int kFmt, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_fp4_kernel(const __grid_constant__ Fp4Maps maps, const Fp4Args args) {
   using L = Layout<kFmt>;
@@ -287,10 +333,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ctl->tfull, 1);
     mbar_init(&ctl->tempty, kEpiWarps);
     mbar_init(&ctl->drain, 1);
+    for (int i = 0; i < kTileSlots; ++i) {
+      mbar_init(&ctl->tile_full[i], 1);
+      mbar_init(&ctl->tile_empty[i], 1 + kScaleWarps + kEpiWarps);
+    }
     ctl->abort = 0;
     fence_barrier_init();
   }
-  if (warp == 0 && lane < 4) tma_prefetch_desc(lane < 3 ? &maps.a[lane] : &maps.b);
+  if (warp == 0 && lane < 8 && (kMode == kBoth || (lane >> 2) == kMode))
+    tma_prefetch_desc((lane & 3) < 3 ? &maps.a[lane >> 2][lane & 3] : &maps.b[lane >> 2]);
   if (warp == 2) {
     tmem_alloc(&ctl->tmem_base, kTmemCols);
     tmem_relinquish();
@@ -300,11 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tile_prefixes(args, ctl);   // its barrier also publishes the mbarriers and the TMEM address
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
-  const int total = ctl->blk_start[args.E] * args.nt;
-  const int tiles = total > static_cast<int>(blockIdx.x)
-                        ? (total - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
-  const int nkb = (args.K + kBK - 1) / kBK;
-  const bool half_end = args.K % kBK != 0;   // the last stage holds 128 elements
+  const int total = ctl->blk_start[args.E] * ((kMode == kDown ? 0 : args.g[0].nt) +
+                                              (kMode == kGateUp ? 0 : args.g[1].nt));
   volatile int* abort_flag = &ctl->abort;
 
   if (warp == 0) {
@@ -312,16 +360,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     warpgroup_reg_dealloc<kCtrlRegs>();
     int issued = 0;
     bool ok = true;
-    for (int it = 0; it < tiles && ok; ++it) {
-      const Tile tl = decode_tile<kGateUp>(ctl, args, blockIdx.x + it * gridDim.x);
-      const int b0 = static_cast<int>(weight_row<kGateUp>(args, tl, 0));
-      const int b1 = static_cast<int>(weight_row<kGateUp>(args, tl, 1));
+    for (int it = 0; ok; ++it) {
+      int t = blockIdx.x + it * gridDim.x;
+      if (kMode == kBoth) {
+        // Tiles are taken in list order by whichever blocks run, so the gate/up
+        // tiles that a down tile waits for are held by running blocks, which
+        // wait on nothing before them.
+        const int slot = it % kTileSlots;
+        if (!warp_wait(&ctl->tile_empty[slot], ((it / kTileSlots) & 1) ^ 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) t = atomicAdd(args.sched, 1);
+        t = __shfl_sync(0xffffffffu, t, 0);
+      }
+      if (t >= total) t = -1;
+      Tile tl{};
+      if (t >= 0) tl = decode_tile<kMode>(ctl, args, t);
+      if (kMode == kBoth) {
+        // A down tile is passed on once its block's Z is written: who takes it
+        // from the ring is then behind Z's stores.
+        if (t >= 0 && !tl.gu) {
+          if (!__all_sync(0xffffffffu, wait_count(args.sched + 1 + tl.blk, kEpiWarps * args.g[0].nt, abort_flag))) {
+            ok = false;
+            break;
+          }
+          fence_proxy_async_global();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          ctl->tile_slot[it % kTileSlots] = t;
+          mbar_arrive(&ctl->tile_full[it % kTileSlots]);
+        }
+      }
+      if (t < 0) break;
+      const int g = tl.gu ? 0 : 1;
+      const int b0 = weight_row(args, tl, 0), b1 = weight_row(args, tl, 1);
       // only the valid rows are fetched (32, 64 or 128): the rest of the A
       // tile keeps stale bytes, which reach only rows that are never stored
       const int a_box = tl.rows <= 32 ? 32 : (tl.rows <= 64 ? 64 : kBM);
-      const CUtensorMap* ma = &maps.a[a_box == kBM ? 0 : (a_box == 64 ? 1 : 2)];
+      const CUtensorMap* ma = &maps.a[g][a_box == kBM ? 0 : (a_box == 64 ? 1 : 2)];
+      const CUtensorMap* mb = &maps.b[g];
       const uint32_t bytes = (a_box + tl.cols) * kRowBytes;
-      for (int kb = 0; kb < nkb; ++kb) {
+      for (int kb = 0; kb < tl.nkb; ++kb) {
         const int stage = issued % kStages;
         if (!warp_wait(&ctl->empty[stage], ((issued / kStages) & 1) ^ 1, abort_flag)) {
           ok = false;
@@ -332,9 +413,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
           mbar_arrive_expect_tx(&ctl->full[stage], bytes);
           tma_load_2d(sa, ma, &ctl->full[stage], kb * kRowBytes, tl.base);
-          tma_load_2d(sb, &maps.b, &ctl->full[stage], kb * kRowBytes, b0);
+          tma_load_2d(sb, mb, &ctl->full[stage], kb * kRowBytes, b0);
           if (tl.cols == kBN)
-            tma_load_2d(sb + 128 * kRowBytes, &maps.b, &ctl->full[stage], kb * kRowBytes, b1);
+            tma_load_2d(sb + 128 * kRowBytes, mb, &ctl->full[stage], kb * kRowBytes, b1);
         }
         __syncwarp();
         ++issued;
@@ -354,14 +435,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t acc = __shfl_sync(0xffffffffu, tmem, 0);   // uniform
     int consumed = 0;
     bool ok = true;
-    for (int it = 0; it < tiles && ok; ++it) {
-      const int n_blk = (blockIdx.x + it * gridDim.x) % args.nt;
-      const int cols = kGateUp ? kBN : min(kBN, args.N - n_blk * kBN);
+    for (int it = 0; ok; ++it) {
+      const int t = claim_tile<kMode>(ctl, it, total, lane);
+      if (t < 0) {
+        ok = t == -1;
+        break;
+      }
+      const Tile tl = decode_tile<kMode>(ctl, args, t);
+      const bool half_end = args.g[tl.gu ? 0 : 1].K % kBK != 0;   // the last stage holds 128 elements
       if (!warp_wait(&ctl->tempty, (it & 1) ^ 1, abort_flag)) {
         ok = false;
         break;
       }
-      for (int kb = 0; kb < nkb; ++kb) {
+      for (int kb = 0; kb < tl.nkb; ++kb) {
         const int stage = consumed % kStages;
         if (!warp_wait(&ctl->full[stage], (consumed / kStages) & 1, abort_flag)) {
           ok = false;
@@ -372,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sfa = sa + L::kABytes + L::kBBytes, sfb = sfa + L::kSaBytes;
         const uint64_t adesc = smem_desc_kmajor_sw128(sa);
         const uint64_t bdesc = smem_desc_kmajor_sw128(sa + L::kABytes);
-        const int steps = half_end && kb == nkb - 1 ? 2 : 4;
+        const int steps = half_end && kb == tl.nkb - 1 ? 2 : 4;
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {   // 64 elements = 32 bytes = 2 descriptor units
@@ -383,13 +469,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_copy_scales(acc + kSfbCol + 8 * atom, smem_desc_scales(sfb + 1024 * atom));
               tmem_copy_scales(acc + kSfbCol + 8 * atom + 4, smem_desc_scales(sfb + 1024 * atom + 512));
             }
-            const uint32_t idesc = cols == kBN ? idesc_fp4<kFmt>(kBM, kBN, id)
-                                               : idesc_fp4<kFmt>(kBM, 128, id);
+            const uint32_t idesc = tl.cols == kBN ? idesc_fp4<kFmt>(kBM, kBN, id)
+                                                  : idesc_fp4<kFmt>(kBM, 128, id);
             mma_fp4<kFmt>(acc, adesc + 2 * k, bdesc + 2 * k, idesc, acc + kSfaCol + 4 * atom,
                           acc + kSfbCol + 8 * atom, (kb | k) > 0 ? 1u : 0u);
           }
           mma_commit(&ctl->empty[stage]);
-          if (kb == nkb - 1) mma_commit(&ctl->tfull);
+          if (kb == tl.nkb - 1) mma_commit(&ctl->tfull);
         }
         __syncwarp();
         ++consumed;
@@ -405,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------- scales
     warpgroup_reg_dealloc<kCtrlRegs>();
     const int sw = warp - kScaleWarp0;
-    if (!lay_out_scales<kFmt, kGateUp>(args, ctl, smem, sw % 3, sw / 3, tiles, nkb, lane) && lane == 0)
+    if (!lay_out_scales<kFmt, kMode>(args, ctl, smem, sw % 3, sw / 3, total, lane) && lane == 0)
       *abort_flag = 1;
   } else {
     // ------------------------------------------------------------ epilogue
@@ -415,22 +501,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ch = ew >> 2;     // half of the tile's columns
     const int row = lq * 32 + lane;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(lq * 32) << 16);
-    // gate/up: gate columns 64 ch.. and up columns 128 + 64 ch..; down: 128 ch..
-    const uint32_t col0 = kGateUp ? 64 * ch : 128 * ch;
-    const uint32_t col1 = kGateUp ? 128 + 64 * ch : 128 * ch + 64;
-    const float ag = args.ag ? __ldcg(args.ag) : 1.f;
-    const float zg = kGateUp && args.zg ? __ldcg(args.zg) : 1.f;
+    const float zg = kMode != kDown && args.zg ? __ldcg(args.zg) : 1.f;
     const float six_zg = __fmul_rn(6.f, zg);
     bool ok = true;
-    for (int it = 0; it < tiles; ++it) {
-      const Tile tl = decode_tile<kGateUp>(ctl, args, blockIdx.x + it * gridDim.x);
-      const float alpha = args.wg ? ag * __ldg(args.wg + tl.e) : ag;
-      if (!mbar_wait(&ctl->tfull, it & 1, abort_flag)) {
+    for (int it = 0;; ++it) {
+      const int t = claim_tile<kMode>(ctl, it, total, lane);
+      if (t < 0) {
+        ok = t == -1;
+        break;
+      }
+      const Tile tl = decode_tile<kMode>(ctl, args, t);
+      const Product& g = args.g[tl.gu ? 0 : 1];
+      const float alpha = (g.ag ? __ldcg(g.ag) : 1.f) * (g.wg ? __ldg(g.wg + tl.e) : 1.f);
+      // gate/up: gate columns 64 ch.. and up columns 128 + 64 ch..; down: 128 ch..
+      const uint32_t col0 = tl.gu ? 64 * ch : 128 * ch;
+      const uint32_t col1 = tl.gu ? 128 + 64 * ch : 128 * ch + 64;
+      if (!warp_wait(&ctl->tfull, it & 1, abort_flag)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      __syncwarp();
       uint32_t p0[64], p1[64];
       tmem_load64_sync(t_lane + col0, p0);
       tmem_load64_sync(t_lane + col1, p1);
@@ -438,8 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->tempty);
       const long long grow = static_cast<long long>(tl.base) + row;
-      const bool valid = row < tl.rows && grow < args.rows;
-      if constexpr (kGateUp) {
+      const bool valid = row < tl.rows;
+      if (kMode == kGateUp || (kMode == kBoth && tl.gu)) {
         // SiLU with the fast exponential and division: their few ulp are far
         // below a 4-bit step
         float z[64];
@@ -462,14 +552,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             codes[b * (kB / 8) + i] = fp4_pack8(z + b * kB + 8 * i, mult);
         }
         if (valid) {
-          uint4* q = reinterpret_cast<uint4*>(args.zq + grow * (args.N / 2) + tl.n_blk * 64 + ch * 32);
+          uint4* q = reinterpret_cast<uint4*>(args.zq + grow * (g.N / 2) + tl.n_blk * 64 + ch * 32);
           q[0] = make_uint4(codes[0], codes[1], codes[2], codes[3]);
           q[1] = make_uint4(codes[4], codes[5], codes[6], codes[7]);
-          uint8_t* s = args.zs + grow * (args.N / kB) + (tl.n_blk * 128 + ch * 64) / kB;
+          uint8_t* s = args.zs + grow * (g.N / kB) + (tl.n_blk * 128 + ch * 64) / kB;
           if constexpr (kFmt == kNvfp4) *reinterpret_cast<uint32_t*>(s) = scales;
           else *reinterpret_cast<uint16_t*>(s) = static_cast<uint16_t>(scales);
         }
-      } else {
+        if (kMode == kBoth) {   // this warp's part of the block's Z, to the down tiles
+          fence_proxy_async_global();
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) red_add_release_gpu(args.sched + 1 + tl.blk, 1);
+        }
+      } else if (kMode != kGateUp) {
         // BF16 rows through the warp's stage: each round the lanes leave 32
         // columns of their rows, then the warp writes 8 rows x 64 bytes per store
         const unsigned vmask = __ballot_sync(0xffffffffu, valid);
@@ -477,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* stage = out_stage + ew * kStageWarpBytes;
           uint4* srow = reinterpret_cast<uint4*>(stage + lane * kStageRowBytes);
           const int c = lane & 3;
-          __nv_bfloat16* gbase = args.out + (static_cast<long long>(tl.base) + lq * 32 + (lane >> 2)) * args.N +
+          __nv_bfloat16* gbase = args.out + (static_cast<long long>(tl.base) + lq * 32 + (lane >> 2)) * g.N +
                                  tl.n_blk * kBN + ch * 128 + 8 * c;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
@@ -499,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if ((vmask >> (8 * i + (lane >> 2))) & 1u) {
                 const uint4 v = *reinterpret_cast<const uint4*>(
                     stage + (8 * i + (lane >> 2)) * kStageRowBytes + 16 * c);
-                *reinterpret_cast<uint4*>(gbase + static_cast<long long>(8 * i) * args.N + 32 * r) = v;
+                *reinterpret_cast<uint4*>(gbase + static_cast<long long>(8 * i) * g.N + 32 * r) = v;
               }
             }
             __syncwarp();
@@ -524,34 +620,37 @@ cudaError_t make_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t r
   return make_map_rows128(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, cols, rows, box_rows);
 }
 
-template <int kFmt, bool kGateUp>
-cudaError_t launch_impl(const uint8_t* a, const uint8_t* w, const Fp4Args& args, int sm_count,
+// The most 128-row blocks that a launch can have.
+long long max_blocks(int E, RowLayout rl) {
+  const long long padded = static_cast<long long>(E) * ((rl.R + kBM - 1) / kBM);
+  return rl.packed ? std::min<long long>(padded, rl.rows / kBM + std::min<long long>(E, rl.rows)) : padded;
+}
+
+cudaError_t product_maps(Fp4Maps* m, int g, const uint8_t* a, uint64_t rows, const uint8_t* w,
+                         uint64_t w_rows, int K) {
+  cudaError_t err = cudaSuccess;
+  for (int i = 0; i < 3 && err == cudaSuccess; ++i) err = make_map(&m->a[g][i], a, K / 2, rows, kBM >> i);
+  if (err == cudaSuccess) err = make_map(&m->b[g], w, K / 2, w_rows, 128);
+  return err;
+}
+
+template <int kFmt, int kMode>
+cudaError_t launch_impl(const Fp4Maps& maps, const Fp4Args& args, long long max_tiles, int sm_count,
                         cudaStream_t s) {
   using L = Layout<kFmt>;
   if (args.E > kMaxExperts) return cudaErrorInvalidValue;
-  auto* kernel = grouped_fp4_kernel<kFmt, kGateUp>;
+  auto* kernel = grouped_fp4_kernel<kFmt, kMode>;
   // The register split assumes exactly kLaunchRegs a thread; with any other
   // count the epilogue's increase could wait forever, so refuse to launch.
   static const int compiled_regs = [] {
     cudaFuncAttributes attr{};
-    return cudaFuncGetAttributes(&attr, grouped_fp4_kernel<kFmt, kGateUp>) == cudaSuccess ? attr.numRegs : -1;
+    return cudaFuncGetAttributes(&attr, grouped_fp4_kernel<kFmt, kMode>) == cudaSuccess ? attr.numRegs : -1;
   }();
   if (compiled_regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  const long long padded = static_cast<long long>(args.E) * ((args.R + kBM - 1) / kBM);
-  const long long blocks =
-      args.packed ? std::min<long long>(padded, (args.rows + kBM - 1) / kBM + args.E) : padded;
-  const int grid = static_cast<int>(std::min<long long>(blocks * args.nt, sm_count));
+  const int grid = static_cast<int>(std::min<long long>(max_tiles, sm_count));
   if (grid <= 0) return cudaSuccess;
-  Fp4Maps maps{};
-  const uint64_t rows = static_cast<uint64_t>(args.rows), row_bytes = args.K / 2;
-  cudaError_t err = make_map(&maps.a[0], a, row_bytes, rows, 128);
-  if (err == cudaSuccess) err = make_map(&maps.a[1], a, row_bytes, rows, 64);
-  if (err == cudaSuccess) err = make_map(&maps.a[2], a, row_bytes, rows, 32);
-  if (err == cudaSuccess)
-    err = make_map(&maps.b, w, row_bytes, static_cast<uint64_t>(args.E) * args.N * (kGateUp ? 2 : 1), 128);
-  if (err == cudaSuccess)
-    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(L::kSmem));
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(L::kSmem));
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
@@ -566,18 +665,18 @@ cudaError_t launch_impl(const uint8_t* a, const uint8_t* w, const Fp4Args& args,
   return cudaLaunchKernelEx(&cfg, kernel, maps, args);
 }
 
-Fp4Args common_args(const uint8_t* as, const float* ag, const int32_t* counts, int E, RowLayout rl,
-                    int K, int N, const uint8_t* ws, const float* wg, int32_t* dev_status) {
+template <int kMode>
+cudaError_t launch_format(int format, const Fp4Maps& maps, const Fp4Args& args, long long max_tiles,
+                          int sm_count, cudaStream_t s) {
+  return format == kNvfp4 ? launch_impl<kNvfp4, kMode>(maps, args, max_tiles, sm_count, s)
+                          : launch_impl<kMxfp4, kMode>(maps, args, max_tiles, sm_count, s);
+}
+
+Fp4Args common_args(const int32_t* counts, int E, RowLayout rl, int32_t* dev_status) {
   Fp4Args a{};
   a.counts = counts;
-  a.as = as;
-  a.ag = ag;
-  a.ws = ws;
-  a.wg = wg;
   a.E = E;
   a.R = rl.R;
-  a.K = K;
-  a.N = N;
   a.packed = rl.packed;
   a.rows = rl.rows;
   a.dev_status = dev_status;
@@ -591,24 +690,56 @@ cudaError_t launch_gemm_gateup_fp4(const uint8_t* xq, const uint8_t* xs, const f
                                    const uint8_t* w13, const uint8_t* s13, const float* g13,
                                    const float* zg, int format, uint8_t* zq, uint8_t* zs,
                                    int32_t* dev_status, int sm_count, cudaStream_t s) {
-  Fp4Args a = common_args(xs, xg, counts, E, rl, H, I, s13, g13, dev_status);
+  Fp4Maps maps{};
+  cudaError_t err = product_maps(&maps, 0, xq, rl.rows, w13, static_cast<uint64_t>(E) * 2 * I, H);
+  if (err != cudaSuccess) return err;
+  Fp4Args a = common_args(counts, E, rl, dev_status);
+  a.g[0] = Product{xs, s13, xg, g13, H, I, I / 128};
   a.zg = zg;
   a.zq = zq;
   a.zs = zs;
-  a.nt = I / 128;
-  return format == kNvfp4 ? launch_impl<kNvfp4, true>(xq, w13, a, sm_count, s)
-                          : launch_impl<kMxfp4, true>(xq, w13, a, sm_count, s);
+  return launch_format<kGateUp>(format, maps, a, max_blocks(E, rl) * a.g[0].nt, sm_count, s);
 }
 
 cudaError_t launch_grouped_gemm_fp4(const uint8_t* aq, const uint8_t* as, const float* ag,
                                     const int32_t* counts, int E, RowLayout rl, int K, int N,
                                     const uint8_t* w, const uint8_t* ws, const float* wg, int format,
                                     void* out, int32_t* dev_status, int sm_count, cudaStream_t s) {
-  Fp4Args a = common_args(as, ag, counts, E, rl, K, N, ws, wg, dev_status);
+  Fp4Maps maps{};
+  cudaError_t err = product_maps(&maps, 1, aq, rl.rows, w, static_cast<uint64_t>(E) * N, K);
+  if (err != cudaSuccess) return err;
+  Fp4Args a = common_args(counts, E, rl, dev_status);
+  a.g[1] = Product{as, ws, ag, wg, K, N, (N + kBN - 1) / kBN};
   a.out = static_cast<__nv_bfloat16*>(out);
-  a.nt = (N + kBN - 1) / kBN;
-  return format == kNvfp4 ? launch_impl<kNvfp4, false>(aq, w, a, sm_count, s)
-                          : launch_impl<kMxfp4, false>(aq, w, a, sm_count, s);
+  return launch_format<kDown>(format, maps, a, max_blocks(E, rl) * a.g[1].nt, sm_count, s);
+}
+
+size_t gemm_fp4_sync_ints(int E, RowLayout rl) { return 1 + static_cast<size_t>(max_blocks(E, rl)); }
+
+bool gemm_fp4_prefer_one_launch(int E, RowLayout rl, int I, int sm_count) {
+  return max_blocks(E, rl) * (I / 128) <= 16LL * sm_count;
+}
+
+cudaError_t launch_gemm_both_fp4(const uint8_t* xq, const uint8_t* xs, const float* xg,
+                                 const int32_t* counts, int E, RowLayout rl, int H, int I,
+                                 const uint8_t* w13, const uint8_t* s13, const float* g13,
+                                 const uint8_t* w2, const uint8_t* s2, const float* g2,
+                                 const float* zg, int format, uint8_t* zq, uint8_t* zs, void* out,
+                                 int* sync, int32_t* dev_status, int sm_count, cudaStream_t s) {
+  Fp4Maps maps{};
+  cudaError_t err = product_maps(&maps, 0, xq, rl.rows, w13, static_cast<uint64_t>(E) * 2 * I, H);
+  if (err == cudaSuccess)
+    err = product_maps(&maps, 1, zq, rl.rows, w2, static_cast<uint64_t>(E) * H, I);
+  if (err != cudaSuccess) return err;
+  Fp4Args a = common_args(counts, E, rl, dev_status);
+  a.g[0] = Product{xs, s13, xg, g13, H, I, I / 128};
+  a.g[1] = Product{zs, s2, zg, g2, I, H, (H + kBN - 1) / kBN};
+  a.zg = zg;
+  a.zq = zq;
+  a.zs = zs;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.sched = sync;
+  return launch_format<kBoth>(format, maps, a, max_blocks(E, rl) * (a.g[0].nt + a.g[1].nt), sm_count, s);
 }
 
 }  // namespace moe

@@ -121,8 +121,10 @@ cudaError_t launch_gemm_gateup_down(const uint8_t* xq, const float* xs, const in
 // ----- weighted combine
 // rows = the number of rows of `out` (E * R padded, the buffer's rows packed);
 // a src_map entry outside [0, rows) is treated like -1.
+// chained: it may be launched while the kernel before it still runs, and waits.
 cudaError_t launch_combine(const void* out, const int32_t* src_map, const float* topk_w, int T,
-                           int H, int K, int64_t rows, void* y, int sm_count, cudaStream_t s);
+                           int H, int K, int64_t rows, void* y, int sm_count, cudaStream_t s,
+                           bool chained = false);
 
 // ----- expert parallelism across ranks (ep.cu)
 // Send plan of one source rank: send_x [T * min(K, W), H] one payload row per
@@ -194,7 +196,8 @@ cudaError_t launch_dispatch_quant_fp4(const void* x, const void* topk_idx, int i
                                       int H, int K, int E, RowLayout rl, int format,
                                       const float* xg, uint8_t* xq, uint8_t* xs, int32_t* counts,
                                       int32_t* src_map, int32_t* dev_status, int32_t* hist,
-                                      int sm_count, cudaStream_t s);
+                                      int sm_count, cudaStream_t s, int* zero = nullptr,
+                                      int n_zero = 0);   // zero: n_zero ints that it clears
 // rows of ragged experts times their weights; null scales over a tensor: 1
 cudaError_t launch_gemm_gateup_fp4(const uint8_t* xq, const uint8_t* xs, const float* xg,
                                    const int32_t* counts, int E, RowLayout rl, int H, int I,
@@ -205,6 +208,18 @@ cudaError_t launch_grouped_gemm_fp4(const uint8_t* aq, const uint8_t* as, const 
                                     const int32_t* counts, int E, RowLayout rl, int K, int N,
                                     const uint8_t* w, const uint8_t* ws, const float* wg, int format,
                                     void* out, int32_t* dev_status, int sm_count, cudaStream_t s);
+
+// Both products in one launch: a down tile starts as soon as its 128-row block's
+// gate/up tiles have written their Z.  sync: gemm_fp4_sync_ints ints, cleared
+// before (by the dispatch); counts as that dispatch left them.
+size_t gemm_fp4_sync_ints(int E, RowLayout rl);
+bool gemm_fp4_prefer_one_launch(int E, RowLayout rl, int I, int sm_count);
+cudaError_t launch_gemm_both_fp4(const uint8_t* xq, const uint8_t* xs, const float* xg,
+                                 const int32_t* counts, int E, RowLayout rl, int H, int I,
+                                 const uint8_t* w13, const uint8_t* s13, const float* g13,
+                                 const uint8_t* w2, const uint8_t* s2, const float* g2,
+                                 const float* zg, int format, uint8_t* zq, uint8_t* zs, void* out,
+                                 int* sync, int32_t* dev_status, int sm_count, cudaStream_t s);
 
 // ----- layer statistics of one routing (kLayerStats 64-bit counters):
 // [0] valid routes, [1] kept routes, [2] messages (sum over tokens of the

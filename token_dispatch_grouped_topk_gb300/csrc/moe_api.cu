@@ -595,6 +595,81 @@ moe_status moe_grouped_gemm_fp4(const uint8_t* a, const uint8_t* a_scale, const 
       reinterpret_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+RowLayout layer_rows(int E, int R, int64_t rows) {
+  return rows != 0 ? RowLayout{R, 1, rows} : padded_rows(E, R);
+}
+}  // namespace
+
+size_t moe_layer_fp4_workspace_size(int T, int K, int E, int R, int64_t rows) {
+  if (T < 0 || K < 1 || K > 32 || !valid_experts(E, R) || (rows != 0 && !valid_rows(rows))) return 0;
+  return moe_dispatch_workspace_size(T, K, E) +
+         align_up(gemm_fp4_sync_ints(E, layer_rows(E, R, rows)) * sizeof(int), 256);
+}
+
+moe_status moe_layer_fp4(const void* x, const void* topk_idx, int idx_bits, const float* topk_w,
+                         int T, int H, int I, int K, int E, int R, int64_t rows, int format,
+                         const uint8_t* w13, const uint8_t* w13_scale, const uint8_t* w2,
+                         const uint8_t* w2_scale, const float* x_gscale, const float* w13_gscale,
+                         const float* z_gscale, const float* w2_gscale, uint8_t* xq, uint8_t* xs,
+                         uint8_t* zq, uint8_t* zs, void* out, void* y, int32_t* counts,
+                         int32_t* src_map, int32_t* dev_status, void* workspace,
+                         size_t workspace_bytes, int flags, moe_stream_t stream) {
+  if (T < 0 || !valid_hidden(H) || !valid_hidden(I) || !valid_experts(E, R) || K < 1 || K > 32 || K > E)
+    return MOE_ERR_INVALID_ARG;
+  if ((idx_bits != 32 && idx_bits != 64) || !valid_fp4(format, x_gscale, w13_gscale, z_gscale) ||
+      !valid_fp4(format, w2_gscale))
+    return MOE_ERR_INVALID_ARG;
+  if (!valid_gemm_flags(flags) || (flags & MOE_W13_INTERLEAVED)) return MOE_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(T) * K > (int64_t{1} << 31) - 1) return MOE_ERR_INVALID_ARG;
+  if (rows != 0 && (!valid_rows(rows) || rows < std::min<int64_t>(static_cast<int64_t>(T) * K,
+                                                                  static_cast<int64_t>(E) * R)))
+    return MOE_ERR_INVALID_ARG;
+  if (counts == nullptr || dev_status == nullptr || w13 == nullptr || w13_scale == nullptr ||
+      w2 == nullptr || w2_scale == nullptr || xq == nullptr || xs == nullptr || zq == nullptr ||
+      zs == nullptr || out == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (x == nullptr || topk_idx == nullptr || topk_w == nullptr || src_map == nullptr || y == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(w13) || !aligned16(w13_scale) || !aligned16(w2) ||
+      !aligned16(w2_scale) || !aligned16(xq) || !aligned16(xs) || !aligned16(zq) || !aligned16(zs) ||
+      !aligned16(out) || !aligned4(x_gscale) || !aligned4(w13_gscale) || !aligned4(z_gscale) ||
+      !aligned4(w2_gscale))
+    return MOE_ERR_INVALID_ARG;
+  const size_t hist_bytes = moe_dispatch_workspace_size(T, K, E);
+  if (workspace == nullptr || workspace_bytes < moe_layer_fp4_workspace_size(T, K, E, R, rows) ||
+      !aligned4(workspace))
+    return MOE_ERR_WORKSPACE;
+  const DeviceInfo* dev = nullptr;
+  if (moe_status st = check_device(&dev); st != MOE_OK) return st;
+  const RowLayout rl = layer_rows(E, R, rows);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int* sync = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + hist_bytes);
+  const bool one = (flags & MOE_GEMM_ONE_LAUNCH)     ? true
+                   : (flags & MOE_GEMM_TWO_LAUNCHES) ? false
+                                                     : gemm_fp4_prefer_one_launch(E, rl, I, dev->sm_count);
+  const int grid = grid_limit(flags, dev->sm_count);
+  cudaError_t err = launch_dispatch_quant_fp4(
+      x, topk_idx, idx_bits, T, H, K, E, rl, format, x_gscale, xq, xs, counts, src_map, dev_status,
+      static_cast<int32_t*>(workspace), dev->sm_count, s, sync,
+      one ? static_cast<int>(gemm_fp4_sync_ints(E, rl)) : 0);
+  if (err != cudaSuccess || T == 0) return from_cuda(err);
+  if (one) {
+    err = launch_gemm_both_fp4(xq, xs, x_gscale, counts, E, rl, H, I, w13, w13_scale, w13_gscale, w2,
+                               w2_scale, w2_gscale, z_gscale, format, zq, zs, out, sync, dev_status,
+                               grid, s);
+  } else {
+    err = launch_gemm_gateup_fp4(xq, xs, x_gscale, counts, E, rl, H, I, w13, w13_scale, w13_gscale,
+                                 z_gscale, format, zq, zs, dev_status, grid, s);
+    if (err == cudaSuccess)
+      err = launch_grouped_gemm_fp4(zq, zs, z_gscale, counts, E, rl, I, H, w2, w2_scale, w2_gscale,
+                                    format, out, dev_status, grid, s);
+  }
+  if (err == cudaSuccess)
+    err = launch_combine(out, src_map, topk_w, T, H, K, rl.rows, y, dev->sm_count, s, true);
+  return from_cuda(err);
+}
+
 size_t moe_experts_w4_workspace_size(int T, int K, int H, int I) {
   if (T < 0 || T > kW4MaxTokens || K < 1 || K > 32 || !valid_hidden(H) || !valid_hidden(I)) return 0;
   return experts_w4_workspace(T, K, H, I);
