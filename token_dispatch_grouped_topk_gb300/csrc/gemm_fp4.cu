@@ -716,8 +716,14 @@ cudaError_t launch_grouped_gemm_fp4(const uint8_t* aq, const uint8_t* as, const 
 
 size_t gemm_fp4_sync_ints(int E, RowLayout rl) { return 1 + static_cast<size_t>(max_blocks(E, rl)); }
 
-bool gemm_fp4_prefer_one_launch(int E, RowLayout rl, int I, int sm_count) {
-  return max_blocks(E, rl) * (I / 128) <= 16LL * sm_count;
+bool gemm_fp4_prefer_one_launch(int E, RowLayout rl, int I, long long mean_rows, int sm_count) {
+  // Whole layers, one launch against two (us): one token of 256 experts 69 / 73,
+  // 16 tokens 348 / 365 (14 waves of tiles at most, half a row an expert), 256
+  // tokens of 64 experts 139 / 155 (6), 512: 149 / 165 (8), 1024: 179 / 179 (10),
+  // 2048: 275 / 258 (15), 4096 of 128: 508 / 474 (30).  The one launch fills the
+  // last gate/up wave with down tiles and starts once, but every tile costs a
+  // ticket and Z a flush; where weights bound the products that is hidden.
+  return max_blocks(E, rl) * (I / 128) <= 10LL * sm_count || mean_rows <= 64;
 }
 
 cudaError_t launch_gemm_both_fp4(const uint8_t* xq, const uint8_t* xs, const float* xg,

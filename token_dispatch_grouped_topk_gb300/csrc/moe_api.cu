@@ -647,7 +647,8 @@ moe_status moe_layer_fp4(const void* x, const void* topk_idx, int idx_bits, cons
   int* sync = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + hist_bytes);
   const bool one = (flags & MOE_GEMM_ONE_LAUNCH)     ? true
                    : (flags & MOE_GEMM_TWO_LAUNCHES) ? false
-                                                     : gemm_fp4_prefer_one_launch(E, rl, I, dev->sm_count);
+                                                     : gemm_fp4_prefer_one_launch(E, rl, I, static_cast<long long>(T) * K / E,
+                                                                                  dev->sm_count);
   const int grid = grid_limit(flags, dev->sm_count);
   cudaError_t err = launch_dispatch_quant_fp4(
       x, topk_idx, idx_bits, T, H, K, E, rl, format, x_gscale, xq, xs, counts, src_map, dev_status,
