@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const Tile tl = decode_tile<kMode>(ctl, args, t);
       const Product& g = args.g[tl.gu ? 0 : 1];
-      const float alpha = (g.ag ? __ldcg(g.ag) : 1.f) * (g.wg ? __ldg(g.wg + tl.e) : 1.f);
+      const float alpha = (g.ag ? __ldcg(g.ag) : 1.f) * (g.wg ? __ldcg(g.wg + tl.e) : 1.f);
       // gate/up: gate columns 64 ch.. and up columns 128 + 64 ch..; down: 128 ch..
       const uint32_t col0 = tl.gu ? 64 * ch : 128 * ch;
       const uint32_t col1 = tl.gu ? 128 + 64 * ch : 128 * ch + 64;
@@ -714,7 +714,9 @@ cudaError_t launch_grouped_gemm_fp4(const uint8_t* aq, const uint8_t* as, const 
   return launch_format<kDown>(format, maps, a, max_blocks(E, rl) * a.g[1].nt, sm_count, s);
 }
 
-size_t gemm_fp4_sync_ints(int E, RowLayout rl) { return 1 + static_cast<size_t>(max_blocks(E, rl)); }
+size_t gemm_fp4_sync_ints(int E, RowLayout rl, int64_t routes) {
+  return 1 + static_cast<size_t>(std::min<long long>(max_blocks(E, rl), routes / kBM + std::min<int64_t>(E, routes)));
+}
 
 bool gemm_fp4_prefer_one_launch(int E, RowLayout rl, int I, long long mean_rows, int sm_count) {
   // Whole layers, one launch against two (us): one token of 256 experts 69 / 73,

@@ -604,7 +604,7 @@ RowLayout layer_rows(int E, int R, int64_t rows) {
 size_t moe_layer_fp4_workspace_size(int T, int K, int E, int R, int64_t rows) {
   if (T < 0 || K < 1 || K > 32 || !valid_experts(E, R) || (rows != 0 && !valid_rows(rows))) return 0;
   return moe_dispatch_workspace_size(T, K, E) +
-         align_up(gemm_fp4_sync_ints(E, layer_rows(E, R, rows)) * sizeof(int), 256);
+         align_up(gemm_fp4_sync_ints(E, layer_rows(E, R, rows), static_cast<int64_t>(T) * K) * sizeof(int), 256);
 }
 
 moe_status moe_layer_fp4(const void* x, const void* topk_idx, int idx_bits, const float* topk_w,
@@ -653,7 +653,7 @@ moe_status moe_layer_fp4(const void* x, const void* topk_idx, int idx_bits, cons
   cudaError_t err = launch_dispatch_quant_fp4(
       x, topk_idx, idx_bits, T, H, K, E, rl, format, x_gscale, xq, xs, counts, src_map, dev_status,
       static_cast<int32_t*>(workspace), dev->sm_count, s, sync,
-      one ? static_cast<int>(gemm_fp4_sync_ints(E, rl)) : 0);
+      one ? static_cast<int>(gemm_fp4_sync_ints(E, rl, static_cast<int64_t>(T) * K)) : 0);
   if (err != cudaSuccess || T == 0) return from_cuda(err);
   if (one) {
     err = launch_gemm_both_fp4(xq, xs, x_gscale, counts, E, rl, H, I, w13, w13_scale, w13_gscale, w2,
