@@ -2,10 +2,15 @@
 its worked values, and bad arguments, refused on the host before a device is
 asked for."""
 import ctypes
+import os
+import re
 
 import numpy as np
+import pytest
+import torch
 
 import oracle as O
+from token_dispatch_grouped_topk_gb300 import api, build
 from test_front_abi import FAKE, MIS, _call
 
 MIS2 = ctypes.c_void_p(4096 + 2)
@@ -96,3 +101,31 @@ def test_layer_rejects_on_host(lib):
     assert _call(lib.moe_layer_fp4, d, ws=None) == -3
     assert _call(lib.moe_layer_fp4, d, ws=MIS2) == -3
     assert _call(lib.moe_layer_fp4, d, ws_bytes=size(112, 2, 8, 128, 0) - 1) == -3
+
+
+def test_what_the_chain_writes_is_read_through_l2():
+    """Counts, scales of rows and scales over tensors are written by the launches
+    before, which may still run when the products start: no read-only loads."""
+    with open(os.path.join(build.PKG_DIR, "csrc", "gemm_fp4.cu")) as f:
+        src = f.read()
+    assert "__ldg(" not in src and "ld.global.nc" not in src and "ld_stream" not in src
+    kernel = src[src.index("grouped_fp4_kernel("):]
+    assert kernel.index("pdl_wait()") < kernel.index("tile_prefixes(args, ctl)")
+    with open(os.path.join(build.PKG_DIR, "csrc", "combine.cu")) as f:
+        src = f.read()
+    head = src[src.index("combine_kernel(const uint4* out"):]
+    params = head[:head.index("{")]
+    assert not re.search(r"(out|src_map)\b[^,]*__restrict__|__restrict__ (out|src_map)", params)
+
+
+def test_binding_refuses_what_is_not_a_4_bit_lane():
+    with pytest.raises(ValueError):
+        api.moe_quantize_fp4(torch.zeros(2, 128))                 # host tensor
+    with pytest.raises(ValueError):
+        api.moe_quantize_fp4(torch.zeros(2, 128), format="int4")
+    with pytest.raises(ValueError):
+        api.MoeLayerBuffers(4, 4, 2, 256, 128, 8, torch.device("cpu"), fp4="fp4")
+    with pytest.raises(ValueError):
+        api.MoeLayerBuffers(4, 4, 2, 256, 128, 8, torch.device("cpu"), fp4="nvfp4", fp4_gscales=(None,))
+    with pytest.raises(ValueError):
+        api.MoeLayerBuffers(4, 4, 2, 256, 128, 8, torch.device("cpu"), fp4="nvfp4", source_slots=2)

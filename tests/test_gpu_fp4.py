@@ -495,10 +495,75 @@ def test_layer_from_the_residual_stream_and_from_the_host(fmt):
         assert all(torch.equal(h[3], y.cpu()) for h in host)
 
 
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("T,E,K,H,I,R,ids", [(64, 1024, 32, 128, 128, 3, torch.int32),
+                                             (3000, 4, 2, 256, 128, 2000, torch.int32),
+                                             (33, 8, 1, 1152, 384, 40, torch.int64)])
+def test_layer_bad_ids_drops_and_nan(fmt, T, E, K, H, I, R, ids):
+    """Ids outside the experts and routes past the capacity are reported and left
+    out; a NaN stays in its token; both launch forms and both layouts agree."""
+    x, idx, p, w, gs = _layer(T, E, K, H, I, T, fmt, pad=0.02)
+    idx = idx.to(ids)
+    idx[3, 0], idx[5, 0] = E, -7
+    x[7, 1] = float("nan")
+    got = []
+    for packed in (False, True):
+        lane = api.MoeLayerBuffers(T, E, K, H, I, R, torch.device(DEV), packed=packed, fp4=fmt, fp4_gscales=gs)
+        for form in ("one", "two", None):
+            lane.gemm_launch = form
+            got.append(lane.forward(x, idx, p, *w).clone())
+        rr = O.route(idx.cpu().numpy(), E, R)
+        assert lane.counts.tolist() == rr.counts.tolist()
+        status, dropped = lane.dev_status.tolist()
+        assert status == (1 | (2 if rr.dropped else 0)) and dropped == rr.dropped
+    flat = [g.view(torch.int16) for g in got]
+    assert all(torch.equal(flat[0], f) for f in flat)
+    nan = got[0].isnan().any(dim=1)
+    assert not nan[:7].any() and not nan[8:].any()
+    assert bool(nan[7]) == bool((lane.src_map[7] >= 0).any())
+
+
+def test_tokens_without_a_route_and_no_tokens():
+    T, E, K, H, I = 20, 4, 2, 256, 128
+    x, idx, p, w, gs = _layer(T, E, K, H, I, 1, "nvfp4")
+    lane = api.MoeLayerBuffers(T, E, K, H, I, T, torch.device(DEV), fp4="nvfp4", fp4_gscales=gs)
+    y = lane.forward(x, torch.full_like(idx, -1), p, *w)
+    assert not y.any() and lane.dev_status.tolist() == [0, 0] and not lane.counts.any()
+    none = api.MoeLayerBuffers(0, E, K, H, I, 4, torch.device(DEV), fp4="nvfp4", fp4_gscales=gs)
+    none.counts.fill_(3)
+    assert none.forward(x[:0], idx[:0], p[:0], *w).shape == (0, H) and not none.counts.any()
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_scale_types_and_side_streams(fmt):
+    """Scales as the 8-bit types that they are, and calls on a stream of their own
+    whose outputs are allocated by the call."""
+    E, R, H, I = 3, 50, 512, 256
+    t8 = torch.float8_e4m3fn if fmt == "nvfp4" else torch.float8_e8m0fnu
+    x = _randn(_gen(3), E, R, H)
+    w, s, wg = weights(E, 2 * I, H, 4, fmt)
+    n = torch.full((E,), R, dtype=torch.int32, device=DEV)
+    xq, xs = api.moe_quantize_fp4(x, format=fmt)
+    want = api.moe_grouped_gemm_fp4(xq, xs, n, w, s, format=fmt, w_gscale=wg)
+    z = api.moe_gemm_gateup_fp4(xq, xs, n, w, s, format=fmt, w13_gscale=wg)
+    assert torch.equal(api.moe_dequantize_fp4(xq, xs.view(t8), format=fmt),
+                       api.moe_dequantize_fp4(xq, xs, format=fmt))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        q, sc = api.moe_quantize_fp4(x, format=fmt, stream=side)
+        out = api.moe_grouped_gemm_fp4(q, sc.view(t8), n, w, s.view(t8), format=fmt, w_gscale=wg, stream=side)
+        zq, zs = api.moe_gemm_gateup_fp4(q, sc, n, w, s, format=fmt, w13_gscale=wg, stream=side, max_ctas=1)
+        del q, sc
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(out, want) and torch.equal(zq, z[0]) and torch.equal(zs, z[1])
+
+
 def test_two_halves_and_two_streams_at_once():
     T, E, K, H, I, R = 600, 16, 4, 512, 256, 300
     x, idx, p, w, gs = _layer(T, E, K, H, I, 11, "nvfp4")
-    two = api.TwoBatchOverlap(T, E, K, H, I, R, torch.device(DEV), fp4="nvfp4", fp4_gscales=gs)
+    two = api.TwoBatchOverlap(T, E, K, H, I, R, torch.device(DEV), gemm_ctas=100, fp4="nvfp4",
+                              fp4_gscales=gs)
     a = two.forward(x, idx, p, *w, overlap=False).clone()
     torch.cuda.synchronize()
     for _ in range(5):

@@ -3,13 +3,15 @@
 //
 //   P[m, n] = ga * gw[e] * sum_k (sa[m, k/B] a[m, k]) * (sw[n, k/B] w[e, n, k])
 // with e2m1 codes a, w, the block scales of the format (fp4.cuh) and the fp32
-// scales over the tensors.  Two launches use it:
+// scales over the tensors:
 //   down     out = bf16(P), any contraction K and output width N;
 //   gate/up  Z = SiLU(G) * U with G and U the products with the first and the
 //            last I rows of W13, fp32, requantised to 4 bits per block
 //            ("SGLang Expert Compute Backend", §1.1 and §3.6, on other codes).
 // Each expert's valid rows are tiled on their own (§2.4); only tiles that hold
-// valid rows are scheduled, and only valid rows are stored.
+// valid rows are scheduled, and only valid rows are stored.  A launch computes
+// one product or, for few tiles, both ("XTuner Domino EP", HyperParallel-MoE
+// section: a task starts when the tiles it needs are done).
 //
 // Design (one CTA per SM, persistent):
 //  - tiles of 128 rows x 256 columns (gate/up: 128 gate and 128 up rows of W13),
@@ -26,11 +28,26 @@
 //    weights' (kept as they come) nor the activations', whose rows are ragged;
 //  - warp 1 issues, per stage, the copies of the scales to TMEM and four MMAs
 //    (M = 128, N = 256, K = 64).  Copies and MMAs of one thread run in order, so
-//    one set of scale columns is enough;
+//    one set of scale columns is enough.  Both issuing warps run converged up to
+//    elect_one: behind a lane test each of the 16 instructions of a stage took 50
+//    to 70 clocks, against 128 of an MMA (16384 tokens, 256 experts of 7168 x
+//    2048: gate/up 2083 -> 1633 us with this alone);
 //  - warps 8-15 take the accumulator to registers (64 gate and 64 up columns, or
 //    128 columns of a row each), hand it back at once, and finish the tile while
 //    the next one's products run.  A Z block lies in one thread, so its scale
 //    needs no exchange.
+//  - a launch of both lists all gate/up tiles, then all down tiles, and takes them
+//    in that order by a ticket.  Each epilogue warp counts its part of a block's Z
+//    (release); the producer passes a down tile on once its block's count is full
+//    (acquire), through a ring that the other warps take tiles from.
+//
+// What bounds it.  Many rows: what an SM can take in, 64 bytes a clock: 48 KB of
+// codes and 6 KB of scales a stage are 850 clocks, the four MMAs 512 and the
+// twelve copies about 120.  16384 tokens (above): gate/up 1540 us, 5.0 PFLOP/s, down
+// 990 us, 3.9; without the scale loads 1410 and 870, without code loads 1210 and
+// 720.  Few rows: weights, 256 tokens to 64 experts of 4096 x 1536 (both products)
+// 113 us, 6.2 TB/s of DRAM.  One token, 8 experts of 7168 x 2048: 47 us for 29 of
+// weights; the rest is two products' first loads and last tiles.
 // Every wait is bounded; on expiry the kernel raises MOE_DEV_TIMEOUT in the
 // status word, drains its own copies and MMAs, frees TMEM and returns.
 #include <algorithm>

@@ -5,7 +5,9 @@
 // 8 bytes a lane, 256 a warp, and scales as one 32-bit word per four (eight)
 // lanes.  The codes and scales are linear over the whole matrix (H is a
 // multiple of 128), so a lane's place follows from its chunk's number alone and
-// only the scale over the tensor depends on the row.
+// only the scale over the tensor depends on the row.  Bound by HBM: 235 M fp32
+// weights to 4 bits 155 us (6.9 TB/s), back to BF16 106 us (5.7 TB/s, most of it
+// writes); a few rows take the launch, 3.5 to 4.5 us.
 #include <algorithm>
 
 #include "fp4.cuh"
