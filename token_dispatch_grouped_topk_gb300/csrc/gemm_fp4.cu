@@ -87,8 +87,8 @@ constexpr uint32_t kSfaCol = 256, kSfbCol = 272;   // scale columns behind the a
 constexpr int kGateUp = 0;
 constexpr int kDown = 1;
 constexpr int kBoth = 2;
-// A launch of both takes tiles by a ticket and passes them to its warps through
-// a ring of this many slots.
+// The producer finds each tile and passes it to the other warps through a ring of
+// this many slots.
 constexpr int kTileSlots = 8;
 
 struct Product {
@@ -119,6 +119,12 @@ struct Fp4Maps {
   CUtensorMap b[2];
 };
 
+struct Tile {
+  int gu;   // a gate/up tile
+  int blk, e, n_blk, rows, cols, base;
+  int nkb;  // stages; 0: no tile, the list has ended
+};
+
 struct alignas(16) Control {
   uint64_t full[kStages];
   uint64_t empty[kStages];
@@ -129,8 +135,10 @@ struct alignas(16) Control {
   uint64_t tile_empty[kTileSlots];
   uint32_t tmem_base;
   int abort;
-  int tile_slot[kTileSlots];
-  int blk_start[kMaxExperts + 1];
+  Tile tiles[kTileSlots];
+  int part[3][kThreads / 32];
+  int light[kMaxExperts + 1];   // prefix of the experts with one row block
+  int heavy[kMaxExperts + 1];   // prefix of the row blocks of those with more
   int cnt[kMaxExperts + 1];   // prefix of the clamped counts
 };
 
@@ -148,25 +156,42 @@ struct Layout {
   static_assert(kStageBytes % 1024 == 0 && kSmem <= 232448, "shared memory of a block");
 };
 
-struct Tile {
-  int gu;   // a gate/up tile
-  int blk, e, n_blk, rows, cols, base;
-  int nkb;  // stages
-};
+__device__ __forceinline__ int row_blocks(const Control* ctl, const Fp4Args& a) {
+  return ctl->light[a.E] + ctl->heavy[a.E];
+}
 
 // Tile t: the N slices of one 128-row block adjacent; a launch of both lists all
 // gate/up tiles before all down tiles.
+// Experts of one block bring their weights from DRAM, those of more mostly reuse
+// them in L2: each on its own is bound by DRAM or by the SMs' intake.  So the two
+// kinds are mixed evenly over the list, each in expert order (4096 tokens to 128
+// skewed experts of 4096 x 1536, gate/up 243 -> 210 us, down 155 -> 128 us).
 template <int kMode>
 __device__ __forceinline__ Tile decode_tile(const Control* ctl, const Fp4Args& a, int t) {
   Tile r;
-  const int gu_tiles = kMode == kBoth ? ctl->blk_start[a.E] * a.g[0].nt : 0;
+  const unsigned n_light = ctl->light[a.E], blocks = row_blocks(ctl, a);
+  const int gu_tiles = kMode == kBoth ? static_cast<int>(blocks) * a.g[0].nt : 0;
   r.gu = kMode == kGateUp || (kMode == kBoth && t < gu_tiles);
   const Product& g = a.g[r.gu ? 0 : 1];
   const int local = r.gu ? t : t - gu_tiles;
   r.blk = local / g.nt;
   r.n_blk = local - r.blk * g.nt;
-  r.e = find_expert(ctl->blk_start, a.E, r.blk);
-  const int m0 = (r.blk - ctl->blk_start[r.e]) * kBM;
+  // light ones before this block, in 32 bits (more than 2^21 blocks go unmixed)
+  const unsigned p = r.blk;
+  unsigned lights = min(p, n_light);
+  bool is_light = p < n_light;
+  if (n_light > 0 && n_light < blocks && blocks <= (1u << 21)) {
+    lights = p * n_light / blocks;
+    is_light = p * n_light - lights * blocks + n_light >= blocks;   // the next block has one more
+  }
+  int m_blk = 0;
+  if (is_light) {
+    r.e = find_expert(ctl->light, a.E, lights);
+  } else {
+    r.e = find_expert(ctl->heavy, a.E, p - lights);
+    m_blk = p - lights - ctl->heavy[r.e];
+  }
+  const int m0 = m_blk * kBM;
   const int count = ctl->cnt[r.e + 1] - ctl->cnt[r.e];
   r.base = (a.packed ? ctl->cnt[r.e] : r.e * a.R) + m0;
   // packed rows past the buffer, which only wrong counts claim, are no rows
@@ -181,20 +206,14 @@ __device__ __forceinline__ int weight_row(const Fp4Args& a, const Tile& t, int h
   return t.gu ? (2 * t.e + h) * a.g[0].N + t.n_blk * 128 : t.e * a.g[1].N + t.n_blk * kBN + h * 128;
 }
 
-// A warp's tile number `it`: its number in the list, -1 behind the last, -2 if a
-// wait ran out.
-template <int kMode>
-__device__ __forceinline__ int claim_tile(Control* ctl, int it, int total, int lane) {
-  if (kMode != kBoth) {
-    const int t = blockIdx.x + it * gridDim.x;
-    return t < total ? t : -1;
-  }
+// A warp's tile number `it` from the ring; false if the wait ran out.
+__device__ __forceinline__ bool claim_tile(Control* ctl, int it, int lane, Tile* tl) {
   const int slot = it % kTileSlots;
-  if (!warp_wait(&ctl->tile_full[slot], (it / kTileSlots) & 1, &ctl->abort)) return -2;
-  const int t = ctl->tile_slot[slot];
+  if (!warp_wait(&ctl->tile_full[slot], (it / kTileSlots) & 1, &ctl->abort)) return false;
+  *tl = ctl->tiles[slot];
   __syncwarp();
   if (lane == 0) mbar_arrive(&ctl->tile_empty[slot]);
-  return t;
+  return true;
 }
 
 // Z is written by ordinary stores and read by TMA, in a launch of both by
@@ -211,33 +230,51 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   mbar_wait(bar, parity, &dummy);
 }
 
-// First 128-row block of each expert, and the prefix of the clamped counts; every thread of the block calls it.  The counts may be the
-// launch before's, still written while this one starts: they are read through
-// L2, after the wait, by all threads at once (one round trip).
+// The prefixes over the experts of the clamped counts, of the experts with one
+// 128-row block and of the others' blocks; every thread of the block calls it.
+// The counts may be the launch before's, still written while this one starts:
+// they are read through L2, after the wait, by all threads at once (one round
+// trip); a thread adds up two experts, a warp 64.
 __device__ __forceinline__ void tile_prefixes(const Fp4Args& a, Control* ctl) {
-  for (int e = threadIdx.x; e < a.E; e += kThreads)
-    ctl->cnt[e + 1] = max(0, min(__ldcg(a.counts + e), a.R));
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int blocks = 0, rows = 0;
-    if (lane == 0) ctl->blk_start[0] = ctl->cnt[0] = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int c = e < a.E ? ctl->cnt[e + 1] : 0;
-      int nb = (c + kBM - 1) / kBM, nr = c;
+  static_assert(2 * kThreads >= kMaxExperts, "two experts a thread");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e = 2 * threadIdx.x;
+  // of the first expert, of both, and with the threads before
+  int one[3], own[3], sum[3];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, nb, o), v = __shfl_up_sync(0xffffffffu, nr, o);
-        if (lane >= o) nb += u, nr += v;
-      }
-      if (e < a.E) {
-        ctl->blk_start[e + 1] = blocks + nb;
-        ctl->cnt[e + 1] = rows + nr;
-      }
-      blocks += __shfl_sync(0xffffffffu, nb, 31);
-      rows += __shfl_sync(0xffffffffu, nr, 31);
+  for (int x = 0; x < 2; ++x) {
+    const int c = e + x < a.E ? max(0, min(__ldcg(a.counts + e + x), a.R)) : 0;
+    const int nb = (c + kBM - 1) / kBM;
+    const int v[3] = {nb == 1 ? 1 : 0, nb > 1 ? nb : 0, c};
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      if (x == 0) one[i] = own[i] = v[i];
+      else own[i] += v[i];
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 3; ++i) sum[i] = own[i];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int u = __shfl_up_sync(0xffffffffu, sum[i], o);
+      if (lane >= o) sum[i] += u;
+    }
+  }
+  if (lane == 31) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) ctl->part[i][warp] = sum[i];
+  }
+  __syncthreads();
+  int* const to[3] = {ctl->light, ctl->heavy, ctl->cnt};
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    int before = sum[i] - own[i];
+    for (int w = 0; w < min(warp, (a.E + 63) / 64); ++w) before += ctl->part[i][w];
+    if (e <= a.E) to[i][e] = before;
+    if (e + 1 <= a.E) to[i][e + 1] = before + one[i];
+    if (e + 2 == a.E) to[i][e + 2] = before + own[i];
   }
   __syncthreads();
 }
@@ -276,17 +313,17 @@ __device__ __forceinline__ void load_scales(const uint8_t* row, int off, int pit
 // Pairs, not more: a parity tells a slot's current use only from the one before,
 // and of the stages between a warp's own, which the other warp waits for, there
 // may be kStages - 1.
-template <int kFmt, int kMode>
+template <int kFmt>
 __device__ __forceinline__ bool lay_out_scales(const Fp4Args& args, Control* ctl, uint8_t* smem,
-                                               int sw, int par, int total, int lane) {
+                                               int sw, int par, int lane) {
   using L = Layout<kFmt>;
   static_assert(kStages >= 3, "a pair of stages may lie between a warp's own");
   const int i = lane >> 1, h = lane & 1;
   int pairs = 0, stages = 0;   // of the tiles before
   for (int it = 0;; ++it) {
-    const int t = claim_tile<kMode>(ctl, it, total, lane);
-    if (t < 0) return t == -1;
-    const Tile tl = decode_tile<kMode>(ctl, args, t);
+    Tile tl;
+    if (!claim_tile(ctl, it, lane, &tl)) return false;
+    if (tl.nkb == 0) return true;
     const Product& g = args.g[tl.gu ? 0 : 1];
     const int pitch = g.K / kFp4Block<kFmt>;
     // rows past the tile's (and columns past N) repeat one: their products are
@@ -357,8 +394,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     ctl->abort = 0;
     fence_barrier_init();
   }
-  if (warp == 0 && lane < 8 && (kMode == kBoth || (lane >> 2) == kMode))
-    tma_prefetch_desc((lane & 3) < 3 ? &maps.a[lane >> 2][lane & 3] : &maps.b[lane >> 2]);
+  // the maps that every launch has: the smallest boxes of rows, the weights
+  if (warp == 0 && lane < 4 && (kMode == kBoth || (lane >> 1) == kMode))
+    tma_prefetch_desc(lane & 1 ? &maps.b[lane >> 1] : &maps.a[lane >> 1][2]);
   if (warp == 2) {
     tmem_alloc(&ctl->tmem_base, kTmemCols);
     tmem_relinquish();
@@ -368,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tile_prefixes(args, ctl);   // its barrier also publishes the mbarriers and the TMEM address
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
-  const int total = ctl->blk_start[args.E] * ((kMode == kDown ? 0 : args.g[0].nt) +
+  const int total = row_blocks(ctl, args) * ((kMode == kDown ? 0 : args.g[0].nt) +
                                               (kMode == kGateUp ? 0 : args.g[1].nt));
   volatile int* abort_flag = &ctl->abort;
 
@@ -377,40 +415,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     warpgroup_reg_dealloc<kCtrlRegs>();
     int issued = 0;
     bool ok = true;
-    for (int it = 0; ok; ++it) {
+    // Finds tile `it` and passes it on; false if a wait ran out.
+    auto pass_on = [&](int it, Tile* tl) {
+      const int slot = it % kTileSlots;
+      if (!warp_wait(&ctl->tile_empty[slot], ((it / kTileSlots) & 1) ^ 1, abort_flag)) return false;
       int t = blockIdx.x + it * gridDim.x;
       if (kMode == kBoth) {
         // Tiles are taken in list order by whichever blocks run, so the gate/up
         // tiles that a down tile waits for are held by running blocks, which
         // wait on nothing before them.
-        const int slot = it % kTileSlots;
-        if (!warp_wait(&ctl->tile_empty[slot], ((it / kTileSlots) & 1) ^ 1, abort_flag)) {
-          ok = false;
-          break;
-        }
         if (lane == 0) t = atomicAdd(args.sched, 1);
         t = __shfl_sync(0xffffffffu, t, 0);
       }
-      if (t >= total) t = -1;
-      Tile tl{};
-      if (t >= 0) tl = decode_tile<kMode>(ctl, args, t);
-      if (kMode == kBoth) {
-        // A down tile is passed on once its block's Z is written: who takes it
-        // from the ring is then behind Z's stores.
-        if (t >= 0 && !tl.gu) {
-          if (!__all_sync(0xffffffffu, wait_count(args.sched + 1 + tl.blk, kEpiWarps * args.g[0].nt, abort_flag))) {
-            ok = false;
-            break;
-          }
-          fence_proxy_async_global();
-        }
+      *tl = Tile{};
+      if (t < total) *tl = decode_tile<kMode>(ctl, args, t);
+      // A down tile is passed on once its block's Z is written: who takes it from
+      // the ring is then behind Z's stores.
+      if (kMode == kBoth && t < total && !tl->gu) {
+        if (!__all_sync(0xffffffffu, wait_count(args.sched + 1 + tl->blk, kEpiWarps * args.g[0].nt, abort_flag)))
+          return false;
+        fence_proxy_async_global();
         __syncwarp();
-        if (lane == 0) {
-          ctl->tile_slot[it % kTileSlots] = t;
-          mbar_arrive(&ctl->tile_full[it % kTileSlots]);
-        }
       }
-      if (t < 0) break;
+      if (lane == 0) {
+        ctl->tiles[slot] = *tl;
+        mbar_arrive(&ctl->tile_full[slot]);
+      }
+      return true;
+    };
+    // Tiles of a fixed order are passed on one ahead, so that the scale warps need
+    // not wait for a tile's last loads to begin the next; a ticket is taken when
+    // its tile is due.
+    Tile nx{};
+    if (kMode != kBoth) ok = pass_on(0, &nx);
+    for (int it = 0; ok; ++it) {
+      Tile tl = nx;
+      if (kMode == kBoth) ok = pass_on(it, &tl);
+      if (!ok || tl.nkb == 0) break;
       const int g = tl.gu ? 0 : 1;
       const int b0 = weight_row(args, tl, 0), b1 = weight_row(args, tl, 1);
       // only the valid rows are fetched (32, 64 or 128): the rest of the A
@@ -436,6 +477,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ++issued;
+        if (kMode != kBoth && kb == 0 && !pass_on(it + 1, &nx)) {
+          ok = false;
+          break;
+        }
       }
     }
     if (!ok) *abort_flag = 1;
@@ -453,12 +498,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int consumed = 0;
     bool ok = true;
     for (int it = 0; ok; ++it) {
-      const int t = claim_tile<kMode>(ctl, it, total, lane);
-      if (t < 0) {
-        ok = t == -1;
-        break;
-      }
-      const Tile tl = decode_tile<kMode>(ctl, args, t);
+      Tile tl;
+      ok = claim_tile(ctl, it, lane, &tl);
+      if (!ok || tl.nkb == 0) break;
       const bool half_end = args.g[tl.gu ? 0 : 1].K % kBK != 0;   // the last stage holds 128 elements
       if (!warp_wait(&ctl->tempty, (it & 1) ^ 1, abort_flag)) {
         ok = false;
@@ -508,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------- scales
     warpgroup_reg_dealloc<kCtrlRegs>();
     const int sw = warp - kScaleWarp0;
-    if (!lay_out_scales<kFmt, kMode>(args, ctl, smem, sw % 3, sw / 3, total, lane) && lane == 0)
+    if (!lay_out_scales<kFmt>(args, ctl, smem, sw % 3, sw / 3, lane) && lane == 0)
       *abort_flag = 1;
   } else {
     // ------------------------------------------------------------ epilogue
@@ -522,12 +564,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float six_zg = __fmul_rn(6.f, zg);
     bool ok = true;
     for (int it = 0;; ++it) {
-      const int t = claim_tile<kMode>(ctl, it, total, lane);
-      if (t < 0) {
-        ok = t == -1;
-        break;
-      }
-      const Tile tl = decode_tile<kMode>(ctl, args, t);
+      Tile tl;
+      ok = claim_tile(ctl, it, lane, &tl);
+      if (!ok || tl.nkb == 0) break;
       const Product& g = args.g[tl.gu ? 0 : 1];
       const float alpha = (g.ag ? __ldcg(g.ag) : 1.f) * (g.wg ? __ldcg(g.wg + tl.e) : 1.f);
       // gate/up: gate columns 64 ch.. and up columns 128 + 64 ch..; down: 128 ch..
@@ -643,10 +682,12 @@ long long max_blocks(int E, RowLayout rl) {
   return rl.packed ? std::min<long long>(padded, rl.rows / kBM + std::min<long long>(E, rl.rows)) : padded;
 }
 
-cudaError_t product_maps(Fp4Maps* m, int g, const uint8_t* a, uint64_t rows, const uint8_t* w,
+// R: no tile has more rows than that, so the larger boxes may go unused.
+cudaError_t product_maps(Fp4Maps* m, int g, const uint8_t* a, uint64_t rows, int R, const uint8_t* w,
                          uint64_t w_rows, int K) {
-  cudaError_t err = cudaSuccess;
-  for (int i = 0; i < 3 && err == cudaSuccess; ++i) err = make_map(&m->a[g][i], a, K / 2, rows, kBM >> i);
+  cudaError_t err = make_map(&m->a[g][2], a, K / 2, rows, 32);
+  if (err == cudaSuccess && R > 32) err = make_map(&m->a[g][1], a, K / 2, rows, 64);
+  if (err == cudaSuccess && R > 64) err = make_map(&m->a[g][0], a, K / 2, rows, kBM);
   if (err == cudaSuccess) err = make_map(&m->b[g], w, K / 2, w_rows, 128);
   return err;
 }
@@ -708,7 +749,7 @@ cudaError_t launch_gemm_gateup_fp4(const uint8_t* xq, const uint8_t* xs, const f
                                    const float* zg, int format, uint8_t* zq, uint8_t* zs,
                                    int32_t* dev_status, int sm_count, cudaStream_t s) {
   Fp4Maps maps{};
-  cudaError_t err = product_maps(&maps, 0, xq, rl.rows, w13, static_cast<uint64_t>(E) * 2 * I, H);
+  cudaError_t err = product_maps(&maps, 0, xq, rl.rows, rl.R, w13, static_cast<uint64_t>(E) * 2 * I, H);
   if (err != cudaSuccess) return err;
   Fp4Args a = common_args(counts, E, rl, dev_status);
   a.g[0] = Product{xs, s13, xg, g13, H, I, I / 128};
@@ -723,7 +764,7 @@ cudaError_t launch_grouped_gemm_fp4(const uint8_t* aq, const uint8_t* as, const 
                                     const uint8_t* w, const uint8_t* ws, const float* wg, int format,
                                     void* out, int32_t* dev_status, int sm_count, cudaStream_t s) {
   Fp4Maps maps{};
-  cudaError_t err = product_maps(&maps, 1, aq, rl.rows, w, static_cast<uint64_t>(E) * N, K);
+  cudaError_t err = product_maps(&maps, 1, aq, rl.rows, rl.R, w, static_cast<uint64_t>(E) * N, K);
   if (err != cudaSuccess) return err;
   Fp4Args a = common_args(counts, E, rl, dev_status);
   a.g[1] = Product{as, ws, ag, wg, K, N, (N + kBN - 1) / kBN};
@@ -752,9 +793,9 @@ cudaError_t launch_gemm_both_fp4(const uint8_t* xq, const uint8_t* xs, const flo
                                  const float* zg, int format, uint8_t* zq, uint8_t* zs, void* out,
                                  int* sync, int32_t* dev_status, int sm_count, cudaStream_t s) {
   Fp4Maps maps{};
-  cudaError_t err = product_maps(&maps, 0, xq, rl.rows, w13, static_cast<uint64_t>(E) * 2 * I, H);
+  cudaError_t err = product_maps(&maps, 0, xq, rl.rows, rl.R, w13, static_cast<uint64_t>(E) * 2 * I, H);
   if (err == cudaSuccess)
-    err = product_maps(&maps, 1, zq, rl.rows, w2, static_cast<uint64_t>(E) * H, I);
+    err = product_maps(&maps, 1, zq, rl.rows, rl.R, w2, static_cast<uint64_t>(E) * H, I);
   if (err != cudaSuccess) return err;
   Fp4Args a = common_args(counts, E, rl, dev_status);
   a.g[0] = Product{xs, s13, xg, g13, H, I, I / 128};
