@@ -413,7 +413,7 @@ def _check(t, dtypes, shape, dev, name):
 def _stream_on(stream, dev):
     """The raw stream of a call on device ``dev``, which has to be the current
     device (where the library launches)."""
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"the inputs are on cuda:{dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
@@ -612,14 +612,16 @@ def _gscale(g, n, dev, name):
     return None if g is None else _check(g, _F32, (n,), dev, name)
 
 
-def _gscale_rows(gscale, t, rows, dev):
+def _gscale_rows(gscale, shape, rows, dev):
     """(address of the scales over the tensor, rows of each) for the ``rows``
-    rows of ``t``: one scale over all of them, or one per leading index of a
-    three-dimensional ``t``."""
+    rows of a tensor ``shape``: one scale over all of them, or one per leading
+    index of a three-dimensional one."""
     if gscale is None:
         return None, rows or 1
-    n = t.shape[0] if t.dim() >= 3 and gscale.numel() != 1 else 1
-    return _check(gscale, _F32, (n,), dev, "gscale"), (rows // n if n else rows) or 1
+    if len(shape) < 3 or gscale.numel() == 1:
+        return _check(gscale, _F32, (1,), dev, "gscale"), rows or 1
+    n = shape[0]
+    return _check(gscale, _F32, (n,), dev, "gscale"), (rows // n if n else 0) or 1
 
 
 def moe_quantize_fp4(x, *, format: str = "nvfp4", gscale=None, xq=None, xs=None, stream=None):
@@ -629,22 +631,22 @@ def moe_quantize_fp4(x, *, format: str = "nvfp4", gscale=None, xq=None, xs=None,
     32, power-of-two scales, no ``gscale``).  Returns ``(xq [..., H/2], xs [...,
     H/16 or H/32])`` uint8."""
     fmt, block = _fp4(format)
-    shape = x.shape
-    H = shape[-1]
-    lead = shape[:-1]
-    q_shape, s_shape = (*lead, H // 2), (*lead, H // block)
+    shape = tuple(x.shape)
+    lead, H = shape[:-1], shape[-1]
+    q_shape, s_shape = lead + (H // 2,), lead + (H // block,)
     dev = x.get_device()
     px = _check(x, _HALF_OR_F32, shape, dev, "x")
     rows = x.numel() // H if H else 0
-    pg, per = _gscale_rows(gscale, x, rows, dev)
+    pg, per = _gscale_rows(gscale, shape, rows, dev)
     if xq is None:
         xq = _new(q_shape, torch.uint8, x.device, stream)
     if xs is None:
         xs = _new(s_shape, torch.uint8, x.device, stream)
     st = _lib.load().moe_quantize_fp4(
-        px, _bits(x), pg, per, rows, H, fmt, _check(xq, _U8, q_shape, dev, "xq"),
+        px, 8 * x.element_size(), pg, per, rows, H, fmt, _check(xq, _U8, q_shape, dev, "xq"),
         _check(xs, _FP4_SCALES[format], s_shape, dev, "xs"), _stream_on(stream, dev))
-    _lib.check("moe_quantize_fp4", st)
+    if st:
+        _lib.check("moe_quantize_fp4", st)
     return xq, xs
 
 
@@ -653,20 +655,20 @@ def moe_dequantize_fp4(xq, xs, *, format: str = "nvfp4", gscale=None, dtype=torc
     """The values of ``moe_quantize_fp4``'s codes and scales (moe_dequantize_fp4):
     ``out [..., H]`` in ``dtype``, bf16 or fp32."""
     fmt, block = _fp4(format)
-    shape = xq.shape
-    H = 2 * shape[-1]
-    lead = shape[:-1]
-    o_shape = (*lead, H)
+    shape = tuple(xq.shape)
+    lead, H = shape[:-1], 2 * shape[-1]
+    o_shape = lead + (H,)
     dev = xq.get_device()
     pq = _check(xq, _U8, shape, dev, "xq")
     rows = 2 * xq.numel() // H if H else 0
-    pg, per = _gscale_rows(gscale, xq, rows, dev)
+    pg, per = _gscale_rows(gscale, shape, rows, dev)
     if out is None:
         out = _new(o_shape, dtype, xq.device, stream)
     st = _lib.load().moe_dequantize_fp4(
-        pq, _check(xs, _FP4_SCALES[format], (*lead, H // block), dev, "xs"), pg, per, rows, H, fmt,
-        _check(out, _HALF_OR_F32, o_shape, dev, "out"), _bits(out), _stream_on(stream, dev))
-    _lib.check("moe_dequantize_fp4", st)
+        pq, _check(xs, _FP4_SCALES[format], lead + (H // block,), dev, "xs"), pg, per, rows, H, fmt,
+        _check(out, _HALF_OR_F32, o_shape, dev, "out"), 8 * out.element_size(), _stream_on(stream, dev))
+    if st:
+        _lib.check("moe_dequantize_fp4", st)
     return out
 
 

@@ -17,7 +17,8 @@
 //  - tiles of 128 rows x 256 columns (gate/up: 128 gate and 128 up rows of W13),
 //    one fp32 accumulator of 256 TMEM columns, N slices of one 128-row block
 //    adjacent in the walk;
-//  - warp 0 streams codes with TMA: stages of K = 256, 128 bytes a row, the
+//  - warp 0 finds the tiles, passes them to the other warps through a ring and
+//    streams their codes with TMA: stages of K = 256, 128 bytes a row, the
 //    128-byte swizzle; kStages of them in a ring;
 //  - warps 2-7 lay the scales of a stage out in shared memory as tcgen05.cp
 //    wants them.  Scales are stored [row, K / B] like the codes, 16 (8) bytes a
@@ -39,14 +40,14 @@
 //  - a launch of both lists all gate/up tiles, then all down tiles, and takes them
 //    in that order by a ticket.  Each epilogue warp counts its part of a block's Z
 //    (release); the producer passes a down tile on once its block's count is full
-//    (acquire), through a ring that the other warps take tiles from.
+//    (acquire).
 //
 // What bounds it.  Many rows: what an SM can take in, 64 bytes a clock: 48 KB of
 // codes and 6 KB of scales a stage are 850 clocks, the four MMAs 512 and the
-// twelve copies about 120.  16384 tokens (above): gate/up 1540 us, 5.0 PFLOP/s, down
-// 990 us, 3.9; without the scale loads 1410 and 870, without code loads 1210 and
+// twelve copies about 120.  16384 tokens (above): gate/up 1498 us, 4.8 PFLOP/s, down
+// 969 us, 3.7; without the scale loads 8 to 15 % less, without code loads 1210 and
 // 720.  Few rows: weights, 256 tokens to 64 experts of 4096 x 1536 (both products)
-// 113 us, 6.2 TB/s of DRAM.  One token, 8 experts of 7168 x 2048: 47 us for 29 of
+// 111 us, 6.3 TB/s of DRAM.  One token, 8 experts of 7168 x 2048: 47 us for 29 of
 // weights; the rest is two products' first loads and last tiles.
 // Every wait is bounded; on expiry the kernel raises MOE_DEV_TIMEOUT in the
 // status word, drains its own copies and MMAs, frees TMEM and returns.
