@@ -493,6 +493,14 @@ def test_layer_from_the_residual_stream_and_from_the_host(fmt):
             pipe.submit(*h, *w)
         pipe.synchronize()
         assert all(torch.equal(h[3], y.cpu()) for h in host)
+        if fmt == "nvfp4":   # other scales over the tensors: not the captured ones.
+            # Twice W2's doubles out and y, exactly.
+            lane.fp4_gscales = (*gs[:3], 2 * gs[3])
+            for h in host:
+                pipe.submit(*h, *w)
+            pipe.synchronize()
+            assert all(torch.equal(h[3], 2 * y.cpu()) for h in host)
+            lane.fp4_gscales = gs
 
 
 @pytest.mark.parametrize("fmt", FMT)
@@ -505,6 +513,7 @@ def test_layer_bad_ids_drops_and_nan(fmt, T, E, K, H, I, R, ids):
     x, idx, p, w, gs = _layer(T, E, K, H, I, T, fmt, pad=0.02)
     idx = idx.to(ids)
     idx[3, 0], idx[5, 0] = E, -7
+    idx[9] = 2                                   # every route of a token to one expert
     x[7, 1] = float("nan")
     got = []
     for packed in (False, True):

@@ -1298,7 +1298,9 @@ class HostPipeline:
         if not self.graph:
             self._forward(k, weights, cs)
             return
-        key = (k,) + tuple(t.data_ptr() for t in weights)
+        # a 4-bit lane's scales over the tensors are captured as well
+        over = [t for t in self.lane.fp4_gscales if t is not None]
+        key = (k,) + tuple(t.data_ptr() for t in (*weights, *over))
         g = self._graphs.get(key)
         if g is None:
             # this step runs eagerly; the capture records the same launches
