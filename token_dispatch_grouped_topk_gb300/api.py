@@ -1246,8 +1246,10 @@ class HostPipeline:
     With ``graph=True`` the layer of each input slot is captured once into a
     CUDA graph (on the slot's first step, which runs eagerly) and replayed on
     later steps, so a step costs one graph launch instead of the layer's
-    separate launches.  A graph is kept per slot and set of weight tensors;
-    new weight tensors are captured anew."""
+    separate launches.  A graph is kept per slot and for everything that its
+    launches hold: the weight tensors and the lane's scales over the tensors
+    (their addresses, each in its place), its launch form, W13's order and its
+    rank offsets.  A step for which any of them is another is captured anew."""
 
     def __init__(self, lane: "MoeLayerBuffers", graph: bool = False):
         self.lane = lane
@@ -1294,13 +1296,20 @@ class HostPipeline:
     def _forward(self, k, weights, stream):
         self.lane.forward(self.x[k], self.idx[k], self.w[k], *weights, stream=stream, y=self.y[k])
 
+    def _graph_key(self, k, weights):
+        """What the captured launches of slot k hold.  An operand that is not
+        there is a None in its place: the same tensor means something else as
+        the scale over x than as the scale over Z."""
+        ln = self.lane
+        at = lambda t: None if t is None else t.data_ptr()
+        return (k, *map(at, weights), *map(at, ln.fp4_gscales), at(ln.rank_offsets), ln.gemm_launch,
+                ln.w13_interleaved)
+
     def _compute(self, k, weights, cs):
         if not self.graph:
             self._forward(k, weights, cs)
             return
-        # a 4-bit lane's scales over the tensors are captured as well
-        over = [t for t in self.lane.fp4_gscales if t is not None]
-        key = (k,) + tuple(t.data_ptr() for t in (*weights, *over))
+        key = self._graph_key(k, weights)
         g = self._graphs.get(key)
         if g is None:
             # this step runs eagerly; the capture records the same launches
