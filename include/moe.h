@@ -599,7 +599,8 @@ moe_status moe_experts_w4(const void* x, const void* topk_idx, int idx_bits, con
  *   moe_grouped_gemm_fp4 with w2 [E, H, I/2] and a_gscale = z_gscale is the down
  *   product.
  *   Codes, scales and out of both products 16-byte aligned.  dev_status device
- *   int32 [2]: MOE_DEV_TIMEOUT may be ORed in.  flags: 0 or MOE_GEMM_MAX_CTAS(n).
+ *   int32 [2]: MOE_DEV_TIMEOUT may be ORed in.  flags: 0 or MOE_GEMM_MAX_CTAS(n);
+ *   a call whose n is below the number of SMs lets no later one start before it ends.
  *   Packed rows at or past `rows` are never touched, even if counts claim more.
  *
  * moe_layer_fp4         the whole branch: moe_dispatch_quant_fp4, both products

@@ -1,0 +1,51 @@
+"""MOE_GEMM_MAX_CTAS on the 4-bit products: the SMs that it leaves are free for
+other streams, also while a capped launch follows a capped launch."""
+import pytest
+import torch
+
+from token_dispatch_grouped_topk_gb300 import api
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.mark.parametrize("fmt", ("nvfp4", "mxfp4"))
+def test_another_streams_product_runs_beside_capped_ones(fmt):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n = 2 * sms // 3
+    block = api.FP4_BLOCK[fmt]
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8, device=DEV)
+    # milliseconds of gate/up on n SMs, then a down product of few tiles
+    R, H, I, N = 8192, 16384, 16384, 128
+    i32 = lambda v: torch.full((1,), v, dtype=torch.int32, device=DEV)
+    xq, xs = u8(1, R, H // 2), u8(1, R, H // block)
+    w13, s13 = u8(1, 2 * I, H // 2), u8(1, 2 * I, H // block)
+    w2, s2 = u8(1, N, I // 2), u8(1, N, I // block)
+    zq, zs, out = u8(1, R, I // 2), u8(1, R, I // block), torch.empty(1, R, N, dtype=torch.bfloat16, device=DEV)
+    st, counts = torch.zeros(2, dtype=torch.int32, device=DEV), i32(R)
+    # the other stream's product: a whole SM for each of its blocks, microseconds long
+    a, sa, wb, sb = u8(1, 128, 256), u8(1, 128, 512 // block), u8(1, 2048, 256), u8(1, 2048, 512 // block)
+    o2, few = torch.empty(1, 128, 2048, dtype=torch.bfloat16, device=DEV), i32(128)
+    st2 = torch.zeros(2, dtype=torch.int32, device=DEV)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    ev = lambda: torch.cuda.Event(enable_timing=True)
+    shares = []
+    for _ in range(4):
+        e0, e1, b1 = ev(), ev(), ev()
+        torch.cuda.synchronize()
+        e0.record(main)
+        kw = dict(format=fmt, dev_status=st, stream=main, max_ctas=n)
+        api.moe_gemm_gateup_fp4(xq, xs, counts, w13, s13, zq=zq, zs=zs, **kw)
+        api.moe_grouped_gemm_fp4(zq, zs, counts, w2, s2, out=out, **kw)
+        e1.record(main)
+        api.moe_grouped_gemm_fp4(a, sa, few, wb, sb, format=fmt, out=o2, dev_status=st2, stream=side,
+                                 max_ctas=sms - n)
+        b1.record(side)
+        torch.cuda.synchronize()
+        shares.append(e0.elapsed_time(b1) / e0.elapsed_time(e1))
+    assert st.tolist() == [0, 0] and st2.tolist() == [0, 0]
+    # the first pass loads the kernels.  Held back until gate/up ends, the other
+    # product ends after nearly all of the main stream's time.
+    assert max(shares[1:]) < 0.5, shares

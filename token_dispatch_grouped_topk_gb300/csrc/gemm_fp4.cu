@@ -111,6 +111,7 @@ struct Fp4Args {
   int* sched;           // both: [0] tile ticket, [1 + b] epilogue warps done with block b
   int E, R;
   int packed;
+  int early;            // the next launch of the chain may start beside this one
   long long rows;       // buffer rows
   int32_t* dev_status;
 };
@@ -379,7 +380,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* out_stage = smem + kStages * L::kStageBytes + sizeof(Control);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  pdl_start();
+  // Not from a capped grid: the next launch's blocks would sit down on the SMs
+  // that it leaves to other streams, and hold them until this one ends.
+  if (args.early) pdl_start();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&ctl->full[i], 1 + kScaleWarps / 2);   // a stage's scales: one of each two
@@ -731,12 +734,13 @@ cudaError_t launch_format(int format, const Fp4Maps& maps, const Fp4Args& args, 
                           : launch_impl<kMxfp4, kMode>(maps, args, max_tiles, sm_count, s);
 }
 
-Fp4Args common_args(const int32_t* counts, int E, RowLayout rl, int32_t* dev_status) {
+Fp4Args common_args(const int32_t* counts, int E, RowLayout rl, int32_t* dev_status, bool capped) {
   Fp4Args a{};
   a.counts = counts;
   a.E = E;
   a.R = rl.R;
   a.packed = rl.packed;
+  a.early = !capped;
   a.rows = rl.rows;
   a.dev_status = dev_status;
   return a;
@@ -748,11 +752,11 @@ cudaError_t launch_gemm_gateup_fp4(const uint8_t* xq, const uint8_t* xs, const f
                                    const int32_t* counts, int E, RowLayout rl, int H, int I,
                                    const uint8_t* w13, const uint8_t* s13, const float* g13,
                                    const float* zg, int format, uint8_t* zq, uint8_t* zs,
-                                   int32_t* dev_status, int sm_count, cudaStream_t s) {
+                                   int32_t* dev_status, int sm_count, bool capped, cudaStream_t s) {
   Fp4Maps maps{};
   cudaError_t err = product_maps(&maps, 0, xq, rl.rows, rl.R, w13, static_cast<uint64_t>(E) * 2 * I, H);
   if (err != cudaSuccess) return err;
-  Fp4Args a = common_args(counts, E, rl, dev_status);
+  Fp4Args a = common_args(counts, E, rl, dev_status, capped);
   a.g[0] = Product{xs, s13, xg, g13, H, I, I / 128};
   a.zg = zg;
   a.zq = zq;
@@ -763,11 +767,11 @@ cudaError_t launch_gemm_gateup_fp4(const uint8_t* xq, const uint8_t* xs, const f
 cudaError_t launch_grouped_gemm_fp4(const uint8_t* aq, const uint8_t* as, const float* ag,
                                     const int32_t* counts, int E, RowLayout rl, int K, int N,
                                     const uint8_t* w, const uint8_t* ws, const float* wg, int format,
-                                    void* out, int32_t* dev_status, int sm_count, cudaStream_t s) {
+                                    void* out, int32_t* dev_status, int sm_count, bool capped, cudaStream_t s) {
   Fp4Maps maps{};
   cudaError_t err = product_maps(&maps, 1, aq, rl.rows, rl.R, w, static_cast<uint64_t>(E) * N, K);
   if (err != cudaSuccess) return err;
-  Fp4Args a = common_args(counts, E, rl, dev_status);
+  Fp4Args a = common_args(counts, E, rl, dev_status, capped);
   a.g[1] = Product{as, ws, ag, wg, K, N, (N + kBN - 1) / kBN};
   a.out = static_cast<__nv_bfloat16*>(out);
   return launch_format<kDown>(format, maps, a, max_blocks(E, rl) * a.g[1].nt, sm_count, s);
@@ -792,13 +796,13 @@ cudaError_t launch_gemm_both_fp4(const uint8_t* xq, const uint8_t* xs, const flo
                                  const uint8_t* w13, const uint8_t* s13, const float* g13,
                                  const uint8_t* w2, const uint8_t* s2, const float* g2,
                                  const float* zg, int format, uint8_t* zq, uint8_t* zs, void* out,
-                                 int* sync, int32_t* dev_status, int sm_count, cudaStream_t s) {
+                                 int* sync, int32_t* dev_status, int sm_count, bool capped, cudaStream_t s) {
   Fp4Maps maps{};
   cudaError_t err = product_maps(&maps, 0, xq, rl.rows, rl.R, w13, static_cast<uint64_t>(E) * 2 * I, H);
   if (err == cudaSuccess)
     err = product_maps(&maps, 1, zq, rl.rows, rl.R, w2, static_cast<uint64_t>(E) * H, I);
   if (err != cudaSuccess) return err;
-  Fp4Args a = common_args(counts, E, rl, dev_status);
+  Fp4Args a = common_args(counts, E, rl, dev_status, capped);
   a.g[0] = Product{xs, s13, xg, g13, H, I, I / 128};
   a.g[1] = Product{zs, s2, zg, g2, I, H, (H + kBN - 1) / kBN};
   a.zg = zg;

@@ -198,16 +198,20 @@ cudaError_t launch_dispatch_quant_fp4(const void* x, const void* topk_idx, int i
                                       int32_t* src_map, int32_t* dev_status, int32_t* hist,
                                       int sm_count, cudaStream_t s, int* zero = nullptr,
                                       int n_zero = 0);   // zero: n_zero ints that it clears
-// rows of ragged experts times their weights; null scales over a tensor: 1
+// rows of ragged experts times their weights; null scales over a tensor: 1.
+// sm_count: the most blocks; capped: they are fewer than the SMs, so that other
+// streams' kernels find room, and no later launch starts before this one ends
 cudaError_t launch_gemm_gateup_fp4(const uint8_t* xq, const uint8_t* xs, const float* xg,
                                    const int32_t* counts, int E, RowLayout rl, int H, int I,
                                    const uint8_t* w13, const uint8_t* s13, const float* g13,
                                    const float* zg, int format, uint8_t* zq, uint8_t* zs,
-                                   int32_t* dev_status, int sm_count, cudaStream_t s);
+                                   int32_t* dev_status, int sm_count, bool capped,
+                                   cudaStream_t s);
 cudaError_t launch_grouped_gemm_fp4(const uint8_t* aq, const uint8_t* as, const float* ag,
                                     const int32_t* counts, int E, RowLayout rl, int K, int N,
                                     const uint8_t* w, const uint8_t* ws, const float* wg, int format,
-                                    void* out, int32_t* dev_status, int sm_count, cudaStream_t s);
+                                    void* out, int32_t* dev_status, int sm_count, bool capped,
+                                    cudaStream_t s);
 
 // Both products in one launch: a down tile starts as soon as its 128-row block's
 // gate/up tiles have written their Z.  sync: gemm_fp4_sync_ints ints, cleared
@@ -219,7 +223,8 @@ cudaError_t launch_gemm_both_fp4(const uint8_t* xq, const uint8_t* xs, const flo
                                  const uint8_t* w13, const uint8_t* s13, const float* g13,
                                  const uint8_t* w2, const uint8_t* s2, const float* g2,
                                  const float* zg, int format, uint8_t* zq, uint8_t* zs, void* out,
-                                 int* sync, int32_t* dev_status, int sm_count, cudaStream_t s);
+                                 int* sync, int32_t* dev_status, int sm_count, bool capped,
+                                 cudaStream_t s);
 
 // ----- layer statistics of one routing (kLayerStats 64-bit counters):
 // [0] valid routes, [1] kept routes, [2] messages (sum over tokens of the

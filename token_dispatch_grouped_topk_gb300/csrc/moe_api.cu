@@ -483,9 +483,14 @@ bool valid_fp4_rows(int64_t rows, int64_t rows_per_gscale, int H) {
          rows_per_gscale <= (int64_t{1} << 30) && valid_hidden(H);
 }
 bool valid_cta_flags(int flags) { return (flags & ~MOE_GEMM_MAX_CTAS(0x7FFF)) == 0; }
-int grid_limit(int flags, int sm_count) {
+// The most blocks of a product, and whether that leaves SMs to other streams.
+struct Grid {
+  int limit;
+  bool capped;
+};
+Grid grid_limit(int flags, int sm_count) {
   const int cap = (flags >> 16) & 0x7FFF;
-  return cap > 0 ? std::min(cap, sm_count) : sm_count;
+  return cap > 0 && cap < sm_count ? Grid{cap, true} : Grid{sm_count, false};
 }
 }  // namespace
 
@@ -566,9 +571,10 @@ moe_status moe_gemm_gateup_fp4(const uint8_t* xq, const uint8_t* xs, const float
     return MOE_ERR_INVALID_ARG;
   const DeviceInfo* dev = nullptr;
   if (moe_status st = check_device(&dev); st != MOE_OK) return st;
+  const Grid grid = grid_limit(flags, dev->sm_count);
   return from_cuda(launch_gemm_gateup_fp4(
       xq, xs, x_gscale, counts, E, rows != 0 ? RowLayout{R, 1, rows} : padded_rows(E, R), H, I, w13,
-      w13_scale, w13_gscale, z_gscale, format, zq, zs, dev_status, grid_limit(flags, dev->sm_count),
+      w13_scale, w13_gscale, z_gscale, format, zq, zs, dev_status, grid.limit, grid.capped,
       reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -589,9 +595,10 @@ moe_status moe_grouped_gemm_fp4(const uint8_t* a, const uint8_t* a_scale, const 
     return MOE_ERR_INVALID_ARG;
   const DeviceInfo* dev = nullptr;
   if (moe_status st = check_device(&dev); st != MOE_OK) return st;
+  const Grid grid = grid_limit(flags, dev->sm_count);
   return from_cuda(launch_grouped_gemm_fp4(
       a, a_scale, a_gscale, counts, E, rows != 0 ? RowLayout{R, 1, rows} : padded_rows(E, R), K, N, w,
-      w_scale, w_gscale, format, out, dev_status, grid_limit(flags, dev->sm_count),
+      w_scale, w_gscale, format, out, dev_status, grid.limit, grid.capped,
       reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -649,7 +656,7 @@ moe_status moe_layer_fp4(const void* x, const void* topk_idx, int idx_bits, cons
                    : (flags & MOE_GEMM_TWO_LAUNCHES) ? false
                                                      : gemm_fp4_prefer_one_launch(E, rl, I, static_cast<long long>(T) * K / E,
                                                                                   dev->sm_count);
-  const int grid = grid_limit(flags, dev->sm_count);
+  const Grid grid = grid_limit(flags, dev->sm_count);
   cudaError_t err = launch_dispatch_quant_fp4(
       x, topk_idx, idx_bits, T, H, K, E, rl, format, x_gscale, xq, xs, counts, src_map, dev_status,
       static_cast<int32_t*>(workspace), dev->sm_count, s, sync,
@@ -658,13 +665,13 @@ moe_status moe_layer_fp4(const void* x, const void* topk_idx, int idx_bits, cons
   if (one) {
     err = launch_gemm_both_fp4(xq, xs, x_gscale, counts, E, rl, H, I, w13, w13_scale, w13_gscale, w2,
                                w2_scale, w2_gscale, z_gscale, format, zq, zs, out, sync, dev_status,
-                               grid, s);
+                               grid.limit, grid.capped, s);
   } else {
     err = launch_gemm_gateup_fp4(xq, xs, x_gscale, counts, E, rl, H, I, w13, w13_scale, w13_gscale,
-                                 z_gscale, format, zq, zs, dev_status, grid, s);
+                                 z_gscale, format, zq, zs, dev_status, grid.limit, grid.capped, s);
     if (err == cudaSuccess)
       err = launch_grouped_gemm_fp4(zq, zs, z_gscale, counts, E, rl, I, H, w2, w2_scale, w2_gscale,
-                                    format, out, dev_status, grid, s);
+                                    format, out, dev_status, grid.limit, grid.capped, s);
   }
   if (err == cudaSuccess)
     err = launch_combine(out, src_map, topk_w, T, H, K, rl.rows, y, dev->sm_count, s, true);
