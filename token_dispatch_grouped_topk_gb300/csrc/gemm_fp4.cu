@@ -686,6 +686,12 @@ long long max_blocks(int E, RowLayout rl) {
   return rl.packed ? std::min<long long>(padded, rl.rows / kBM + std::min<long long>(E, rl.rows)) : padded;
 }
 
+// The most 128-row blocks that a layer of so many routes can have, whatever room
+// its buffers hold.
+long long layer_blocks(int E, RowLayout rl, int64_t routes) {
+  return std::min<long long>(max_blocks(E, rl), routes / kBM + std::min<int64_t>(E, routes));
+}
+
 // R: no tile has more rows than that, so the larger boxes may go unused.
 cudaError_t product_maps(Fp4Maps* m, int g, const uint8_t* a, uint64_t rows, int R, const uint8_t* w,
                          uint64_t w_rows, int K) {
@@ -778,17 +784,19 @@ cudaError_t launch_grouped_gemm_fp4(const uint8_t* aq, const uint8_t* as, const 
 }
 
 size_t gemm_fp4_sync_ints(int E, RowLayout rl, int64_t routes) {
-  return 1 + static_cast<size_t>(std::min<long long>(max_blocks(E, rl), routes / kBM + std::min<int64_t>(E, routes)));
+  return 1 + static_cast<size_t>(layer_blocks(E, rl, routes));
 }
 
-bool gemm_fp4_prefer_one_launch(int E, RowLayout rl, int I, long long mean_rows, int sm_count) {
-  // Whole layers, one launch against two (us): one token of 256 experts 69 / 73,
-  // 16 tokens 348 / 365 (14 waves of tiles at most, half a row an expert), 256
-  // tokens of 64 experts 139 / 155 (6), 512: 149 / 165 (8), 1024: 179 / 179 (10),
-  // 2048: 275 / 258 (15), 4096 of 128: 508 / 474 (30).  The one launch fills the
-  // last gate/up wave with down tiles and starts once, but every tile costs a
-  // ticket and Z a flush; where weights bound the products that is hidden.
-  return max_blocks(E, rl) * (I / 128) <= 10LL * sm_count || mean_rows <= 64;
+bool gemm_fp4_prefer_one_launch(int E, RowLayout rl, int I, int64_t routes, int sm_count) {
+  // Whole layers from call to call, one launch / two (us), by the most waves of
+  // gate/up tiles: one token of 256 experts of 7168 x 2048 58 / 62 (0.8 waves),
+  // 16000 of 16 of 2048 x 512 103 / 108 (3.7), 256 of 64 of 4096 x 1536 130 / 142
+  // (6.3), 768 160 / 165 (8.8), 1024 178 / 172 (10.1), 2048 274 / 250 (15.2), 4096
+  // skewed ones of 128 543 / 474 (30), 1000 of 1024 of 1024 x 1024 349 / 275 (56).
+  // The one launch fills the last gate/up wave with down tiles and starts once, but
+  // every tile costs a ticket and Z a flush.  Between 10 and 14 waves, where few of
+  // many experts have rows, it can still be ahead: 16 tokens of 256 experts 337 / 347.
+  return layer_blocks(E, rl, routes) * (I / 128) <= 10LL * sm_count;
 }
 
 cudaError_t launch_gemm_both_fp4(const uint8_t* xq, const uint8_t* xs, const float* xg,

@@ -217,7 +217,7 @@ cudaError_t launch_grouped_gemm_fp4(const uint8_t* aq, const uint8_t* as, const 
 // gate/up tiles have written their Z.  sync: gemm_fp4_sync_ints ints, cleared
 // before (by the dispatch); counts as that dispatch of `routes` routes left them.
 size_t gemm_fp4_sync_ints(int E, RowLayout rl, int64_t routes);
-bool gemm_fp4_prefer_one_launch(int E, RowLayout rl, int I, long long mean_rows, int sm_count);
+bool gemm_fp4_prefer_one_launch(int E, RowLayout rl, int I, int64_t routes, int sm_count);
 cudaError_t launch_gemm_both_fp4(const uint8_t* xq, const uint8_t* xs, const float* xg,
                                  const int32_t* counts, int E, RowLayout rl, int H, int I,
                                  const uint8_t* w13, const uint8_t* s13, const float* g13,

@@ -652,15 +652,15 @@ moe_status moe_layer_fp4(const void* x, const void* topk_idx, int idx_bits, cons
   const RowLayout rl = layer_rows(E, R, rows);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int* sync = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + hist_bytes);
+  const int64_t routes = static_cast<int64_t>(T) * K;
   const bool one = (flags & MOE_GEMM_ONE_LAUNCH)     ? true
                    : (flags & MOE_GEMM_TWO_LAUNCHES) ? false
-                                                     : gemm_fp4_prefer_one_launch(E, rl, I, static_cast<long long>(T) * K / E,
-                                                                                  dev->sm_count);
+                                                     : gemm_fp4_prefer_one_launch(E, rl, I, routes, dev->sm_count);
   const Grid grid = grid_limit(flags, dev->sm_count);
   cudaError_t err = launch_dispatch_quant_fp4(
       x, topk_idx, idx_bits, T, H, K, E, rl, format, x_gscale, xq, xs, counts, src_map, dev_status,
       static_cast<int32_t*>(workspace), dev->sm_count, s, sync,
-      one ? static_cast<int>(gemm_fp4_sync_ints(E, rl, static_cast<int64_t>(T) * K)) : 0);
+      one ? static_cast<int>(gemm_fp4_sync_ints(E, rl, routes)) : 0);
   if (err != cudaSuccess || T == 0) return from_cuda(err);
   if (one) {
     err = launch_gemm_both_fp4(xq, xs, x_gscale, counts, E, rl, H, I, w13, w13_scale, w13_gscale, w2,
