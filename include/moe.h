@@ -570,7 +570,8 @@ moe_status moe_experts_w4(const void* x, const void* topk_idx, int idx_bits, con
  * code, beyond 6 to 6; an e4m3 scale beyond 448 to 448.  A block whose scale
  * rounds to zero has zero codes.  A block with a NaN or an infinity gets the
  * scale NaN, and so NaN in every product with it.  g is positive and finite,
- * with amax / g and s g inside fp32's normal range.
+ * with amax / g and s g inside fp32's normal range; for a tensor (an expert) of
+ * zeros it may be 0, as amax / (6 * 448) then is: scales, codes and products are 0.
  *
  * moe_quantize_fp4      x device BF16 (x_bits = 16) or fp32 (32) [rows, H] to xq
  *   device [rows, H/2] and xs device [rows, H/16] (NVFP4) or [rows, H/32].

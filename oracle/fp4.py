@@ -35,7 +35,8 @@ def fp4_quantize(x: np.ndarray, fmt: str, g=None):
         bad = ~np.isfinite(amax)
         if fmt == "nvfp4":
             g = np.broadcast_to(np.float32(1.0) if g is None else np.asarray(g, np.float32), (x.shape[0],))[:, None]
-            t = np.where(bad, np.float32(0), amax) / (np.float32(6.0) * g)
+            some = ~bad & (amax != 0)   # a block of zeros has scale 0, whatever g is
+            t = np.where(some, amax, np.float32(0)) / np.where(some, np.float32(6.0) * g, np.float32(1))
             scale = e4m3_encode(np.minimum(t, np.float32(448.0)))
             s = e4m3_decode(scale).astype(np.float32)
             r = np.where(s > 0, np.float32(1.0) / (s * g), np.float32(0))

@@ -12,8 +12,9 @@
 // product x * (1 / (s g)) each rounded to nearest, then the code (nearest, ties
 // to even, beyond 6 to 6).  The reciprocal instead of a division per element
 // moves only values within 2^-23 of a midpoint.  A block whose scale rounds to
-// zero has zero codes.  A block with a NaN or an infinity gets the scale NaN
-// (0x7F, 0xFF), which makes every product with it NaN.
+// zero has zero codes, and so has a block of zeros, whatever g is: that of a tensor
+// of zeros, taken from its data, is 0.  A block with a NaN or an infinity gets the
+// scale NaN (0x7F, 0xFF), which makes every product with it NaN.
 #pragma once
 
 #include <cuda_fp4.h>
@@ -37,9 +38,9 @@ __device__ __forceinline__ float e4m3_to_f32(uint8_t v) {
 template <int kFmt>
 __device__ __forceinline__ uint8_t fp4_block_scale(uint32_t amax, float g, float six_g, float* mult) {
   if constexpr (kFmt == kNvfp4) {
-    if (amax >= 0x7F800000u) {
+    if (amax == 0u || amax >= 0x7F800000u) {   // not 0 / (6 g): g may be 0
       *mult = 0.f;
-      return 0x7F;
+      return amax == 0u ? 0 : 0x7F;
     }
     const uint8_t b = static_cast<uint8_t>(__nv_cvt_float_to_fp8(
         __fdiv_rn(__uint_as_float(amax), six_g), __NV_SATFINITE, __NV_E4M3));
