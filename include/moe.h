@@ -776,6 +776,14 @@ moe_status moe_ep_result_map(const int32_t* route_msg, const int32_t* route_pos,
  * is involved.
  * ------------------------------------------------------------------------- */
 moe_status moe_selftest_bounded_wait(int32_t* dev_status, moe_stream_t stream);
+/* moe_selftest_fp4_wait -- the same of the 4-bit products' one launch: on scratch
+ * (device, moe_selftest_fp4_scratch_size() bytes, 16-byte aligned) one block computes
+ * gate/up tiles and then waits for a count of theirs that never fills.  It gives up
+ * after the wait limit, sets MOE_DEV_TIMEOUT in dev_status[0] (int32[2], zeroed by
+ * the caller), drains its copies and tensor-core work and returns normally. */
+size_t moe_selftest_fp4_scratch_size(void);
+moe_status moe_selftest_fp4_wait(void* scratch, size_t scratch_bytes, int32_t* dev_status,
+                                 moe_stream_t stream);
 
 #ifdef __cplusplus
 }

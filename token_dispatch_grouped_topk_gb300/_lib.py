@@ -19,6 +19,8 @@ c_int64, c_float = ctypes.c_int64, ctypes.c_float
 SIGNATURES = {
     "moe_abi_version": (c_int, []),
     "moe_selftest_bounded_wait": (c_int, [c_void_p, c_void_p]),
+    "moe_selftest_fp4_scratch_size": (c_size_t, []),
+    "moe_selftest_fp4_wait": (c_int, [c_void_p, c_size_t, c_void_p, c_void_p]),
     "moe_status_string": (c_char_p, [c_int]),
     "moe_dispatch_workspace_size": (c_size_t, [c_int, c_int, c_int]),
     "moe_dispatch": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int,
