@@ -564,6 +564,10 @@ moe_status moe_experts_w4(const void* x, const void* topk_idx, int idx_bits, con
  *   MOE_FP4_NVFP4  blocks of 16, scales in e4m3, and an fp32 scale g over the
  *                  tensor (over an expert, for weights); a NULL g is 1.
  *                  s = e4m3(amax / (6 g)), code = e2m1(x * (1 / (s g)))
+ *                  g = (largest magnitude of the tensor) / (6 * 448) uses e4m3's
+ *                  whole range.  With g = 1 a block whose amax is below 6 * 2^-6 =
+ *                  0.094 gets a subnormal scale, off by up to 2^-10: a seventh of
+ *                  the scale of weights around 0.02.  Weights want their g.
  *   MOE_FP4_MXFP4  blocks of 32, scales in e8m0 (2^(byte - 127)), no g (NULL).
  *                  s = 2^(floor(log2 amax) - 2), code = e2m1(x / s)
  * in fp32, each step rounded to nearest; codes to nearest, ties to the even

@@ -628,8 +628,10 @@ def moe_quantize_fp4(x, *, format: str = "nvfp4", gscale=None, xq=None, xs=None,
     """Rows ``x [..., H]`` bf16 or fp32 to microscaled 4 bits (moe_quantize_fp4):
     ``"nvfp4"`` (blocks of 16, e4m3 scales, ``gscale`` fp32 over the tensor:
     ``[1]``, or ``[E]`` for ``x [E, N, H]``; None is 1) or ``"mxfp4"`` (blocks of
-    32, power-of-two scales, no ``gscale``).  Returns ``(xq [..., H/2], xs [...,
-    H/16 or H/32])`` uint8."""
+    32, power-of-two scales, no ``gscale``).  Weights want their own ``gscale``,
+    the largest magnitude / 2688: under 1 the scales of blocks that stay below
+    0.094 are e4m3's subnormals.  Returns ``(xq [..., H/2], xs [..., H/16 or
+    H/32])`` uint8."""
     fmt, block = _fp4(format)
     shape = tuple(x.shape)
     lead, H = shape[:-1], shape[-1]
@@ -1135,8 +1137,9 @@ class MoeLayerBuffers:
                          rows=self.rows if self.packed else 0)
 
     def gemms(self, w13, w13_scale, w2, w2_scale, stream=None, max_ctas=0):
-        """Both GEMMs on the FP8 (4-bit) activations dispatch_quant wrote, in the
-        library's launch form for the layer (or ``gemm_launch``)."""
+        """Both GEMMs on the FP8 activations dispatch_quant wrote, in the
+        library's launch form for the layer (or ``gemm_launch``); on a 4-bit lane
+        the two products one after the other, whatever ``gemm_launch`` says."""
         if self.fp4:
             xq, xs, zq, zs = self.fp4_rows
             gx, g13, gz, g2 = self.fp4_gscales

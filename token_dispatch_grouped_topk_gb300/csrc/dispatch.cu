@@ -600,9 +600,11 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
 // before the block finds its routes' slots; with few blocks, blockIdx.z shares a
 // block's rows among several (1009 tokens of 1408, six routes each: 12.9 -> 8.3 us).
 // Measured with the counting launches: 16384 tokens of 7168 to eight of 256 experts
-// 158 us (763 MB, 4.8 TB/s), 4096 of 4096 to 128 skewed ones 32; one launch, 256 tokens
-// of 4096 to 64: 9 us.  Bound by the stores of many rows, by latency with few.  A lane takes 16 values (two
-// 16-byte loads, 8 bytes of codes), a warp 512 at a time, 1, 2 or 4 times a token.
+// with room for 768 rows 157 us (122380 rows kept, 728 MB: 4.6 TB/s), 4096 of 4096 to
+// 128 skewed ones 32; one launch, 256 tokens of 4096 to 64: 8 us.  Bound by latency:
+// with many rows by that of the loads, at 24 warps an SM (80 registers): DRAM 58 % busy,
+// L2 33 %, most stalls on loads.  A lane takes 16 values (two 16-byte loads, 8 bytes of
+// codes), a warp 512 at a time, 1, 2 or 4 times a token.
 template <typename IdT, int kFmt, bool kSingle>
 __global__ void __launch_bounds__(kDispatchWarps * 32)
     route_scatter_fp4_kernel(const uint4* __restrict__ x, const float* xg,

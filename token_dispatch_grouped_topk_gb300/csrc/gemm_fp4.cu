@@ -4,7 +4,11 @@
 //   P[m, n] = ga * gw[e] * sum_k (sa[m, k/B] a[m, k]) * (sw[n, k/B] w[e, n, k])
 // with e2m1 codes a, w, the block scales of the format (fp4.cuh) and the fp32
 // scales over the tensors:
-//   down     out = bf16(P), any contraction K and output width N;
+//   down     out = bf16(P), any contraction K and output width N.  The rows are
+//     BF16 between this product and the combine, as on the FP8 path: out is the
+//     caller's buffer, and fp32 rows would double what both move of it (the
+//     combine is bound by that).  It is a rounding of at most 2^-8 more than y's
+//     own: 2.3e-3 instead of 1.7e-3 of a layer's outputs against 64 bits;
 //   gate/up  Z = SiLU(G) * U with G and U the products with the first and the
 //            last I rows of W13, fp32, requantised to 4 bits per block
 //            ("SGLang Expert Compute Backend", §1.1 and §3.6, on other codes).
@@ -44,11 +48,15 @@
 //
 // What bounds it.  Many rows: what an SM can take in, 64 bytes a clock: 48 KB of
 // codes and 6 KB of scales a stage are 850 clocks, the four MMAs 512 and the
-// twelve copies about 120.  16384 tokens (above): gate/up 1498 us, 4.8 PFLOP/s, down
-// 969 us, 3.7; without the scale loads 8 to 15 % less, without code loads 1210 and
-// 720.  Few rows: weights, 256 tokens to 64 experts of 4096 x 1536 (both products)
-// 111 us, 6.3 TB/s of DRAM.  One token, 8 experts of 7168 x 2048: 47 us for 29 of
-// weights; the rest is two products' first loads and last tiles.
+// twelve copies about 120.  Counted on 16 full experts of 768 rows, gate/up takes
+// in 55 bytes a clock over the whole launch (tensor pipe 51 %); down 42 (39 %),
+// whose tiles are eight stages long, so that draining the accumulator and storing
+// 64 KB of BF16 a tile weigh as well.  16384 tokens (above, 122380 rows kept):
+// gate/up 1511 us, 4.8 PFLOP/s, down 968 us, 3.7; without the scale loads 8 to 15 %
+// less, without code loads 1210 and 720.  Few rows: weights, 256 tokens to 64
+// experts of 4096 x 1536 (both products) 112 us, 6.2 TB/s of DRAM.  One token, 8
+// experts of 7168 x 2048: 46 us for 29 of weights; the rest is two products' first
+// loads and last tiles.
 // Every wait is bounded; on expiry the kernel raises MOE_DEV_TIMEOUT in the
 // status word, drains its own copies and MMAs, frees TMEM and returns.
 #include <algorithm>

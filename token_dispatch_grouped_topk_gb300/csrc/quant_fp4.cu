@@ -133,8 +133,9 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Blocks for so many threads, up to 64 an SM one after the other (235 M weights:
-// 168 and 111 us there and back, 177 and 128 with eight resident ones that go on).
+// Blocks for so many threads, up to 64 an SM one after the other (235 M weights
+// between two events, which add the launch: 168 and 111 us there and back, 177 and
+// 128 with eight resident ones that go on).
 int blocks_for(long long threads, int sm_count) {
   return static_cast<int>(std::min<long long>((threads + kThreads - 1) / kThreads, 64LL * sm_count));
 }
